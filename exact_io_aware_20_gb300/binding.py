@@ -16,7 +16,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libfa_gb300.so")
 
 FA_F16, FA_BF16 = 0, 1
-FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT, FA_ERR_WORKSPACE = range(6)
+(FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT, FA_ERR_WORKSPACE,
+ FA_ERR_CACHE) = range(7)
 
 # Symbols include/fa.h declares, with their ctypes signatures.
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
@@ -43,6 +44,12 @@ SIGNATURES = {
     "fa_fwd_strided": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _i, _vp, _vp]),
     "fa_bwd_strided": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
                             _f, _i, _vp, _i, _vp, _sz, _vp]),
+    "fa_rope": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _i, _i, _vp, _vp]),
+    "fa_cache_append": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp,
+                             _vp]),
+    "fa_fwd_cache": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp, _vp, _vp, _vp, _sz,
+                          _vp]),
+    "fa_fwd_cache_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "fa_get_device_status": (_i, [_vp]),
     "fa_strerror": (ctypes.c_char_p, [_i]),
     "fa_selftest_expired_wait": (_i, [_i, _vp]),
@@ -370,3 +377,270 @@ def backward_blocksparse(q, k, v, o, lse, dout, block_mask, causal: bool, scale:
                                      workspace.numel() * workspace.element_size(),
                                      _stream_ptr(stream)), "fa_bwd_blocksparse")
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------- rotary positions, 8-bit cache
+ROPE_MAX_PAIRS, ROPE_MAX_AXES = 128, 4
+
+
+class _FaRopeSpec(ctypes.Structure):
+    """struct fa_rope_spec"""
+    _fields_ = [("axes", ctypes.c_int), ("pairs", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("freq", ctypes.c_double * ROPE_MAX_PAIRS),
+                ("axis", ctypes.c_ubyte * ROPE_MAX_PAIRS)]
+
+
+class _FaCache(ctypes.Structure):
+    """struct fa_cache"""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("block_table", _vp),
+                ("pages", _i), ("page_size", _i), ("table_width", _i), ("Hkv", _i), ("d", _i),
+                ("k_strides", FaStrides), ("v_strides", FaStrides)]
+
+
+class Rope:
+    """The angles of a rotation (struct fa_rope_spec): pair p turns by freq[p]
+    radians per position of axis axis[p] (all on one axis unless given).
+    freq: a sequence of numbers or a tensor, read once, here."""
+
+    def __init__(self, freq, axis=None, interleaved: bool = False):
+        freq = [float(f) for f in freq]
+        axis = [0] * len(freq) if axis is None else [int(a) for a in axis]
+        if not 1 <= len(freq) <= ROPE_MAX_PAIRS or len(axis) != len(freq):
+            raise ValueError(f"expected 1 to {ROPE_MAX_PAIRS} frequencies and an axis for each")
+        if min(axis) < 0 or max(axis) >= ROPE_MAX_AXES:
+            raise ValueError(f"axes are numbered 0 to {ROPE_MAX_AXES - 1}")
+        self.axes, self.pairs = max(axis) + 1, len(freq)
+        self.spec = _FaRopeSpec(axes=self.axes, pairs=self.pairs, interleaved=int(bool(interleaved)))
+        self.spec.freq[:self.pairs] = freq
+        self.spec.axis[:self.pairs] = axis
+        self._ref = ctypes.addressof(self.spec)
+
+
+class Cache:
+    """A paged 8-bit key/value cache (struct fa_cache): k, v
+    [pages, Hkv, page_size, d] of torch.float8_e4m3fn (or their bytes as
+    uint8; any view with d contiguous), k_scale, v_scale fp32 [pages, Hkv],
+    block_table int32 [B, table_width].  The tensors are the caller's; the
+    object keeps them alive and holds their addresses."""
+
+    def __init__(self, k, v, k_scale, v_scale, block_table):
+        if k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("expected k and v [pages, Hkv, page_size, d]")
+        pages, Hkv, page, d = k.shape
+        for t in (k, v):
+            if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+                raise TypeError("the cache's k and v are float8_e4m3fn (or uint8 codes)")
+            if t.stride(3) != 1:
+                raise ValueError("the last (d) dimension must be contiguous")
+        for t in (k_scale, v_scale):
+            if t.dtype != torch.float32 or tuple(t.shape) != (pages, Hkv) or not t.is_contiguous():
+                raise ValueError(f"scales must be contiguous fp32 [{pages}, {Hkv}]")
+        if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous():
+            raise ValueError("block_table must be contiguous int32 [B, table_width]")
+        self.tensors = (k, v, k_scale, v_scale, block_table)
+        if any(not t.is_cuda or t.device != k.device for t in self.tensors):
+            raise ValueError("the cache's tensors must be on one CUDA device")
+        self.pages, self.Hkv, self.page_size, self.d = pages, Hkv, page, d
+        self.B, self.table_width = block_table.shape
+        self.device = k.device
+        self.struct = _FaCache(*(t.data_ptr() for t in self.tensors), pages, page, self.table_width,
+                               Hkv, d, _view_strides(k), _view_strides(v))
+        self._ref = ctypes.addressof(self.struct)
+
+
+def _view_strides(t):
+    """FaStrides of a [.., .., .., d] view; a dimension of one element has no
+    stride of its own and takes the contiguous one."""
+    s = t.stride()
+    n = t.shape
+    row = s[2] if n[2] > 1 else n[3]
+    head = s[1] if n[1] > 1 else n[2] * n[3]
+    batch = s[0] if n[0] > 1 else n[1] * n[2] * n[3]
+    return FaStrides(batch, head, row)
+
+
+_NO_STRIDES = FaStrides(0, 0, 0)
+
+
+def _view(t, like, heads, what):
+    """FaStrides of a [B, heads, N, d] view on like's device and of its dtype."""
+    if t is None:
+        return _NO_STRIDES
+    if (t.dim() != 4 or t.shape[0] != like.shape[0] or t.shape[1] != heads
+            or t.shape[2:] != like.shape[2:]):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected "
+                         f"{(like.shape[0], heads) + tuple(like.shape[2:])}")
+    if t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{what} must have the dtype and device of the other tensors")
+    if t.stride(3) != 1:
+        raise ValueError("the last (d) dimension must be contiguous")
+    return _view_strides(t)
+
+
+def _ints(t, shape, device, what):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{what} must be contiguous int32 {list(shape)} on the inputs' device")
+    return t.data_ptr()
+
+
+class _On:
+    """The device and the stream of a call: makes the tensors' device current
+    where another one is, and takes that device's current stream unless one is
+    given.  On a given stream everything a call allocates comes from that
+    stream's memory, so that it is not handed out again before the call's work
+    is done; its outputs are marked as used on the caller's stream too."""
+
+    def __init__(self, device, stream):
+        if device.type != "cuda":
+            raise ValueError("expected CUDA tensors")
+        self.guard = None
+        self.caller = None
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError("the stream belongs to another device than the tensors")
+            current = torch.cuda.current_stream(device)
+            if stream != current:
+                self.guard, self.caller = torch.cuda.stream(stream), current
+        if self.guard is None and device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+        self.stream = torch.cuda.current_stream(device) if stream is None else stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        self.ptr = self.stream.cuda_stream or None
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def made(self, t):
+        if self.caller is not None:
+            t.record_stream(self.caller)
+        return t
+
+
+def _positions(positions, rope_spec, B, N, device):
+    """(address, pos_batch) of positions [axes, B or 1, N] ([B or 1, N] on one axis)."""
+    if positions is None:
+        return None, 1
+    shape = tuple(positions.shape)
+    if len(shape) == 2 and rope_spec is not None and rope_spec.axes == 1:
+        shape = (1,) + shape
+    axes = 1 if rope_spec is None else rope_spec.axes
+    if (positions.dtype != torch.int32 or len(shape) != 3 or shape[0] != axes or shape[1] not in (1, B)
+            or shape[2] != N or not positions.is_contiguous() or positions.device != device):
+        raise ValueError(f"positions must be contiguous int32 [{axes}, {B} or 1, {N}] on the "
+                         "inputs' device")
+    return positions.data_ptr(), shape[1]
+
+
+def _rope(q, k, positions, table, inverse, q_out, k_out, stream):
+    if q.dim() != 4:
+        raise ValueError("expected q [B, H, N, d]")
+    B, H, N, d = q.shape
+    Hkv = 0 if k is None else k.shape[1]
+    code = _dtype_code(q)
+    with _On(q.device, stream) as on:
+        st = (FaStrides * 4)()
+        st[0] = _view(q, q, H, "q")
+        st[1] = _view(k, q, Hkv, "k")
+        q_out = on.made(torch.empty_like(q)) if q_out is None else q_out
+        if k is not None and k_out is None:
+            k_out = on.made(torch.empty_like(k))
+        st[2] = _view(q_out, q, H, "q_out")
+        st[3] = _view(k_out, q, Hkv, "k_out")
+        pos, pos_batch = _positions(positions, table, B, N, q.device)
+        _check(load().fa_rope(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), B, H, Hkv, N, d,
+                              code, table._ref, pos, pos_batch, inverse, st, on.ptr), "fa_rope")
+    return q_out, k_out
+
+
+def rope(q, k, positions, table: Rope, q_out=None, k_out=None, stream=None):
+    """(q_out, k_out): q [B, H, N, d] and k [B, Hkv, N, d] (or None) rotated by
+    `table` (fa_rope).  positions int32 [axes, B or 1, N] ([B or 1, N] on one
+    axis), None: 0 .. N - 1.  Any views with d contiguous; outputs are
+    allocated like the inputs unless given, and may be the inputs."""
+    return _rope(q, k, positions, table, 0, q_out, k_out, stream)
+
+
+def rope_backward(dq_out, dk_out, positions, table: Rope, dq=None, dk=None, stream=None):
+    """(dq, dk) of `rope` from the gradients of its outputs."""
+    return _rope(dq_out, dk_out, positions, table, 1, dq, dk, stream)
+
+
+def cache_append(cache: Cache, q, k, v, seq_lens, new_lens=None, rope: Rope | None = None,
+                 positions=None, q_out=None, stream=None):
+    """Append the tokens k, v [B, Hkv, N, d] to the cache, keys rotated by
+    `rope`, and return q [B, H, N, d] rotated (None for q None)
+    (fa_cache_append).  seq_lens int32 [B]: lengths counting the new tokens;
+    new_lens int32 [B]: how many of the N rows are tokens (None: all);
+    positions as in `rope`, None: the tokens' numbers."""
+    if k.dim() != 4:
+        raise ValueError("expected k [B, Hkv, N, d]")
+    B, Hkv, N, d = k.shape
+    if Hkv != cache.Hkv or d != cache.d or B != cache.B or k.device != cache.device:
+        raise ValueError(f"k{tuple(k.shape)} does not belong to a cache of {cache.B} sequences, "
+                         f"{cache.Hkv} heads, d {cache.d} on {cache.device}")
+    code = _dtype_code(k)
+    H = 0 if q is None else q.shape[1]
+    with _On(k.device, stream) as on:
+        st = (FaStrides * 4)()
+        st[0] = _view(q, k, H, "q")
+        st[1] = _view(k, k, Hkv, "k")
+        st[2] = _view(v, k, Hkv, "v")
+        if q is None:
+            q_out = None
+        elif q_out is None:
+            q_out = on.made(torch.empty_like(q))
+        st[3] = _view(q_out, k, H, "q_out")
+        pos, pos_batch = _positions(positions, rope, B, N, k.device)
+        _check(load().fa_cache_append(
+            cache._ref, _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out), B, H, N, code,
+            _ints(seq_lens, (B,), k.device, "seq_lens"), _ints(new_lens, (B,), k.device, "new_lens"),
+            None if rope is None else rope._ref, pos, pos_batch, st, on.ptr), "fa_cache_append")
+    return q_out
+
+
+def forward_cache(q, cache: Cache, seq_lens, causal: bool, scale: float, new_lens=None, out=None,
+                  lse=None, workspace=None, stream=None):
+    """(o, lse) of q [B, H, Nq, d] against the first seq_lens[b] tokens of the
+    cache (fa_fwd_cache).  causal: the new_lens[b] query rows (None: all Nq)
+    are the sequence's last tokens."""
+    if q.dim() != 4:
+        raise ValueError("expected q [B, H, Nq, d]")
+    B, H, Nq, d = q.shape
+    if d != cache.d or B != cache.B or q.device != cache.device or H % cache.Hkv:
+        raise ValueError(f"q{tuple(q.shape)} does not fit a cache of {cache.B} sequences, "
+                         f"{cache.Hkv} heads, d {cache.d} on {cache.device}")
+    code = _dtype_code(q)
+    lib = load()
+    with _On(q.device, stream) as on:
+        st = (FaStrides * 2)()
+        st[0] = _view(q, q, H, "q")
+        out = on.made(torch.empty_like(q)) if out is None else out
+        st[1] = _view(out, q, H, "out")
+        if lse is None:
+            lse = on.made(torch.empty((B, H, Nq), dtype=torch.float32, device=q.device))
+        elif lse.dtype != torch.float32 or tuple(lse.shape) != (B, H, Nq) or \
+                not lse.is_contiguous() or lse.device != q.device:
+            raise ValueError(f"lse must be contiguous fp32 [{B}, {H}, {Nq}] on the inputs' device")
+        if workspace is None:
+            need = int(lib.fa_fwd_cache_workspace_size(B, H, cache.Hkv, Nq, d))
+            workspace = on.made(torch.empty(max(need, 256), dtype=torch.uint8, device=q.device))
+        elif workspace.device != q.device:
+            raise ValueError("the workspace must be on the inputs' device")
+        _check(lib.fa_fwd_cache(
+            q.data_ptr(), cache._ref, out.data_ptr(), lse.data_ptr(), B, H, Nq, int(causal),
+            float(scale), code, _ints(seq_lens, (B,), q.device, "seq_lens"),
+            _ints(new_lens, (B,), q.device, "new_lens"), st, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), on.ptr), "fa_fwd_cache")
+    return out, lse
+
+
+def fwd_cache_workspace_size(B, H, Hkv, Nq, d) -> int:
+    """Bytes of workspace forward_cache needs on the current device."""
+    return int(load().fa_fwd_cache_workspace_size(B, H, Hkv, Nq, d))

@@ -24,11 +24,15 @@ namespace {
 
 thread_local char g_cuda_msg[256] = "no CUDA error recorded";
 
+}  // namespace
+
 int cuda_fail(cudaError_t e, const char* where) {
   std::snprintf(g_cuda_msg, sizeof(g_cuda_msg), "%s: %s (%s)", where, cudaGetErrorName(e),
                 cudaGetErrorString(e));
   return FA_ERR_CUDA;
 }
+
+namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
@@ -49,6 +53,8 @@ int g_dev_ok[64];   // 0 = unknown, 1 = yes, 2 = no
 std::mutex g_dev_mu;
 
 unsigned int* g_err_ptr[64];
+
+}  // namespace
 
 // Checks that the current device is an sm_103 part and returns the device
 // address of its error word in *err (both cached per device).
@@ -77,6 +83,8 @@ int check_device(unsigned int** err) {
   *err = g_err_ptr[dev];
   return FA_OK;
 }
+
+namespace {
 
 bool aligned(const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
 
@@ -119,7 +127,7 @@ namespace {
 // robin; the map itself holds only the address and the geometry, so an entry
 // is valid on any device.
 struct TmapKey {
-  int kind;                      // 0: 16-bit 4-D view, 1: fp32 3-D array
+  int kind;                      // 0: 16-bit 4-D view, 1: fp32 3-D array, 2: 8-bit 4-D view
   const void* base;
   long long dims[4], strides[3];
   int box[2];
@@ -185,6 +193,38 @@ cudaError_t make_tmap_4d(CUtensorMap* map, const void* base, int cols, int rows,
                         strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
+  tmap_store(key, *map);
+  return cudaSuccess;
+}
+
+cudaError_t make_tmap_u8_4d(CUtensorMap* map, const void* base, int cols, int rows, int heads,
+                            int pages, const Strides& st, int box_cols, int box_rows) {
+  TmapKey key{};
+  key.kind = 2;
+  key.base = base;
+  key.dims[0] = cols;
+  key.dims[1] = rows;
+  key.dims[2] = heads;
+  key.dims[3] = pages;
+  key.strides[0] = st.n;
+  key.strides[1] = st.h;
+  key.strides[2] = st.b;
+  key.box[0] = box_cols;
+  key.box[1] = box_rows;
+  if (tmap_lookup(key, map)) return cudaSuccess;
+  std::call_once(g_encode_once, load_encoder);
+  if (g_encode_err != cudaSuccess) return g_encode_err;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                        static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(pages)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(st.n), static_cast<cuuint64_t>(st.h),
+                           static_cast<cuuint64_t>(st.b)};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1, 1};
+  cuuint32_t estride[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims,
+                        strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        box_cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return cudaErrorInvalidValue;
   tmap_store(key, *map);
   return cudaSuccess;
@@ -363,6 +403,8 @@ size_t splitkv_bytes(int B, int H, int Nq, int d, int splits) {
   return o + l;
 }
 
+}  // namespace
+
 // Strides of a caller's view: each a positive multiple of 8 elements (16
 // bytes, the tensor-map stride unit) below 2^39 elements.
 bool valid_strides(const fa_strides* s, int n, Strides* out) {
@@ -375,6 +417,8 @@ bool valid_strides(const fa_strides* s, int n, Strides* out) {
   }
   return true;
 }
+
+namespace {
 
 // st: element strides of q, k, v, o (nullptr: contiguous).
 int fwd_common(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H,
@@ -653,6 +697,7 @@ extern "C" int fa_get_device_status(fa_stream_t stream) {
     e = cudaMemcpyToSymbol(fa::g_device_error, &zero, sizeof(zero));
     if (e != cudaSuccess) return fa::cuda_fail(e, "clear device error word");
     if (word & fa::kErrTimeout) return FA_ERR_TIMEOUT;
+    if (word & fa::kErrCache) return FA_ERR_CACHE;
     std::snprintf(fa::g_cuda_msg, sizeof(fa::g_cuda_msg),
                   "a kernel found its dynamic shared memory base misaligned (error word %#x)",
                   word);
@@ -668,7 +713,8 @@ extern "C" const char* fa_strerror(int status) {
     case FA_ERR_UNSUPPORTED: return "unsupported head dim, dtype or device (needs sm_103)";
     case FA_ERR_CUDA: return fa::g_cuda_msg;
     case FA_ERR_TIMEOUT: return "a bounded device-side wait expired";
-    case FA_ERR_WORKSPACE: return "backward workspace missing, misaligned or too small";
+    case FA_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
+    case FA_ERR_CACHE: return "a page table entry or a sequence length of the cache was out of range";
     default: return "unknown status";
   }
 }

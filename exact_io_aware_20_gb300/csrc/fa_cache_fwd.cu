@@ -1,0 +1,937 @@
+// Attention over the paged 8-bit cache (fa_fwd_cache).
+//
+// Scores and weights.  For a page with scales ks and vs and codes K8, V8,
+//     s = scale * ks * (q . K8),    O = sum_j p_j vs V8_j / sum_j p_j.
+// e4m3 codes widen to f16 exactly, so both products run on f16 operands with
+// fp32 sums: q as f16 (a bf16 row is first divided by the power of two of its
+// largest element, which loses nothing that the product could show), and the
+// weights as f16 with the value scale taken into the exponent,
+//     p'_j = 2^(s_j log2 e + log2 vs - m),  m = max_j (s_j log2 e + log2 vs),
+// so that they lie in [0, 1] whatever the pages' scales are; the row sum adds
+// p'_j / vs in fp32.  The running maximum is moved only when it grows by more
+// than 8 (p' then stays below 2^8, well inside f16), so that most tiles need
+// one vote and no reduction.
+//
+// Work.  What bounds it for few query rows is the cache's bytes: the G query
+// heads of a key/value head, times the query tokens, form the rows of one
+// unit, so a page is read once for all of them.  Sequences have unlike
+// lengths that only the device knows: the steps (of 4 warps x kTile keys) of
+// all units, laid end to end, are cut into equal shares, one for each
+// resident CTA, so every CTA streams the same number of bytes.  A unit that
+// lies in several shares leaves normalisation to the merge kernel: each piece
+// writes its maximum, sum and unnormalised O, at most two pieces a CTA.
+//
+// A warp has its own ring of kStages tiles (kTile keys of K and V, 8 KB) in
+// shared memory, filled by TMA through the page table, and its own running
+// maximum, sum and O; the four warps of a CTA meet only where a unit ends.
+// With S^T = K Q^T and O^T = V^T P^T the cache is the A operand (16 keys or 16
+// columns a fragment), so 8 query rows fill an MMA: a step of mma.sync
+// m16n8k16 costs nothing that shows beside the loads.
+#include <algorithm>
+#include <atomic>
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "cache_seq.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStages = 3;
+constexpr float kNoMax = -1e30f;    // running maximum before the first key
+constexpr float kGrow = 8.f;        // the maximum moves when it grows by more (log2 units)
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int D>
+struct Tile {
+  static constexpr int kKeys = 4096 / D;                 // keys of a warp's tile
+  static constexpr int kStep = kWarps * kKeys;           // keys of a CTA's step
+  static constexpr int kBytes = 4096;                    // of K, and of V
+  static constexpr int kPitch = D < 128 ? D : 128;       // bytes of a row in shared memory
+  static constexpr int kHalves = D / kPitch;             // 128-column parts, one after another
+  static constexpr int kSub = kKeys / 16;                // pages that a tile can touch
+};
+
+struct FwdCacheParams {
+  SeqParams seq;
+  const uint16_t* q;
+  uint16_t* o;
+  float* lse;
+  Strides qs, os;
+  const float *k_scale, *v_scale;
+  const int* table;
+  int width, pages, page_log2;
+  int H, Hkv, rows;       // rows = G * Nq of a unit's key/value head
+  int row_tiles;
+  int bf16;
+  float scale_log2;
+  float* part_o;          // [CTA][2][row tile][D]
+  float2* part_ml;        // [CTA][2][row tile]
+  int ctas;
+};
+
+__device__ __forceinline__ uint32_t widen(uint32_t two) {   // two e4m3 codes -> f16x2
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+}
+
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Bytes that are NaN codes (0x7f, 0xff), as a byte mask.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+}
+
+// The key of a 16-key fragment that row g (of 8) of the fragment's halves
+// stands for.  Chosen so that neither the K loads (8 lanes read rows g, g + 1)
+// nor the V loads (8 lanes read the four even or odd rows) meet a bank twice
+// under TMA's swizzle of the tile.
+template <int D>
+__device__ __forceinline__ int key_of(int g) {
+  if constexpr (D == 64) return (g & 4) | ((g & 1) << 1) | (((g >> 1) ^ g) & 1);
+  else return g ^ ((g & 1) << 2);
+}
+
+// Byte offset of 16-byte chunk c of row r in a tile part.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  if constexpr (D == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  else return r * 128 + ((c ^ (r & 7)) << 4);
+}
+
+// Steps of a tile of rows.
+template <int D>
+__device__ __forceinline__ int steps_of(int lim) {
+  return (lim + Tile<D>::kStep - 1) / Tile<D>::kStep;
+}
+
+// Limits of entry e = b * row_tiles + row tile.
+template <int NT>
+__device__ __forceinline__ TileLimits limits_of(const FwdCacheParams& p, int e, Sequence* s,
+                                                bool* bad) {
+  const int b = e / p.row_tiles, rt = e % p.row_tiles;
+  *s = sequence_at(p.seq, b, bad);
+  return tile_limits(p.seq, *s, rt * 8 * NT, min(p.rows, (rt + 1) * 8 * NT));
+}
+
+// Sum over the block's threads (every thread gets it); red: kWarps values.
+__device__ __forceinline__ long long block_sum(long long x, long long* red) {
+  #pragma unroll
+  for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = 0;
+  #pragma unroll
+  for (int i = 0; i < kWarps; ++i) x += red[i];
+  return x;
+}
+
+// All steps of the call, the key/value heads of an entry counted together.
+template <int D, int NT>
+__device__ long long total_steps(const FwdCacheParams& p, long long* red, bool* bad) {
+  long long mine = 0;
+  const int entries = p.seq.B * p.row_tiles;
+  for (int e = threadIdx.x; e < entries; e += kThreads) {
+    Sequence s;
+    mine += steps_of<D>(limits_of<NT>(p, e, &s, bad).lim);
+  }
+  return block_sum(mine, red);
+}
+
+// The entry in which step `at` (of all entries, one head) lies: found->x the
+// entry, found->y the steps before it.
+template <int D, int NT>
+__device__ void find_entry(const FwdCacheParams& p, long long at, long long* red,
+                           longlong2* found) {
+  const int entries = p.seq.B * p.row_tiles, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long before = 0;
+  for (int e0 = 0; e0 < entries; e0 += kThreads) {
+    const int e = e0 + threadIdx.x;
+    Sequence s;
+    bool bad = false;
+    const long long mine = e < entries ? steps_of<D>(limits_of<NT>(p, e, &s, &bad).lim) : 0;
+    long long upto = mine;
+    #pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, upto, m);
+      if (lane >= m) upto += x;
+    }
+    __syncthreads();
+    if (lane == 31) red[warp] = upto;
+    __syncthreads();
+    long long all = 0;
+    #pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) upto += red[i];
+      all += red[i];
+    }
+    if (mine > 0 && before + upto - mine <= at && at < before + upto) {
+      found->x = e;
+      found->y = before + upto - mine;
+    }
+    before += all;
+    if (at < before) break;
+  }
+  __syncthreads();
+}
+
+// Where a walk over the steps of a share stands.
+template <int D, int NT>
+struct Walk {
+  int e, h, step, steps;   // entry, key/value head, step and steps of the unit
+  int lim, full;
+  Sequence seq;
+  __device__ __forceinline__ void enter(const FwdCacheParams& p) {
+    bool bad = false;
+    const TileLimits t = limits_of<NT>(p, e, &seq, &bad);
+    lim = t.lim;
+    full = t.full;
+    steps = steps_of<D>(lim);
+  }
+  __device__ __forceinline__ void next_unit(const FwdCacheParams& p) {
+    step = 0;
+    if (++h == p.Hkv) {
+      h = 0;
+      const int entries = p.seq.B * p.row_tiles;
+      do {
+        if (++e >= entries) { steps = lim = full = 0; return; }
+        enter(p);
+      } while (steps == 0);
+    }
+  }
+};
+
+template <int D, int NT>
+struct Smem {
+  using T = Tile<D>;
+  static constexpr int kRing = kWarps * kStages * 2 * T::kBytes;
+  static constexpr int kQOff = kRing;
+  static constexpr int kQBytes = D * NT * 16;              // q fragments, f16
+  static constexpr int kBufOff = kQOff + kQBytes;          // O of two warps while they are joined
+  static constexpr int kBufBytes = 2 * 8 * NT * D * 4;
+  static constexpr int kStatOff = kBufOff + kBufBytes;     // (maximum, sum) [warp][row]
+  static constexpr int kStatBytes = kWarps * 8 * NT * 8;
+  static constexpr int kQsOff = kStatOff + kStatBytes;     // [row] power of two taken off q
+  static constexpr int kMetaOff = kQsOff + 8 * NT * 4;     // (ks, log2 vs) [warp][stage][page]
+  static constexpr int kMetaBytes = kWarps * kStages * T::kSub * 8;
+  static constexpr int kBarOff = kMetaOff + kMetaBytes;
+  static constexpr int kMiscOff = kBarOff + kWarps * kStages * 8;
+  static constexpr int kAlloc = kMiscOff + 64 + 1024;      // slack to align the base
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads)
+cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                 const __grid_constant__ FwdCacheParams p) {
+  using T = Tile<D>;
+  using S = Smem<D, NT>;
+  constexpr int kMT = D / 16;                  // 16-column fragments of O^T
+  constexpr int kChunks = D / 64;              // 64-column parts of a row
+  constexpr bool kQRegs = kChunks * 8 * NT <= 32;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  long long* red = reinterpret_cast<long long*>(smem + S::kBufOff);
+  longlong2* found = reinterpret_cast<longlong2*>(smem + S::kBufOff + 64);
+  volatile int* abort = reinterpret_cast<volatile int*>(smem + S::kMiscOff);
+  uint2* q_frag = reinterpret_cast<uint2*>(smem + S::kQOff);
+  float2* stat = reinterpret_cast<float2*>(smem + S::kStatOff);
+  float* q_pow = reinterpret_cast<float*>(smem + S::kQsOff);
+  float2* meta = reinterpret_cast<float2*>(smem + S::kMetaOff) + warp * kStages * T::kSub;
+  const uint32_t ring = base + warp * kStages * 2 * T::kBytes;
+  const uint32_t bars = base + S::kBarOff + warp * kStages * 8;
+
+  grid_launch_dependents();   // the merge may be set up; it waits for this grid's end
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kWarps * kStages; ++i) mbar_init(base + S::kBarOff + 8 * i, 1);
+    *abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  bool bad = false;
+  const long long total = total_steps<D, NT>(p, red, &bad) * p.Hkv;
+  if (bad && blockIdx.x == 0) atomicOr(p.seq.err, kErrCache);
+  const long long share = (total + p.ctas - 1) / p.ctas;
+  const long long lo = blockIdx.x * share, hi = min(total, lo + share);
+  if (lo >= hi) return;
+  find_entry<D, NT>(p, lo / p.Hkv, red, found);
+  // found holds the entry by its steps of one head: entry e's Hkv units stand
+  // one after another from step found->y * Hkv on
+  Walk<D, NT> at;
+  at.e = static_cast<int>(found->x);
+  {
+    at.enter(p);
+    const long long rest = lo - found->y * p.Hkv;
+    at.h = static_cast<int>(rest / at.steps);
+    at.step = static_cast<int>(rest % at.steps);
+  }
+  __syncthreads();   // found is read; its place is the join buffer's
+
+  // ---------------------------------------------------------------- loads
+  const int sub_log2 = min(p.page_log2, 31 - __clz(T::kKeys));   // keys of a box
+  const int subs = T::kKeys >> sub_log2;                         // boxes (pages) of a tile
+  const uint32_t box_bytes = static_cast<uint32_t>(T::kPitch) << sub_log2;
+  Walk<D, NT> f = at;
+  long long f_left = hi - lo;
+  int fetched = 0, done = 0;
+  int tb_first = 0, tb_steps = 0;      // steps of f's unit that the table registers cover
+  int tb_page = 0;
+  float tb_ks = 1.f, tb_vs = 1.f;
+  bool dead = false;                   // a wait gave up: no further loads
+  // Issue the warp's next tile, if it has one left in the share.
+  auto fetch = [&]() {
+    while (f_left > 0 && !dead) {
+      const int k0 = (f.step * kWarps + warp) * T::kKeys;
+      const bool mine = k0 < f.lim;
+      if (mine) {
+        if (f.step >= tb_first + tb_steps) {
+          // the pages and scales of the next 32 / subs steps, one a lane
+          tb_first = f.step;
+          tb_steps = 32 / subs;
+          const int key = ((f.step + lane / subs) * kWarps + warp) * T::kKeys +
+                          ((lane & (subs - 1)) << sub_log2);
+          tb_page = 0;
+          tb_ks = tb_vs = 1.f;
+          if (key < f.lim) {
+            const int b = f.e / p.row_tiles;
+            tb_page = p.table[static_cast<long long>(b) * p.width + (key >> p.page_log2)];
+            if (static_cast<unsigned>(tb_page) >= static_cast<unsigned>(p.pages)) {
+              atomicOr(p.seq.err, kErrCache);
+              tb_page = 0;
+            }
+            const long long sc = static_cast<long long>(tb_page) * p.Hkv + f.h;
+            tb_ks = p.k_scale[sc];
+            tb_vs = p.v_scale[sc];
+          }
+        }
+        const int stage = fetched % kStages;
+        const int from = (f.step - tb_first) * subs;
+        const uint32_t bar = bars + 8 * stage;
+        const uint32_t dst = ring + stage * 2 * T::kBytes;
+        const int boxes = min(subs, (f.lim - k0 + (1 << sub_log2) - 1) >> sub_log2);
+        if (lane == 0) mbar_arrive_expect_tx(bar, boxes * T::kHalves * 2 * box_bytes);
+        for (int i = 0; i < boxes; ++i) {
+          const int page = __shfl_sync(0xffffffffu, tb_page, from + i);
+          const int row = subs > 1 ? 0 : k0 & ((1 << p.page_log2) - 1);
+          if (lane == 0) {
+            #pragma unroll
+            for (int c = 0; c < T::kHalves; ++c) {
+              const uint32_t to = dst + c * T::kKeys * T::kPitch + i * box_bytes;
+              tma_load_4d(to, &tm_k, bar, c * 128, row, f.h, page);
+              tma_load_4d(to + T::kBytes, &tm_v, bar, c * 128, row, f.h, page);
+            }
+          }
+        }
+        const float ks = __shfl_sync(0xffffffffu, tb_ks, from + (lane & (subs - 1)));
+        const float vs = __shfl_sync(0xffffffffu, tb_vs, from + (lane & (subs - 1)));
+        if (lane < subs) meta[stage * T::kSub + lane] = make_float2(ks, log2f(vs));
+        __syncwarp();
+        ++fetched;
+      }
+      --f_left;
+      if (++f.step == f.steps && f_left > 0) {
+        f.next_unit(p);
+        tb_steps = 0;
+        tb_first = 0;
+      }
+      if (mine) break;
+    }
+  };
+  #pragma unroll 1
+  for (int i = 0; i < kStages; ++i) fetch();
+
+  // ---------------------------------------------------------------- units
+  long long left = hi - lo;
+  while (left > 0) {
+    const int b = at.e / p.row_tiles, row0 = at.e % p.row_tiles * 8 * NT;
+    const int end = static_cast<int>(min(static_cast<long long>(at.steps), at.step + left));
+    // q of the unit's rows as B fragments of S^T = K Q^T: lane (g, t) of
+    // fragment (64-column part c, j) holds row g, columns 64c + 16t + 4j ..+3
+    for (int nt = warp; nt < NT; nt += kWarps) {
+      const int r = row0 + nt * 8 + g;
+      uint4 w[kChunks][2];
+      float amax = 0.f;
+      #pragma unroll
+      for (int c = 0; c < kChunks; ++c) w[c][0] = w[c][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < p.rows && r / p.seq.G < at.seq.n) {
+        const uint16_t* src = p.q + b * p.qs.b + (at.h * p.seq.G + r % p.seq.G) * p.qs.h +
+                              (r / p.seq.G) * p.qs.n + 16 * t;
+        #pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          w[c][0] = *reinterpret_cast<const uint4*>(src + 64 * c);
+          w[c][1] = *reinterpret_cast<const uint4*>(src + 64 * c + 8);
+        }
+      }
+      float down = 1.f;
+      if (p.bf16) {
+        #pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          #pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t u[4] = {w[c][i].x, w[c][i].y, w[c][i].z, w[c][i].w};
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 x = unpack2<true>(u[k]);
+              amax = fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y)));
+            }
+          }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23), 1), 253);
+        const bool plain = !(amax > 0.f) || !(amax < __uint_as_float(0x7f800000u));
+        down = plain ? 1.f : __uint_as_float(static_cast<uint32_t>(254 - e) << 23);   // 2^(127 - e)
+        if (t == 0) q_pow[nt * 8 + g] = plain ? 1.f : __uint_as_float(static_cast<uint32_t>(e) << 23);
+      } else if (t == 0) {
+        q_pow[nt * 8 + g] = 1.f;
+      }
+      #pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+        #pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t u[4] = {w[c][i].x, w[c][i].y, w[c][i].z, w[c][i].w};
+          if (p.bf16) {
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 x = unpack2<true>(u[k]);
+              u[k] = pack2<false>(x.x * down, x.y * down);
+            }
+          }
+          q_frag[((c * 4 + 2 * i) * NT + nt) * 32 + lane] = make_uint2(u[0], u[1]);
+          q_frag[((c * 4 + 2 * i + 1) * NT + nt) * 32 + lane] = make_uint2(u[2], u[3]);
+        }
+    }
+    __syncthreads();
+    uint2 qr[kQRegs ? kChunks * 4 : 1][kQRegs ? NT : 1];
+    if constexpr (kQRegs) {
+      #pragma unroll
+      for (int i = 0; i < kChunks * 4; ++i)
+        #pragma unroll
+        for (int nt = 0; nt < NT; ++nt) qr[i][nt] = q_frag[(i * NT + nt) * 32 + lane];
+    }
+    float qscale[NT][2], m[NT][2], l[NT][2];
+    float acc[kMT][NT][4];
+    #pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      #pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        qscale[nt][c] = q_pow[nt * 8 + 2 * t + c] * p.scale_log2;
+        m[nt][c] = kNoMax;
+        l[nt][c] = 0.f;
+      }
+    #pragma unroll
+    for (int i = 0; i < kMT; ++i)
+      #pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) acc[i][nt][k] = 0.f;
+
+    for (int step = at.step; step < end; ++step) {
+      const int k0 = (step * kWarps + warp) * T::kKeys;
+      if (k0 >= at.lim) continue;
+      const int stage = done % kStages;
+      if (!dead && !wait_uniform(bars + 8 * stage, (done / kStages) & 1, abort)) dead = true;
+      if (dead) continue;
+      const uint32_t kt = ring + stage * 2 * T::kBytes, vt = kt + T::kBytes;
+      const bool partial = k0 + T::kKeys > at.full;
+      #pragma unroll
+      for (int mt = 0; mt < T::kKeys / 16; ++mt) {
+        if (k0 + mt * 16 >= at.lim) break;
+        const float2 sc = meta[stage * T::kSub + ((mt * 16) >> sub_log2)];
+        const float inv_vs = ex2_approx(-sc.y);
+        // S^T of 16 keys
+        float s[NT][4];
+        #pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+        const int kr = mt * 16 + key_of<D>(g);
+        #pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          const uint32_t part = kt + (c >> 1) * T::kKeys * T::kPitch;
+          const uint4 x = ld_shared_v4(part + chunk_at<D>(kr, 4 * (c & 1) + t));
+          const uint4 y = ld_shared_v4(part + chunk_at<D>(kr + 8, 4 * (c & 1) + t));
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+          #pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t a0 = widen(xs[j] & 0xffffu), a2 = widen(xs[j] >> 16);
+            const uint32_t a1 = widen(ys[j] & 0xffffu), a3 = widen(ys[j] >> 16);
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint2 q2 = kQRegs ? qr[kQRegs ? c * 4 + j : 0][kQRegs ? nt : 0]
+                                      : q_frag[((c * 4 + j) * NT + nt) * 32 + lane];
+              mma(s[nt], a0, a1, a2, a3, q2.x, q2.y);
+            }
+          }
+        }
+        bool grow = false;
+        #pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          #pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            s[nt][k] = fmaf(s[nt][k], qscale[nt][k & 1] * sc.x, sc.y);
+            if (partial) {
+              const int r = row0 + nt * 8 + 2 * t + (k & 1);
+              const int key = k0 + kr + (k >> 1) * 8;
+              const int sees = p.seq.causal ? min(at.seq.len, at.seq.len - at.seq.n + r / p.seq.G + 1)
+                                            : at.seq.len;
+              if (key >= sees) s[nt][k] = -INFINITY;
+            }
+            grow |= s[nt][k] > m[nt][k & 1] + kGrow;
+          }
+        if (__any_sync(0xffffffffu, grow)) {
+          #pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            #pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float top = fmaxf(s[nt][c], s[nt][c + 2]);
+              #pragma unroll
+              for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+              const float now = fmaxf(m[nt][c], top);
+              const float f = ex2_approx(m[nt][c] - now);
+              m[nt][c] = now;
+              l[nt][c] *= f;
+              #pragma unroll
+              for (int i = 0; i < kMT; ++i) {
+                acc[i][nt][c] *= f;
+                acc[i][nt][c + 2] *= f;
+              }
+            }
+        }
+        // the weights, as B fragments of O^T = V^T P^T
+        uint32_t p0[NT], p1[NT];
+        #pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[4];
+          #pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            w[k] = ex2_approx(s[nt][k] - m[nt][k & 1]);
+            l[nt][k & 1] = fmaf(w[k], inv_vs, l[nt][k & 1]);
+          }
+          p0[nt] = transpose8x8(pack2<false>(w[0], w[1]));
+          p1[nt] = transpose8x8(pack2<false>(w[2], w[3]));
+        }
+        const int va = mt * 16 + key_of<D>(2 * t), vb = mt * 16 + key_of<D>(2 * t + 1);
+        bool nans = false;
+        #pragma unroll
+        for (int half = 0; half < T::kHalves; ++half) {
+          const uint32_t part = vt + half * T::kKeys * T::kPitch;
+          constexpr int kWords = D == 64 ? 2 : 4;    // 4-column words of a lane
+          uint32_t v[4][kWords];
+          #pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = (i & 1 ? vb : va) + (i >> 1) * 8;
+            if constexpr (D == 64) {
+              const uint32_t a = part + chunk_at<D>(r, g >> 1) + (g & 1) * 8;
+              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[i][0]), "=r"(v[i][1]) : "r"(a) : "memory");
+            } else {
+              const uint4 x = ld_shared_v4(part + chunk_at<D>(r, g));
+              v[i][0] = x.x;
+              v[i][1] = x.y;
+              v[i][2] = x.z;
+              v[i][3] = x.w;
+            }
+          }
+          if (partial) {
+            // a NaN in a masked place would turn 0 * NaN into NaN: NaN codes
+            // are taken out here and their effect on the rows that see them
+            // is added below
+            #pragma unroll
+            for (int i = 0; i < 4; ++i)
+              #pragma unroll
+              for (int w = 0; w < kWords; ++w) {
+                const uint32_t n = nan_bytes(v[i][w]);
+                nans |= n != 0;
+                v[i][w] &= ~n;
+              }
+          }
+          #pragma unroll
+          for (int w = 0; w < kWords; ++w)
+            #pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const uint32_t sel = u ? 0x7362u : 0x5140u;
+              const uint32_t x = __byte_perm(v[0][w], v[1][w], sel);
+              const uint32_t y = __byte_perm(v[2][w], v[3][w], sel);
+              const uint32_t a0 = widen(x & 0xffffu), a1 = widen(x >> 16);
+              const uint32_t a2 = widen(y & 0xffffu), a3 = widen(y >> 16);
+              #pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma(acc[half * 8 + 2 * w + u][nt], a0, a1, a2, a3, p0[nt], p1[nt]);
+            }
+        }
+        if (partial && __any_sync(0xffffffffu, nans)) {
+          // how many NaN values each row sees in each column: the product of
+          // the NaN places with the places that the rows see
+          uint32_t c0[NT], c1[NT];
+          #pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float w[4];
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = s[nt][k] == -INFINITY ? 0.f : 1.f;
+            c0[nt] = transpose8x8(pack2<false>(w[0], w[1]));
+            c1[nt] = transpose8x8(pack2<false>(w[2], w[3]));
+          }
+          #pragma unroll
+          for (int im = 0; im < kMT; ++im) {
+            // columns of fragment im held by this lane: words of the loads above
+            const int half = im / 8, w = im % 8 / 2, u = im & 1;
+            const uint32_t part = vt + half * T::kKeys * T::kPitch;
+            uint32_t n[4];
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = (i & 1 ? vb : va) + (i >> 1) * 8;
+              const uint32_t a = D == 64 ? part + chunk_at<D>(r, g >> 1) + (g & 1) * 8 + 4 * w
+                                         : part + chunk_at<D>(r, g) + 4 * w;
+              uint32_t x;
+              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(a) : "memory");
+              n[i] = nan_bytes(x) & 0x38383838u;     // 1.0 where the code is NaN
+            }
+            const uint32_t sel = u ? 0x7362u : 0x5140u;
+            const uint32_t x = __byte_perm(n[0], n[1], sel), y = __byte_perm(n[2], n[3], sel);
+            #pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float hits[4] = {0.f, 0.f, 0.f, 0.f};
+              mma(hits, widen(x & 0xffffu), widen(x >> 16), widen(y & 0xffffu), widen(y >> 16),
+                  c0[nt], c1[nt]);
+              #pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (hits[k] > 0.f) acc[im][nt][k] = __uint_as_float(0x7fffffffu);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      ++done;
+      fetch();
+    }
+
+    // -------------------------------------------------------------- join the warps
+    #pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      #pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        #pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], x);
+        if (g == 0) stat[warp * 8 * NT + nt * 8 + 2 * t + c] = make_float2(m[nt][c], l[nt][c]);
+      }
+    __syncthreads();
+    #pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      #pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float2 st[kWarps];
+        float top = kNoMax;
+        #pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          st[w] = stat[w * 8 * NT + nt * 8 + 2 * t + c];
+          top = fmaxf(top, st[w].x);
+        }
+        float sum = 0.f;
+        #pragma unroll
+        for (int w = 0; w < kWarps; ++w) sum = fmaf(st[w].y, ex2_approx(st[w].x - top), sum);
+        const float f = ex2_approx(m[nt][c] - top);
+        m[nt][c] = top;
+        l[nt][c] = sum;
+        #pragma unroll
+        for (int i = 0; i < kMT; ++i) {
+          acc[i][nt][c] *= f;
+          acc[i][nt][c + 2] *= f;
+        }
+      }
+    float4* buf = reinterpret_cast<float4*>(smem + S::kBufOff);
+    #pragma unroll
+    for (int round = 2; round > 0; round >>= 1) {
+      if (warp >= round && warp < 2 * round) {
+        float4* to = buf + (warp - round) * kMT * NT * 32 + lane;
+        #pragma unroll
+        for (int i = 0; i < kMT; ++i)
+          #pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            to[(i * NT + nt) * 32] = make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]);
+      }
+      __syncthreads();
+      if (warp < round) {
+        const float4* from = buf + warp * kMT * NT * 32 + lane;
+        #pragma unroll
+        for (int i = 0; i < kMT; ++i)
+          #pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float4 x = from[(i * NT + nt) * 32];
+            acc[i][nt][0] += x.x;
+            acc[i][nt][1] += x.y;
+            acc[i][nt][2] += x.z;
+            acc[i][nt][3] += x.w;
+          }
+      }
+      __syncthreads();
+    }
+    if (warp == 0) {
+      const bool whole = at.step == 0 && end == at.steps;
+      const long long slot = 2ll * blockIdx.x + (at.step > 0 ? 0 : 1);
+      constexpr int kVec = D == 64 ? 8 : 16;       // consecutive columns of a lane
+      #pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        #pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int rr = nt * 8 + 2 * t + c, r = row0 + rr;
+          if (r < p.rows) {
+            const int i = r / p.seq.G, head = at.h * p.seq.G + r % p.seq.G;
+            const bool live = i < at.seq.n;
+            const float sum = live ? l[nt][c] : 0.f;
+            if (whole) {
+              // a sum that is not above 0 is a row without keys, or NaN
+              const float inv = sum == 0.f ? 0.f : 1.f / sum;
+              #pragma unroll
+              for (int half = 0; half < T::kHalves; ++half) {
+                uint16_t* dst = p.o + b * p.os.b + head * p.os.h + i * p.os.n + 128 * half + kVec * g;
+                uint32_t w[kVec / 2];
+                #pragma unroll
+                for (int k = 0; k < kVec / 2; ++k) {
+                  const float x = acc[half * 8 + k][nt][c] * inv;
+                  const float y = acc[half * 8 + k][nt][2 + c] * inv;
+                  w[k] = sum == 0.f ? 0u : p.bf16 ? pack2<true>(x, y) : pack2<false>(x, y);
+                }
+                #pragma unroll
+                for (int k = 0; k < kVec / 8; ++k)
+                  reinterpret_cast<uint4*>(dst)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+              }
+              if (g == 0)
+                p.lse[(static_cast<long long>(b) * p.H + head) * p.seq.Nq + i] =
+                    sum == 0.f ? -INFINITY : (m[nt][c] + log2f(sum)) * kLn2;
+            } else {
+              #pragma unroll
+              for (int half = 0; half < T::kHalves; ++half) {
+                float* dst = p.part_o + (slot * 8 * NT + rr) * D + 128 * half + kVec * g;
+                #pragma unroll
+                for (int k = 0; k < kVec / 4; ++k)
+                  reinterpret_cast<float4*>(dst)[k] =
+                      make_float4(acc[half * 8 + 2 * k][nt][c], acc[half * 8 + 2 * k][nt][2 + c],
+                                  acc[half * 8 + 2 * k + 1][nt][c], acc[half * 8 + 2 * k + 1][nt][2 + c]);
+              }
+              if (g == 0) p.part_ml[slot * 8 * NT + rr] = make_float2(m[nt][c], sum);
+            }
+          }
+        }
+    }
+    left -= end - at.step;
+    if (left > 0) at.next_unit(p);
+  }
+  if (dead) {
+    // the copies still in flight, before their shared memory goes away
+    for (int i = done; i < fetched; ++i) drain_wait(bars + 8 * (i % kStages), (i / kStages) & 1);
+    if (lane == 0 && *abort == 2) atomicOr(p.seq.err, kErrTimeout);
+  }
+}
+
+// Joins the pieces of the units that lie in several shares, and writes the
+// units that see no key.  One CTA a unit, a warp a row; the pieces' weights
+// first, then their O, four rows of loads in flight.
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads)
+cache_merge_kernel(const __grid_constant__ FwdCacheParams p) {
+  constexpr int kVec = D / 32;
+  __shared__ long long red[kWarps];
+  const int unit = blockIdx.x, e = unit / p.Hkv, h = unit % p.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  bool bad = false;
+  const long long total = total_steps<D, NT>(p, red, &bad) * p.Hkv;
+  Sequence seq;
+  const TileLimits lim = limits_of<NT>(p, e, &seq, &bad);
+  const int steps = steps_of<D>(lim.lim);
+  // the steps of the entries before this one
+  long long before = 0;
+  for (int x = threadIdx.x; x < e; x += kThreads) {
+    Sequence s;
+    before += steps_of<D>(limits_of<NT>(p, x, &s, &bad).lim);
+  }
+  before = block_sum(before, red);
+  const long long share = (total + p.ctas - 1) / p.ctas;
+  const long long first = before * p.Hkv + static_cast<long long>(h) * steps;
+  const int c0 = steps > 0 ? static_cast<int>(first / share) : 0;
+  const int c1 = steps > 0 ? static_cast<int>((first + steps - 1) / share) : 0;
+  const int row0 = e % p.row_tiles * 8 * NT, b = e / p.row_tiles;
+  grid_dependency_wait();   // (every CTA: this grid's end is to imply the other's)
+  if (steps > 0 && c0 == c1) return;      // whole: written by its CTA
+  for (int rr = warp; rr < 8 * NT && row0 + rr < p.rows; rr += kWarps) {
+    const int r = row0 + rr, i = r / p.seq.G, head = h * p.seq.G + r % p.seq.G;
+    float top = kNoMax, sum = 0.f;
+    float acc[kVec];
+    #pragma unroll
+    for (int k = 0; k < kVec; ++k) acc[k] = 0.f;
+    if (steps > 0) {
+      for (int c = c0 + lane; c <= c1; c += 32)
+        top = fmaxf(top, p.part_ml[(2ll * c + (c == c0)) * 8 * NT + rr].x);
+      #pragma unroll
+      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      for (int cb = c0; cb <= c1; cb += 32) {
+        float2 ml = make_float2(kNoMax, 0.f);
+        const int mine = cb + lane;
+        if (mine <= c1) ml = p.part_ml[(2ll * mine + (mine == c0)) * 8 * NT + rr];
+        const float w = mine <= c1 ? ex2_approx(ml.x - top) : 0.f;
+        float part = ml.y * w;
+        #pragma unroll
+        for (int x = 16; x > 0; x >>= 1) part += __shfl_xor_sync(0xffffffffu, part, x);
+        sum += part;
+        const int n = min(32, c1 - cb + 1);
+        for (int k0 = 0; k0 < n; k0 += 4) {
+          float x[4][kVec], wk[4];
+          #pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            wk[k] = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+            const int c = cb + k0 + k;
+            #pragma unroll
+            for (int v = 0; v < kVec; ++v) x[k][v] = 0.f;
+            if (k0 + k < n) {
+              const float* src = p.part_o + ((2ll * c + (c == c0)) * 8 * NT + rr) * D + lane * kVec;
+              #pragma unroll
+              for (int v = 0; v < kVec; v += 2) {
+                const float2 y = *reinterpret_cast<const float2*>(src + v);
+                x[k][v] = y.x;
+                x[k][v + 1] = y.y;
+              }
+            }
+          }
+          #pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k0 + k < n)
+              #pragma unroll
+              for (int v = 0; v < kVec; ++v) acc[v] = fmaf(x[k][v], wk[k], acc[v]);
+        }
+      }
+    }
+    if (i >= seq.n) sum = 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + b * p.os.b + head * p.os.h + i * p.os.n + lane * kVec);
+    #pragma unroll
+    for (int v = 0; v < kVec; v += 2)
+      dst[v / 2] = sum == 0.f ? 0u
+                   : p.bf16 ? pack2<true>(acc[v] * inv, acc[v + 1] * inv)
+                            : pack2<false>(acc[v] * inv, acc[v + 1] * inv);
+    if (lane == 0)
+      p.lse[(static_cast<long long>(b) * p.H + head) * p.seq.Nq + i] =
+          sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  }
+}
+
+// Rows of a unit's tile: the fewest 8-row fragments that hold all G * Nq rows,
+// up to what the accumulators of a warp allow (128 registers of O).
+int row_fragments(int rows, int d) {
+  const int most = d == 64 ? 8 : d == 128 ? 4 : 2;
+  int nt = 1;
+  while (nt < most && 8 * nt < rows) nt *= 2;
+  return nt;
+}
+
+template <int D, int NT>
+cudaError_t ctas_for(int sms, int* ctas) {
+  static std::atomic<int> per_sm[64];   // by device, 0 = not asked yet
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (per_sm[dev & 63] == 0) {
+    auto kern = cache_fwd_kernel<D, NT>;
+    constexpr int smem = Smem<D, NT>::kAlloc;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    int n = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, smem);
+    if (e != cudaSuccess) return e;
+    per_sm[dev & 63] = std::max(1, std::min(n, 2));
+  }
+  *ctas = per_sm[dev & 63] * sms;
+  return cudaSuccess;
+}
+
+template <int D, int NT>
+cudaError_t launch(const Cache& cache, FwdCacheParams& p, int sms, cudaStream_t stream) {
+  cudaError_t e = ctas_for<D, NT>(sms, &p.ctas);
+  if (e != cudaSuccess) return e;
+  constexpr int cols = D < 128 ? D : 128;
+  const int box_rows = std::min(cache.page, Tile<D>::kKeys);
+  CUtensorMap tk, tv;
+  if ((e = make_tmap_u8_4d(&tk, cache.k, D, cache.page, cache.Hkv, cache.pages, cache.ks, cols,
+                           box_rows)) != cudaSuccess)
+    return e;
+  if ((e = make_tmap_u8_4d(&tv, cache.v, D, cache.page, cache.Hkv, cache.pages, cache.vs, cols,
+                           box_rows)) != cudaSuccess)
+    return e;
+  cache_fwd_kernel<D, NT><<<p.ctas, kThreads, Smem<D, NT>::kAlloc, stream>>>(tk, tv, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.seq.B) * p.row_tiles * p.Hkv);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_merge_kernel<D, NT>, p);
+}
+
+}  // namespace
+
+// Two pieces of a row tile for each of at most two CTAs an SM.
+size_t cache_fwd_workspace_bytes(int, int H, int Hkv, int Nq, int d, int sms) {
+  const size_t rows = 8ull * row_fragments(static_cast<int>(std::min(1ll * H / Hkv * Nq, 1ll << 20)), d);
+  return 4ull * sms * rows * (d * sizeof(float) + sizeof(float2));
+}
+
+cudaError_t launch_cache_fwd(const Cache& cache, const CacheFwdCall& c, int sms,
+                             cudaStream_t stream) {
+  FwdCacheParams p = {};
+  p.seq = {c.seq_lens, c.new_lens, c.B, c.H / cache.Hkv, c.Nq, c.causal,
+           static_cast<long long>(cache.width) * cache.page, c.err};
+  p.q = static_cast<const uint16_t*>(c.q);
+  p.o = static_cast<uint16_t*>(c.o);
+  p.lse = c.lse;
+  p.qs = c.qs;
+  p.os = c.os;
+  p.k_scale = cache.k_scale;
+  p.v_scale = cache.v_scale;
+  p.table = cache.table;
+  p.width = cache.width;
+  p.pages = cache.pages;
+  while ((1 << p.page_log2) < cache.page) ++p.page_log2;
+  p.H = c.H;
+  p.Hkv = cache.Hkv;
+  p.rows = p.seq.G * c.Nq;
+  p.bf16 = c.bf16;
+  p.scale_log2 = c.scale * 1.4426950408889634f;
+  const int nt = row_fragments(p.rows, cache.d);
+  p.row_tiles = (p.rows + 8 * nt - 1) / (8 * nt);
+  p.part_o = static_cast<float*>(c.workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + 4ull * sms * 8 * nt * cache.d);
+  switch (cache.d * 16 + nt) {
+    case 64 * 16 + 1: return launch<64, 1>(cache, p, sms, stream);
+    case 64 * 16 + 2: return launch<64, 2>(cache, p, sms, stream);
+    case 64 * 16 + 4: return launch<64, 4>(cache, p, sms, stream);
+    case 64 * 16 + 8: return launch<64, 8>(cache, p, sms, stream);
+    case 128 * 16 + 1: return launch<128, 1>(cache, p, sms, stream);
+    case 128 * 16 + 2: return launch<128, 2>(cache, p, sms, stream);
+    case 128 * 16 + 4: return launch<128, 4>(cache, p, sms, stream);
+    case 256 * 16 + 1: return launch<256, 1>(cache, p, sms, stream);
+    case 256 * 16 + 2: return launch<256, 2>(cache, p, sms, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace fa

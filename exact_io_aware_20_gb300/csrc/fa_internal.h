@@ -5,6 +5,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "fa.h"
+
 namespace fa {
 
 // Shapes and pointers of one call, after validation.
@@ -93,6 +95,11 @@ struct BwdArgs {
 cudaError_t make_tmap_4d(CUtensorMap* map, const void* base, int cols, int rows, int heads,
                          int batch, const Strides& st, int box_cols, int box_rows);
 
+// The same over an 8-bit [pages][heads][rows][cols] view (byte strides st);
+// box_cols 128 (128-byte swizzle) or 64 (64-byte swizzle).
+cudaError_t make_tmap_u8_4d(CUtensorMap* map, const void* base, int cols, int rows, int heads,
+                            int pages, const Strides& st, int box_cols, int box_rows);
+
 // Encode a 3-D tiled tensor map over a contiguous fp32 [planes][rows][cols]
 // array with a box of box_cols x box_rows of one plane and no swizzle;
 // coordinates (col, row, plane).
@@ -103,6 +110,68 @@ cudaError_t make_tmap_f32_3d(CUtensorMap* map, const float* base, int cols, int 
 // to timing_end, or -1 when timing is off or out of event pairs.
 int timing_begin(int kind, cudaStream_t stream);
 void timing_end(int slot, cudaStream_t stream);
+
+// Rotary positions (see fa_rope_spec): the angles' fractions of a turn per
+// position in 2^-64 turns, and where a token's positions are.
+struct RopeArgs {
+  unsigned long long turn[FA_ROPE_MAX_PAIRS];
+  unsigned char axis[FA_ROPE_MAX_PAIRS];
+  const int* positions;   // [axes][pos_batch][N], nullptr: the token's own number
+  int pos_batch;
+  int axes, pairs;        // pairs == 0: no rotation
+  int interleaved, inverse;
+};
+
+struct RopeCall {
+  const void *q, *k;      // k nullptr: q only
+  void *q_out, *k_out;
+  Strides qs, ks, qos, kos;
+  int B, H, Hkv, N, d, bf16;
+};
+cudaError_t launch_rope(const RopeCall& c, const RopeArgs& r, cudaStream_t stream);
+
+// A paged 8-bit cache (see fa_cache), strides in bytes.
+struct Cache {
+  unsigned char *k, *v;
+  float *k_scale, *v_scale;
+  const int* table;
+  int pages, page, width;   // pages, tokens of a page, entries of a table row
+  int Hkv, d;
+  Strides ks, vs;
+};
+
+struct AppendCall {
+  const void *q, *k, *v;    // q nullptr: keys and values only
+  void* q_out;
+  Strides qs, ks, vs, qos;
+  int B, H, N, bf16;
+  const int *seq_lens, *new_lens;
+  unsigned int* err;
+};
+cudaError_t launch_cache_append(const Cache& cache, const AppendCall& c, const RopeArgs& r,
+                                cudaStream_t stream);
+
+struct CacheFwdCall {
+  const void* q;
+  void* o;
+  float* lse;
+  Strides qs, os;
+  int B, H, Nq, causal, bf16;
+  float scale;
+  const int *seq_lens, *new_lens;
+  void* workspace;
+  unsigned int* err;
+};
+size_t cache_fwd_workspace_bytes(int B, int H, int Hkv, int Nq, int d, int sms);
+cudaError_t launch_cache_fwd(const Cache& cache, const CacheFwdCall& c, int sms,
+                             cudaStream_t stream);
+
+// C-ABI helpers: record a CUDA error's text (returns FA_ERR_CUDA); check that
+// the current device is an sm_103 part and get its error word; a caller's
+// strides.
+int cuda_fail(cudaError_t e, const char* where);
+int check_device(unsigned int** err);
+bool valid_strides(const fa_strides* s, int n, Strides* out);
 
 cudaError_t launch_fwd(const Problem& p, const FwdArgs& a, cudaStream_t stream);
 cudaError_t launch_fwd_blocksparse(const Problem& p, const FwdArgs& a, cudaStream_t stream);

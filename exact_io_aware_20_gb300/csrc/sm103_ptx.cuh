@@ -20,6 +20,7 @@ namespace fa {
 
 // Bits of the device-side error word the kernels report into.
 constexpr unsigned int kErrTimeout = 1u;
+constexpr unsigned int kErrCache = 4u;   // a page index or a sequence length out of range
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

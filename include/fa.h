@@ -61,7 +61,9 @@ enum fa_status {
   FA_ERR_UNSUPPORTED = 2, /* head dim, dtype or device (not sm_103) not supported */
   FA_ERR_CUDA = 3,        /* a CUDA call failed; fa_strerror(FA_ERR_CUDA) has its text */
   FA_ERR_TIMEOUT = 4,     /* a bounded device-side wait expired (from fa_get_device_status) */
-  FA_ERR_WORKSPACE = 5    /* backward workspace missing, misaligned or too small for the path */
+  FA_ERR_WORKSPACE = 5,   /* workspace missing, misaligned or too small for the path */
+  FA_ERR_CACHE = 6        /* a page table entry or a sequence length was out of range (from
+                             fa_get_device_status) */
 };
 
 /*
@@ -276,9 +278,135 @@ int fa_bwd_blocksparse(const void *q, const void *k, const void *v, const void *
                        void *workspace, size_t workspace_bytes, fa_stream_t stream);
 
 /*
+ * Rotary positions (no counterpart on the pages: the rotation that attention
+ * models apply to q and k before the products above).  A pair (x1, x2) of
+ * columns of a row whose token stands at position t turns by the angle
+ * t * freq:
+ *     (x1, x2)  ->  (x1 cos - x2 sin,  x2 cos + x1 sin).
+ * Pair p is columns (p, p + pairs) of the first 2 * pairs columns, or columns
+ * (2p, 2p + 1) when interleaved; columns from 2 * pairs on are copied.  A
+ * token has one position for each axis (one for text; time, height and width
+ * for video) and pair p takes the position of axis[p].  freq is in radians
+ * per position; the angle is kept as a 64-bit fraction of a turn, so far
+ * positions lose nothing (angles are good to about 2^-23 radians at every
+ * position).
+ */
+#define FA_ROPE_MAX_PAIRS 128
+#define FA_ROPE_MAX_AXES 4
+typedef struct fa_rope_spec {
+  int axes;        /* 1 .. FA_ROPE_MAX_AXES */
+  int pairs;       /* a multiple of 8, 8 <= pairs <= d / 2 */
+  int interleaved; /* 0 or 1 */
+  double freq[FA_ROPE_MAX_PAIRS];         /* finite */
+  unsigned char axis[FA_ROPE_MAX_PAIRS];  /* < axes */
+} fa_rope_spec;
+
+/*
+ * Rotates q [B][H][N][d] into q_out and k [B][Hkv][N][d] into k_out (16-bit,
+ * `dtype`; each rotated value rounded once) in one launch.  inverse = 1 turns
+ * the other way: the backward pass, from the gradients of q_out and k_out to
+ * those of q and k.  k may be NULL (k_out then too; Hkv is not looked at).
+ * positions: int32 [axes][pos_batch][N] on the device, pos_batch 1 (the same
+ * for every sequence) or B, any values (negative ones too); NULL: row n of
+ * every sequence stands at n on every axis.  strides[4]: of q, k, q_out,
+ * k_out as in fa_fwd_strided (the entries of a NULL k are not looked at);
+ * NULL: contiguous.  An output may be its own input (same pointer and
+ * strides) and must not overlap anything else.  spec is read during the call.
+ */
+int fa_rope(const void *q, const void *k, void *q_out, void *k_out, int B, int H, int Hkv, int N,
+            int d, int dtype, const fa_rope_spec *spec, const int *positions, int pos_batch,
+            int inverse, const fa_strides *strides, fa_stream_t stream);
+
+/*
+ * A paged key/value cache held in 8 bits (no counterpart on the pages: the
+ * form in which a server keeps K and V between decoding steps).  A page holds
+ * page_size tokens of every key/value head as e4m3 codes, with one fp32 scale
+ * for each (page, head) of K and of V: the value of a code is code * scale.
+ * Token t of sequence b is row t % page_size of page
+ * block_table[b * table_width + t / page_size].  All arrays are device
+ * memory.  k and v are [pages][Hkv][page_size][d] views with the d codes of a
+ * row contiguous, 16-byte aligned, with byte strides that are positive
+ * multiples of 16 (batch = from page to page); the scales are contiguous
+ * [pages][Hkv], block_table is contiguous [B][table_width].  Entries of
+ * block_table past a sequence's last page are not read.
+ *
+ * Scales are powers of two when fa_cache_append writes them: the smallest
+ * 2^e, e >= -100, for which the largest finite magnitude among the tokens
+ * being added to the page is at most 448 * 2^e, but never smaller than the
+ * scale of tokens that the page holds already.  When it grows, the codes that
+ * are there are rounded again for the new scale (exact for all but e4m3
+ * subnormals).  A page whose first row is being written starts anew: what it
+ * held before does not matter.
+ */
+typedef struct fa_cache {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  const int *block_table;
+  int pages, page_size; /* page_size 16, 32, 64, 128 or 256 */
+  int table_width;
+  int Hkv, d;
+  fa_strides k_strides, v_strides; /* all zero: contiguous */
+} fa_cache;
+
+/*
+ * Appends the tokens k, v [B][Hkv][N][d] (16-bit) to the cache and rotates
+ * the keys, and q [B][H][N][d] into q_out, on the way; one launch.
+ * seq_lens: int32 [B], the length of each sequence counting its new tokens.
+ * new_lens: int32 [B], 0 <= new_lens[b] <= N, how many of the N rows of
+ * sequence b are tokens (a padded batch); NULL: all N.  Row i of sequence b
+ * becomes token seq_lens[b] - new_lens[b] + i; rows from new_lens[b] on are
+ * not stored, and their rows of q_out are set to zero.  positions as in
+ * fa_rope; NULL: a token's position is its number in the sequence.  spec NULL:
+ * no rotation (q is then copied).  q may be NULL (q_out then too, and H is
+ * not looked at).  Keys are rounded once, from the rotated fp32 value to
+ * e4m3.  NaN is stored as NaN, and so is an infinity (e4m3 has none); neither
+ * takes part in the scale.  Pages that receive tokens must not be shared
+ * between sequences.  strides[4]: of q, k, v, q_out; NULL: contiguous.  q_out
+ * may be q.
+ *
+ * A sequence whose length is below its new tokens or above the table's pages,
+ * or whose new_lens entry is outside 0 .. N, is skipped (its q_out rows are
+ * set to zero), and a page outside 0 .. pages - 1 is not written: either is
+ * reported by the next fa_get_device_status as FA_ERR_CACHE.
+ */
+int fa_cache_append(const fa_cache *cache, const void *q, const void *k, const void *v,
+                    void *q_out, int B, int H, int N, int dtype, const int *seq_lens,
+                    const int *new_lens, const fa_rope_spec *spec, const int *positions,
+                    int pos_batch, const fa_strides *strides, fa_stream_t stream);
+
+/*
+ * Attention over the cache: o, lse as fa_fwd_qk writes them, for q
+ * [B][H][Nq][d] and, in sequence b, the first seq_lens[b] cached tokens.
+ * With causal = 1 the new_lens[b] query rows (NULL: all Nq) are the last
+ * tokens of the sequence: row i sees tokens up to seq_lens[b] - new_lens[b] +
+ * i; with causal = 0 every row sees every token (an encoder's states).  Rows
+ * from new_lens[b] on, and rows that see no token, get O = 0 and L = -inf.
+ * What lies in masked places (rows of a page past the length, later tokens)
+ * does not reach a row, whatever its value, NaN included.  The lengths are
+ * read on the device, so a captured graph serves growing sequences.
+ * Scales must be positive and finite, between 2^-100 and 2^120.
+ * strides[2]: of q, o; NULL: contiguous.  workspace: device memory of at
+ * least fa_fwd_cache_workspace_size(...) bytes for the current device,
+ * 256-byte aligned; its contents on entry do not matter.  Sequences with a
+ * length outside 0 .. table_width * page_size or a new_lens entry outside
+ * 0 .. Nq count as empty, and pages outside 0 .. pages - 1 give undefined
+ * rows (nothing out of range is read): both are reported by the next
+ * fa_get_device_status as FA_ERR_CACHE.
+ */
+int fa_fwd_cache(const void *q, const fa_cache *cache, void *o, float *lse, int B, int H, int Nq,
+                 int causal, float scale, int dtype, const int *seq_lens, const int *new_lens,
+                 const fa_strides *strides, void *workspace, size_t workspace_bytes,
+                 fa_stream_t stream);
+
+/* Bytes of workspace fa_fwd_cache needs on the current device; 0 for invalid
+ * sizes. */
+size_t fa_fwd_cache_workspace_size(int B, int H, int Hkv, int Nq, int d);
+
+/*
  * Synchronises `stream`, then reports (and clears) the device-side error
  * word: FA_ERR_TIMEOUT if a kernel gave up on a bounded wait since the last
- * call, FA_ERR_CUDA if the stream itself failed, FA_OK otherwise.
+ * call, FA_ERR_CACHE if a kernel met a page table entry or a sequence length
+ * out of range, FA_ERR_CUDA if the stream itself failed, FA_OK otherwise.
  */
 int fa_get_device_status(fa_stream_t stream);
 

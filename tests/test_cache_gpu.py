@@ -1,0 +1,433 @@
+"""The paged 8-bit cache: fa_cache_append and fa_fwd_cache against 64-bit plain
+forms (cache_ref.py), and a run of them together as a server makes it."""
+import math
+
+import pytest
+import torch
+
+import cache_ref as ref
+from exact_io_aware_20_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+T = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def dev(x):
+    return None if x is None else x.to(DEV)
+
+
+def device_cache(codes, scales, table):
+    return binding.Cache(codes[0].to(DEV), codes[1].to(DEV), scales[0].to(DEV), scales[1].to(DEV),
+                         table.to(DEV))
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+# ------------------------------------------------------------------ append
+def check_pages(got_codes, got_scales, want, exact_rows, bound=None):
+    """Codes and scales against a ref.Paged; `bound`: [pages, Hkv, page, d]
+    slack of the values (0 where they are to be equal)."""
+    values = ref.codes_to_values(got_codes)
+    scales = got_scales.cpu().double()
+    assert torch.equal(scales, want.scales)
+    a, b = values * scales[..., None, None], want.values * want.scales[..., None, None]
+    same = torch.isnan(a) & torch.isnan(b) | (a == b)
+    if exact_rows:
+        assert same.all()
+    else:
+        near = (a - b).abs() <= bound
+        assert (same | near).all()
+        assert same.double().mean() > 0.999
+
+
+def run_append(dtype, d, page, Hkv, H, N, starts, new, axes, interleaved, pairs, given_pos,
+               layout="bnhd", value=1.0, seed=0):
+    g = torch.Generator().manual_seed(seed + 7 * d + page + N)
+    B = len(starts)
+    lens = [s + n for s, n in zip(starts, new)]
+    width = max(1, max(-(-n // page) for n in lens)) + 1
+    codes, scales, table = ref.make_cache(B * width + 2, Hkv, page, d, B, width, g, lens)
+    cache = device_cache(codes, scales, table)
+
+    def tokens(heads):
+        x = torch.randn(B, N, heads, d, generator=g) * value
+        x = x * torch.exp(torch.randn(B, 1, heads, 1, generator=g))
+        x = x.to(T[dtype])
+        return x.transpose(1, 2) if layout == "bnhd" else x.transpose(1, 2).contiguous()
+
+    q, k, v = tokens(H), tokens(Hkv), tokens(Hkv)
+    freq = [10000.0 ** (-i / max(1, pairs)) for i in range(pairs)]
+    axis = [i * axes // max(1, pairs) for i in range(pairs)]
+    rope = binding.Rope(freq, axis, interleaved) if pairs else None
+    pos = torch.randint(0, 200000, (axes, B, N), generator=g, dtype=torch.int32) if given_pos else None
+    full = all(n == N for n in new)
+    q_out = binding.cache_append(cache, dev(q), dev(k), dev(v), ints(lens),
+                                 new_lens=None if full else ints(new), rope=rope, positions=dev(pos))
+    binding.device_status()
+    if pos is None:
+        pos = torch.stack([torch.tensor([starts[b] + i for i in range(N)]) for b in range(B)])[None]
+        pos = pos.expand(axes, B, N)
+    kr, qr = ref.rotate(k, pos, freq, axis, interleaved), ref.rotate(q, pos, freq, axis, interleaved)
+    slack = ref.rotate_slack(k, pairs, interleaved) * 2.0 ** -21
+    want_k, want_v = ref.Paged(codes[0], scales[0]), ref.Paged(codes[1], scales[1])
+    bound = torch.zeros_like(want_k.values)
+    for b in range(B):
+        want_k.append(kr[b, :, :new[b]], starts[b], table[b])
+        want_v.append(v[b, :, :new[b]].double(), starts[b], table[b])
+        for i in range(new[b]):
+            p, r = int(table[b][(starts[b] + i) // page]), (starts[b] + i) % page
+            # a value within the rotation's error of a border may round to the
+            # other side: one step, 2^-3 of the value or 2^-9 of the scale
+            bound[p, :, r] = slack[b, :, i] + torch.maximum(
+                kr[b, :, i].abs() * 2.0 ** -3, want_k.scales[p][:, None] * 2.0 ** -9) * 1.01
+    check_pages(cache.tensors[0], cache.tensors[2], want_k, pairs == 0, bound)
+    check_pages(cache.tensors[1], cache.tensors[3], want_v, True)
+    for b in range(B):
+        qb = qr[b, :, :new[b]]
+        lim = ref.half_step(q.dtype) * qb.abs() * 1.001 + 2.0 ** -25 \
+            + 2.0 ** -21 * ref.rotate_slack(q, pairs, interleaved)[b, :, :new[b]]
+        assert ((q_out[b, :, :new[b]].cpu().double() - qb).abs() <= lim).all()
+        assert (q_out[b, :, new[b]:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d,page,N", [(64, 16, 1), (128, 64, 1), (256, 32, 3), (128, 16, 40),
+                                      (64, 32, 100), (128, 64, 150), (256, 64, 70), (128, 128, 200),
+                                      (256, 256, 300)])
+@pytest.mark.parametrize("axes,interleaved,part,given", [(1, False, 1, True), (3, True, 1, True),
+                                                         (1, False, 2, False), (1, True, 0, False)])
+def test_append(dtype, d, page, N, axes, interleaved, part, given):
+    starts = [0, 5, page, page - 1, 2 * page + 3]
+    run_append(dtype, d, page, 2, 6, N, starts, [N] * 5, axes, interleaved,
+               d // 2 // part if part else 0, given)
+
+
+@pytest.mark.parametrize("d,page,N", [(64, 16, 33), (128, 64, 9), (256, 128, 140)])
+def test_append_padded_batch(d, page, N):
+    run_append("f16", d, page, 4, 4, N, [0, 7, page, 30, 1, 0], [N, 1, 0, N // 2, N - 1, 0], 1, False,
+               d // 2, False, layout="bhnd")
+
+
+@pytest.mark.parametrize("value", [1e-6, 30.0, 60000.0 / 500])
+def test_append_grows_or_keeps_the_scale(value):
+    """Tokens far smaller and far larger than those that the page holds."""
+    run_append("bf16", 128, 32, 2, 2, 7, [3, 31, 20, 40], [7, 7, 7, 7], 1, False, 0, False, value=value)
+
+
+def test_append_one_by_one_keeps_what_is_there():
+    """A page filled token by token, each larger than the last: the codes that
+    are there are rounded again for every new scale, as the definition says."""
+    g = torch.Generator().manual_seed(11)
+    codes, scales, table = ref.make_cache(3, 1, 16, 64, 1, 2, g)
+    cache = device_cache(codes, scales, table)
+    want = ref.Paged(codes[1], scales[1])
+    for t in range(20):
+        x = (torch.randn(1, 1, 1, 64, generator=g) * 2.0 ** t / 100).half()
+        binding.cache_append(cache, None, dev(x), dev(x), ints([t + 1]))
+        want.append(x[0].double(), t, table[0])
+    binding.device_status()
+    check_pages(cache.tensors[1], cache.tensors[3], want, True)
+
+
+def test_append_infinities_nan_zeros_and_extremes():
+    g = torch.Generator().manual_seed(12)
+    codes, scales, table = ref.make_cache(4, 1, 16, 64, 2, 2, g)
+    cache = device_cache(codes, scales, table)
+    x = torch.randn(2, 1, 16, 64, generator=g).bfloat16()
+    x[0, 0, 2, 5], x[0, 0, 3, 6], x[0, 0, 4, 7] = math.inf, -math.inf, math.nan
+    x[1] = 0
+    x[1, 0, 1, 0] = 3.3895e38     # the largest bf16
+    y = torch.zeros(2, 1, 16, 64).bfloat16()
+    y[1, 0, 0, 0] = 1e-38
+    binding.cache_append(cache, None, dev(x), dev(y), ints([16, 16]))
+    binding.device_status()
+    for which, t in ((0, x), (1, y)):
+        want = ref.Paged(codes[which], scales[which])
+        for b in range(2):
+            want.append(t[b].double(), 0, table[b])
+        check_pages(cache.tensors[which], cache.tensors[2 + which], want, True)
+
+
+def test_append_into_strided_pages_leaves_the_rest():
+    """Pages as [pages, page, heads, d] inside a wider buffer; what is not a new
+    token's row stays, byte for byte."""
+    g = torch.Generator().manual_seed(13)
+    buf = torch.randint(0, 255, (6, 32, 2, 2, 128), generator=g, dtype=torch.uint8).to(DEV)
+    kept = buf.clone()
+    kc, vc = (buf[:, :, i].transpose(1, 2) for i in (0, 1))
+    sc = [torch.ones(6, 2, device=DEV) for _ in range(2)]
+    table = torch.tensor([[4, 1], [0, 5]], dtype=torch.int32)
+    cache = binding.Cache(kc, vc, sc[0], sc[1], table.to(DEV))
+    x = torch.randn(2, 2, 8, 128, generator=g).half()
+    binding.cache_append(cache, None, dev(x), dev(x), ints([36, 8]))
+    binding.device_status()
+    changed = (buf != kept).any(-1).any(-1).any(-1).cpu()
+    allowed = torch.zeros(6, 32, dtype=torch.bool)
+    allowed[4, 28:], allowed[1, :4], allowed[0, :8] = True, True, True
+    assert not (changed & ~allowed).any()
+    assert torch.equal(kc[1, :, :4], vc[1, :, :4]) and bool((sc[0][[2, 3, 5]] == 1).all())
+
+
+# ------------------------------------------------------------------ attention
+def check_attention(o, lse, q, k, v, table, lens, new, causal, scale):
+    want, l_want, slack, l_slack = ref.attend(q, k, v, table, lens, new, causal, scale)
+    o, lse = o.cpu().double(), lse.cpu().double()
+    empty = torch.isneginf(l_want)
+    assert torch.equal(torch.isneginf(lse), empty)
+    assert (o[empty] == 0).all()
+    l_err = (lse - l_want)[~empty].abs()
+    assert (l_err <= l_slack[~empty]).all(), float((l_err - l_slack[~empty]).max())
+    err = (o - want).abs()
+    bound = slack * 1.001 + ref.half_step(q.dtype) * (want.abs() + slack) + 2.0 ** -25
+    assert (err <= bound).all(), float((err - bound).max())
+
+
+def run_attention(dtype, d, page, H, Hkv, Nq, lens, new=None, causal=True, layout="bhnd", seed=0,
+                  spread=1.0, splice=None):
+    g = torch.Generator().manual_seed(seed + d + page + Nq + sum(lens))
+    B = len(lens)
+    width = max(1, max(-(-n // page) for n in lens)) + 2
+    codes, scales, table = ref.make_cache(B * width + 3, Hkv, page, d, B, width, g, lens, spread)
+    for c in codes:     # rows past a sequence's length hold anything, NaN among it
+        for b in range(B):
+            if lens[b] % page:
+                c.view(torch.uint8)[int(table[b][lens[b] // page]), :, lens[b] % page:] = 0x7F
+    if splice is not None:
+        splice(codes, table)
+    cache = device_cache(codes, scales, table)
+    if layout == "bhnd":
+        q = torch.randn(B, H, Nq, d, generator=g).to(T[dtype])
+    else:
+        q = torch.randn(B, Nq, H, d, generator=g).to(T[dtype]).transpose(1, 2)
+    scale = 1.0 / math.sqrt(d)
+    o, lse = binding.forward_cache(dev(q), cache, ints(lens), causal, scale,
+                                   new_lens=None if new is None else ints(new))
+    binding.device_status()
+    check_attention(o, lse, q, ref.Paged(codes[0], scales[0]), ref.Paged(codes[1], scales[1]), table,
+                    lens, [Nq] * B if new is None else new, causal, scale)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("H,Hkv", [(4, 4), (8, 2), (16, 1), (7, 1)])
+def test_single_tokens(dtype, d, page, H, Hkv):
+    run_attention(dtype, d, page, H, Hkv, 1, [1, 15, 16, 17, 100, 0, 300, 1031])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("H,Hkv,Nq", [(4, 2, 2), (4, 1, 3), (8, 2, 7), (2, 2, 33), (6, 2, 50),
+                                      (2, 1, 150)])
+def test_several_tokens(d, causal, H, Hkv, Nq):
+    run_attention("bf16", d, 32, H, Hkv, Nq, [Nq, Nq + 1, 200, 333], causal=causal, layout="bnhd")
+
+
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64), (256, 16)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_padded_queries_and_short_sequences(d, page, causal):
+    """Query rows that are no tokens, sequences shorter than their query rows,
+    empty ones."""
+    run_attention("f16", d, page, 4, 2, 12, [12, 40, 0, 3, 100, 5], [12, 3, 4, 9, 0, 5], causal=causal)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("Nq", [3, 90])
+def test_nan_in_later_tokens_reaches_only_the_rows_that_see_it(d, Nq):
+    """A NaN among the last token's values is 0 * NaN for every earlier row of
+    the same tile if the weights alone hide it."""
+    lens = [100 + Nq]
+    g = torch.Generator().manual_seed(5)
+    codes, scales, table = ref.make_cache(16, 1, 16, d, 1, 14, g, lens)
+    clean = device_cache(codes, scales, table)
+    q = torch.randn(1, 2, Nq, d, generator=g).half()
+    want, _ = binding.forward_cache(dev(q), clean, ints(lens), True, 0.1)
+    last = lens[0] - 1
+    for c in codes:
+        c.view(torch.uint8)[int(table[0][last // 16]), 0, last % 16, 3] = 0xFF
+    o, lse = binding.forward_cache(dev(q), device_cache(codes, scales, table), ints(lens), True, 0.1)
+    binding.device_status()
+    assert torch.equal(o[:, :, :-1], want[:, :, :-1])
+    assert torch.isnan(o[:, :, -1]).all() and torch.isnan(lse[:, :, -1]).all()
+    # NaN among the values only: only that column of the row that sees it
+    codes[0].view(torch.uint8)[int(table[0][last // 16]), 0, last % 16, 3] = 0x11
+    fine = device_cache(codes, scales, table)
+    o, lse = binding.forward_cache(dev(q), fine, ints(lens), True, 0.1)
+    hit = torch.isnan(o)
+    assert hit[:, :, -1, 3].all() and int(hit.sum()) == 2 and torch.isfinite(lse).all()
+
+
+def test_scales_of_unlike_size():
+    """Pages whose value scales differ by 2^40 and more: the weights carry the
+    scale, so the large ones must not drown or overflow the small ones' sums."""
+    g = torch.Generator().manual_seed(6)
+    lens = [500, 77]
+    codes, scales, table = ref.make_cache(80, 2, 16, 128, 2, 33, g, lens)
+    scales[1] = 2.0 ** torch.randint(-50, 20, (80, 2), generator=g).float()
+    cache = device_cache(codes, scales, table)
+    q = torch.randn(2, 4, 1, 128, generator=g).bfloat16()
+    o, lse = binding.forward_cache(dev(q), cache, ints(lens), True, 0.05)
+    binding.device_status()
+    check_attention(o, lse, q, ref.Paged(codes[0], scales[0]), ref.Paged(codes[1], scales[1]), table,
+                    lens, [1, 1], True, 0.05)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** 60])
+def test_queries_far_from_one(size):
+    """bf16 rows beyond f16's range: scores are the same as for rows of size one
+    with the scale taken over by the softmax scale."""
+    g = torch.Generator().manual_seed(7)
+    codes, scales, table = ref.make_cache(10, 1, 64, 128, 1, 5, g, [300])
+    cache = device_cache(codes, scales, table)
+    q = torch.randn(1, 4, 1, 128, generator=g).bfloat16()
+    a = binding.forward_cache(dev(q), cache, ints([300]), True, 0.1)
+    b = binding.forward_cache(dev((q.float() * size).bfloat16()), cache, ints([300]), True,
+                              0.1 / size)
+    binding.device_status()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_a_long_cache_and_byte_offsets_past_32_bits():
+    """300,000 tokens of one sequence, at the far end of a pool of more than
+    2^32 bytes; sampled against equal codes: the softmax of equal scores."""
+    page, d, Hkv = 256, 128, 8
+    pages = (1 << 32) // (Hkv * page * d) + 1300
+    k = torch.zeros(pages, Hkv, page, d, dtype=torch.uint8, device=DEV)
+    v = torch.zeros_like(k)
+    ks, vs = torch.ones(pages, Hkv, device=DEV), torch.ones(pages, Hkv, device=DEV)
+    n = 300000
+    need = -(-n // page)
+    table = torch.arange(pages - need, pages, dtype=torch.int32, device=DEV)[None]
+    v[pages - need:] = 0x38                       # 1.0
+    v[pages - 1, :, (n - 1) % page] = 0x40        # 2.0 at the last token
+    v[pages - 1, :, (n - 1) % page + 1:] = 0x7F
+    cache = binding.Cache(k, v, ks, vs, table)
+    q = torch.randn(1, 16, 1, d, device=DEV).bfloat16()
+    o, lse = binding.forward_cache(q, cache, ints([n]), True, 1.0)
+    binding.device_status()
+    assert float((lse - math.log(n)).abs().max()) < 1e-4
+    assert float((o.float() - 1).abs().max()) <= 2.0 ** -8 and float(o.float().min()) >= 1.0
+    x = torch.randn(1, Hkv, 1, d, device=DEV).bfloat16()
+    binding.cache_append(cache, None, x, x, ints([n + 1]))
+    binding.device_status()
+    got = ref.codes_to_values(cache.tensors[1][pages - 1, :, n % page]) \
+        * vs[pages - 1].cpu().double()[:, None]
+    want = x[0, :, 0].cpu().double()
+    assert bool((vs[pages - 1] == 1).all())       # the page's scale was larger than the token needs
+    assert ((got - want).abs() <= torch.maximum(want.abs() * 2.0 ** -4, torch.tensor(2.0 ** -10))).all()
+
+
+def test_the_same_bits_every_time_and_any_workspace():
+    g = torch.Generator().manual_seed(8)
+    lens = [3000, 1, 700, 2049]
+    codes, scales, table = ref.make_cache(400, 4, 16, 128, 4, 190, g, lens)
+    cache = device_cache(codes, scales, table)
+    q = torch.randn(4, 8, 1, 128, generator=g).bfloat16().to(DEV)
+    need = binding.fwd_cache_workspace_size(4, 8, 4, 1, 128)
+    first = None
+    for fill in (0, 0xFF, 0x3F):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device=DEV)
+        out = binding.forward_cache(q, cache, ints(lens), True, 0.09, workspace=ws)
+        if first is None:
+            first = out
+        assert torch.equal(out[0], first[0]) and torch.equal(out[1], first[1])
+    # a sequence alone gives what it gives in a batch, up to where its keys are split
+    alone = binding.Cache(*cache.tensors[:4], cache.tensors[4][3:4].contiguous())
+    o, lse = binding.forward_cache(q[3:4], alone, ints(lens[3:]), True, 0.09)
+    assert float((lse - first[1][3:4]).abs().max()) < 1e-5
+    assert float((o.float() - first[0][3:4].float()).abs().max()) <= 2.0 ** -8 * float(o.float().abs().max())
+    binding.device_status()
+
+
+def test_ranges_out_of_bounds_are_reported():
+    """Lengths and pages outside their range are skipped on the device and
+    reported; the other sequences are served."""
+    g = torch.Generator().manual_seed(9)
+    lens = [40, 40, 40]
+    codes, scales, table = ref.make_cache(12, 2, 16, 64, 3, 3, g, lens)
+    good = device_cache(codes, scales, table)
+    q = torch.randn(3, 4, 1, 64, generator=g).half().to(DEV)
+    want = binding.forward_cache(q, good, ints(lens), True, 0.1)
+    binding.device_status()
+    for bad in (49, -1):
+        o, lse = binding.forward_cache(q, good, ints([40, bad, 40]), True, 0.1)
+        with pytest.raises(binding.FaError) as e:
+            binding.device_status()
+        assert e.value.status == binding.FA_ERR_CACHE
+        assert torch.equal(o[[0, 2]], want[0][[0, 2]])
+        assert (o[1] == 0).all() and torch.isneginf(lse[1]).all()
+    for page in (12, -1):
+        table2 = table.clone()
+        table2[1, 1] = page
+        cache = device_cache(codes, scales, table2)
+        o, _ = binding.forward_cache(q, cache, ints(lens), True, 0.1)
+        with pytest.raises(binding.FaError):
+            binding.device_status()
+        assert torch.equal(o[[0, 2]], want[0][[0, 2]])
+        kept = [t.clone() for t in cache.tensors]
+        x = torch.randn(3, 2, 9, 64, generator=g).half().to(DEV)
+        binding.cache_append(cache, None, x, x, ints([8, 25, 9]))   # 8 < 9 new; rows 16.. on the bad page
+        with pytest.raises(binding.FaError) as e:
+            binding.device_status()
+        assert e.value.status == binding.FA_ERR_CACHE
+        touched = (cache.tensors[1].view(torch.uint8) != kept[1].view(torch.uint8)).any(-1).any(-1).any(-1)
+        assert set(touched.nonzero()[:, 0].tolist()) == {int(table[2][0])}
+    binding.device_status()
+
+
+# ------------------------------------------------------------------ together
+@pytest.mark.parametrize("d,page,H,Hkv", [(64, 16, 4, 2), (128, 64, 8, 2), (256, 32, 2, 1)])
+def test_a_server_s_run(d, page, H, Hkv):
+    """Prompts of unlike length, then single tokens, in one captured graph whose
+    lengths grow on the device; against fp64 over all tokens so far."""
+    g = torch.Generator().manual_seed(10)
+    B, N, scale = 3, 45, 1.0 / math.sqrt(d)
+    new = [45, 17, 1]
+    width = -(-(N + 8) // page)
+    codes, scales, table = ref.make_cache(B * width + 1, Hkv, page, d, B, width, g)
+    cache = device_cache(codes, scales, table)
+    freq = [10000.0 ** (-i / (d // 2)) for i in range(d // 2)]
+    rope = binding.Rope(freq)
+
+    def tokens(n):
+        return [torch.randn(B, n, h, d, generator=g).bfloat16().transpose(1, 2) for h in (H, Hkv, Hkv)]
+
+    q, k, v = tokens(N)
+    lens = ints(new)
+    qr = binding.cache_append(cache, dev(q), dev(k), dev(v), lens, new_lens=ints(new), rope=rope)
+    o, lse = binding.forward_cache(qr, cache, lens, True, scale, new_lens=ints(new))
+    binding.device_status()
+
+    def held():
+        return [ref.Paged(cache.tensors[i], cache.tensors[2 + i]) for i in (0, 1)]
+
+    check_attention(o, lse, qr.cpu(), *held(), table, new, new, True, scale)
+    # single tokens, captured once
+    q1, k1, v1 = (dev(x).contiguous() for x in tokens(1))
+    ws = torch.empty(binding.fwd_cache_workspace_size(B, H, Hkv, 1, d), dtype=torch.uint8, device=DEV)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        lens.add_(1)
+        qg = binding.cache_append(cache, q1, k1, v1, lens, rope=rope)
+        og, lg = binding.forward_cache(qg, cache, lens, True, scale, workspace=ws)
+    for step in range(6):
+        nq, nk, nv = tokens(1)
+        q1.copy_(nq), k1.copy_(nk), v1.copy_(nv)
+        graph.replay()
+        binding.device_status()
+        now = [n + step + 1 for n in new]
+        assert lens.tolist() == now
+        check_attention(og, lg, qg.cpu(), *held(), table, now, [1] * B, True, scale)
+        # the key that was stored is the rotated one, to half a step of e4m3
+        want = ref.rotate(nk, torch.tensor(now)[None, :, None] - 1, freq, [0] * len(freq), False)
+        K = held()[0]
+        for b in range(B):
+            for h in range(Hkv):
+                got = K.rows(table[b], now[b], h)[-1]
+                s = float(K.scales[int(table[b][(now[b] - 1) // page]), h])
+                lim = want[b, h, 0].abs() * 2.0 ** -4 + s * 2.0 ** -10 + 1e-5
+                assert ((got - want[b, h, 0]).abs() <= lim).all()

@@ -1,0 +1,355 @@
+// The work of fa_fwd_cache, shared by its two kernels: lengths read on the
+// device, the flat order of the steps and its cut into equal shares, and the
+// kernel that joins the pieces of units that lie in several shares.
+//
+// A unit is a tile of RT query rows of one key/value head of one sequence, a
+// step STEP of its keys.  Units follow one another in the order (sequence, row
+// tile, head); CTA c takes steps [c * share, (c + 1) * share) of them all, so
+// that every CTA has the same number of steps whatever the lengths are.  A
+// CTA's first unit may have begun in the share before and its last may go on
+// in the next: it writes those as pieces (slot 0: the piece does not begin
+// its unit, slot 1: it does), the units inside it as results.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "fa_internal.h"
+#include "sm103_ptx.cuh"
+
+namespace fa {
+
+struct SeqParams {
+  const int *seq_lens, *new_lens;
+  int B, G, Nq, causal;
+  long long capacity;   // tokens that a table row can map
+  unsigned int* err;
+};
+
+struct FwdCacheParams {
+  SeqParams seq;
+  const uint16_t* q;
+  uint16_t* o;
+  float* lse;
+  Strides qs, os;
+  const unsigned char *k, *v;
+  Strides ks, vs;         // bytes
+  const float *k_scale, *v_scale;
+  const int* table;
+  int width, pages, page_log2;
+  int H, Hkv, rows;       // rows = G * Nq of a unit's key/value head
+  int row_tiles;
+  int bf16;
+  float scale_log2;
+  float* part_o;          // [CTA][2][RT][D]: O of a piece, not divided by its sum
+  float2* part_ml;        // [CTA][2][RT]: its running maximum (log2 units) and sum
+  int ctas;
+};
+
+constexpr float kNoMax = -1e30f;    // running maximum before the first key
+constexpr float kGrow = 8.f;        // the maximum moves when it grows by more (log2 units)
+constexpr float kLogE2 = 0.6931471805599453f;
+
+// Tokens of sequence b and the query rows among them; both 0 when a length is
+// out of range (*bad is set).
+struct Sequence {
+  int len, n;
+};
+__device__ __forceinline__ Sequence sequence_at(const SeqParams& p, int b, bool* bad) {
+  Sequence s;
+  s.len = p.seq_lens[b];
+  s.n = p.new_lens != nullptr ? p.new_lens[b] : p.Nq;
+  if (s.len < 0 || s.len > p.capacity || s.n < 0 || s.n > p.Nq) {
+    *bad = true;
+    s.len = s.n = 0;
+  }
+  return s;
+}
+
+// Rows of a key/value head are taken token by token, row r = i * G + g being
+// query head g of token i, so that a tile of consecutive rows spans few
+// tokens and a causal tile ends early.  `lim`: the keys that any row of the
+// tile [r0, r1) sees; `full`: the keys that every one of its live rows sees.
+struct TileLimits {
+  int lim, full;
+};
+__device__ __forceinline__ TileLimits tile_limits(const SeqParams& p, const Sequence& s, int r0,
+                                                  int r1) {
+  const int i0 = r0 / p.G, i1 = min(s.n - 1, (r1 - 1) / p.G);
+  TileLimits t;
+  if (i0 > i1) {
+    t.lim = t.full = 0;
+  } else if (p.causal) {
+    t.lim = max(0, s.len - s.n + i1 + 1);
+    t.full = max(0, s.len - s.n + i0 + 1);
+  } else {
+    t.lim = t.full = s.len;
+  }
+  return t;
+}
+// The keys that row r sees.
+__device__ __forceinline__ int row_limit(const SeqParams& p, const Sequence& s, int r) {
+  return p.causal ? min(s.len, s.len - s.n + r / p.G + 1) : s.len;
+}
+
+__device__ __forceinline__ uint32_t widen(uint32_t two) {   // two e4m3 codes -> f16x2
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
+  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+}
+
+// Bytes that are NaN codes (0x7f, 0xff), as a byte mask.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+}
+
+// The power of two that a bf16 row with largest magnitude amax is divided by
+// to become f16 (1 for rows of zeros, NaN or infinities): `up` it, `down` its
+// reciprocal.
+__device__ __forceinline__ void row_power(float amax, float* up, float* down) {
+  const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23), 1), 253);
+  const bool plain = !(amax > 0.f) || !(amax < __uint_as_float(0x7f800000u));
+  *down = plain ? 1.f : __uint_as_float(static_cast<uint32_t>(254 - e) << 23);   // 2^(127 - e)
+  *up = plain ? 1.f : __uint_as_float(static_cast<uint32_t>(e) << 23);
+}
+
+template <int STEP>
+__device__ __forceinline__ int steps_of(int lim) {
+  return (lim + STEP - 1) / STEP;
+}
+
+// Limits of entry e = b * row_tiles + row tile.
+template <int RT>
+__device__ __forceinline__ TileLimits limits_of(const FwdCacheParams& p, int e, Sequence* s,
+                                                bool* bad) {
+  const int b = e / p.row_tiles, rt = e % p.row_tiles;
+  *s = sequence_at(p.seq, b, bad);
+  return tile_limits(p.seq, *s, rt * RT, min(p.rows, (rt + 1) * RT));
+}
+
+// Sum over the block's threads (every thread gets it); red: a value a warp.
+template <int THREADS>
+__device__ __forceinline__ long long block_sum(long long x, long long* red) {
+  #pragma unroll
+  for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = 0;
+  #pragma unroll
+  for (int i = 0; i < THREADS / 32; ++i) x += red[i];
+  return x;
+}
+
+// All steps of the call, one key/value head counted.
+template <int RT, int STEP, int THREADS>
+__device__ long long total_steps(const FwdCacheParams& p, long long* red, bool* bad) {
+  long long mine = 0;
+  const int entries = p.seq.B * p.row_tiles;
+  for (int e = threadIdx.x; e < entries; e += THREADS) {
+    Sequence s;
+    mine += steps_of<STEP>(limits_of<RT>(p, e, &s, bad).lim);
+  }
+  return block_sum<THREADS>(mine, red);
+}
+
+// The entry in which step `at` (of all entries, one head) lies: found->x the
+// entry, found->y the steps before it.
+template <int RT, int STEP, int THREADS>
+__device__ void find_entry(const FwdCacheParams& p, long long at, long long* red,
+                           longlong2* found) {
+  const int entries = p.seq.B * p.row_tiles, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long before = 0;
+  for (int e0 = 0; e0 < entries; e0 += THREADS) {
+    const int e = e0 + threadIdx.x;
+    Sequence s;
+    bool bad = false;
+    const long long mine = e < entries ? steps_of<STEP>(limits_of<RT>(p, e, &s, &bad).lim) : 0;
+    long long upto = mine;
+    #pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, upto, m);
+      if (lane >= m) upto += x;
+    }
+    __syncthreads();
+    if (lane == 31) red[warp] = upto;
+    __syncthreads();
+    long long all = 0;
+    #pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+      if (i < warp) upto += red[i];
+      all += red[i];
+    }
+    if (mine > 0 && before + upto - mine <= at && at < before + upto) {
+      found->x = e;
+      found->y = before + upto - mine;
+    }
+    before += all;
+    if (at < before) break;
+  }
+  __syncthreads();
+}
+
+// Where a walk over the steps of a share stands.
+template <int RT, int STEP>
+struct Walk {
+  int e, h, step, steps;   // entry, key/value head, step and steps of the unit
+  int lim, full;
+  Sequence seq;
+  __device__ __forceinline__ void enter(const FwdCacheParams& p) {
+    bool bad = false;
+    const TileLimits t = limits_of<RT>(p, e, &seq, &bad);
+    lim = t.lim;
+    full = t.full;
+    steps = steps_of<STEP>(lim);
+  }
+  // found: of find_entry(lo / Hkv); entry e's Hkv units stand one after
+  // another from step found->y * Hkv on
+  __device__ __forceinline__ void start(const FwdCacheParams& p, const longlong2* found,
+                                        long long lo) {
+    e = static_cast<int>(found->x);
+    enter(p);
+    const long long rest = lo - found->y * p.Hkv;
+    h = static_cast<int>(rest / steps);
+    step = static_cast<int>(rest % steps);
+  }
+  __device__ __forceinline__ void next_unit(const FwdCacheParams& p) {
+    step = 0;
+    if (++h == p.Hkv) {
+      h = 0;
+      const int entries = p.seq.B * p.row_tiles;
+      do {
+        if (++e >= entries) { steps = lim = full = 0; return; }
+        enter(p);
+      } while (steps == 0);
+    }
+  }
+};
+
+// Joins the pieces of units that lie in several shares, and writes the units
+// that see no key.  Block (c, y) looks for the unit that begins in share c and
+// goes on behind it; its warps take a row each: the pieces' weights first,
+// then their O, four loads in flight.
+constexpr int kMergeThreads = 128;
+template <int D, int RT, int STEP>
+__global__ void __launch_bounds__(kMergeThreads)
+cache_merge_kernel(const __grid_constant__ FwdCacheParams p) {
+  constexpr int kVec = D / 32, kWarps = kMergeThreads / 32;
+  __shared__ long long red[kWarps];
+  __shared__ longlong2 found;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row_first = blockIdx.y * kWarps + warp, row_step = gridDim.y * kWarps;
+  bool bad = false;
+  const long long total = total_steps<RT, STEP, kMergeThreads>(p, red, &bad) * p.Hkv;
+  const long long share = (total + p.ctas - 1) / p.ctas;
+  const int c0 = blockIdx.x;
+  const long long end = (c0 + 1) * share;
+  bool joins = end < total && share > 0;      // (share > 0 wherever a step is)
+  Walk<RT, STEP> at;
+  int c1 = 0;
+  if (joins) {
+    find_entry<RT, STEP, kMergeThreads>(p, (end - 1) / p.Hkv, red, &found);
+    at.start(p, &found, end - 1);
+    const long long first = end - 1 - at.step, last = first + at.steps - 1;
+    joins = last >= end && first >= end - share;
+    c1 = static_cast<int>(last / share);
+  }
+  grid_dependency_wait();   // (every CTA: this grid's end is to imply the other's)
+  if (joins) {
+    const int row0 = at.e % p.row_tiles * RT, b = at.e / p.row_tiles;
+    for (int rr = row_first; rr < RT && row0 + rr < p.rows; rr += row_step) {
+      const int r = row0 + rr, i = r / p.seq.G, head = at.h * p.seq.G + r % p.seq.G;
+      float top = kNoMax, sum = 0.f;
+      float acc[kVec];
+      #pragma unroll
+      for (int k = 0; k < kVec; ++k) acc[k] = 0.f;
+      for (int c = c0 + lane; c <= c1; c += 32)
+        top = fmaxf(top, p.part_ml[(2ll * c + (c == c0)) * RT + rr].x);
+      #pragma unroll
+      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      for (int cb = c0; cb <= c1; cb += 32) {
+        float2 ml = make_float2(kNoMax, 0.f);
+        const int mine = cb + lane;
+        if (mine <= c1) ml = p.part_ml[(2ll * mine + (mine == c0)) * RT + rr];
+        const float w = ex2_approx(ml.x - top);
+        float part = ml.y == 0.f ? 0.f : ml.y * w;
+        #pragma unroll
+        for (int x = 16; x > 0; x >>= 1) part += __shfl_xor_sync(0xffffffffu, part, x);
+        sum += part;
+        // a piece without keys for the row has left its O unwritten
+        const uint32_t has = __ballot_sync(0xffffffffu, ml.y != 0.f);
+        const int n = min(32, c1 - cb + 1);
+        for (int k0 = 0; k0 < n; k0 += 4) {
+          float x[4][kVec], wk[4];
+          #pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            wk[k] = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+            const int c = cb + k0 + k;
+            #pragma unroll
+            for (int v = 0; v < kVec; ++v) x[k][v] = 0.f;
+            if (k0 + k < n && (has >> (k0 + k) & 1)) {
+              const float* src = p.part_o + ((2ll * c + (c == c0)) * RT + rr) * D + lane * kVec;
+              #pragma unroll
+              for (int v = 0; v < kVec; v += 2) {
+                const float2 y = *reinterpret_cast<const float2*>(src + v);
+                x[k][v] = y.x;
+                x[k][v + 1] = y.y;
+              }
+            }
+          }
+          #pragma unroll
+          for (int k = 0; k < 4; ++k)
+            #pragma unroll
+            for (int v = 0; v < kVec; ++v) acc[v] = fmaf(x[k][v], wk[k], acc[v]);
+        }
+      }
+      if (i >= at.seq.n) sum = 0.f;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + b * p.os.b + head * p.os.h + i * p.os.n + lane * kVec);
+      #pragma unroll
+      for (int v = 0; v < kVec; v += 2)
+        dst[v / 2] = sum == 0.f ? 0u
+                     : p.bf16 ? pack2<true>(acc[v] * inv, acc[v + 1] * inv)
+                              : pack2<false>(acc[v] * inv, acc[v + 1] * inv);
+      if (lane == 0)
+        p.lse[(static_cast<long long>(b) * p.H + head) * p.seq.Nq + i] =
+            sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLogE2;
+    }
+  }
+  for (int e = blockIdx.x; e < p.seq.B * p.row_tiles; e += gridDim.x) {
+    Sequence seq;
+    if (limits_of<RT>(p, e, &seq, &bad).lim > 0) continue;
+    const int row0 = e % p.row_tiles * RT, b = e / p.row_tiles;
+    for (int h = 0; h < p.Hkv; ++h)
+      for (int rr = row_first; rr < RT && row0 + rr < p.rows; rr += row_step) {
+        const int r = row0 + rr, i = r / p.seq.G, head = h * p.seq.G + r % p.seq.G;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + b * p.os.b + head * p.os.h + i * p.os.n + lane * kVec);
+        #pragma unroll
+        for (int v = 0; v < kVec; v += 2) dst[v / 2] = 0u;
+        if (lane == 0) p.lse[(static_cast<long long>(b) * p.H + head) * p.seq.Nq + i] = -INFINITY;
+      }
+  }
+}
+
+// Launches the join behind the attention kernel, as its programmatic
+// dependent.
+template <int D, int RT, int STEP>
+cudaError_t launch_cache_merge(const FwdCacheParams& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.ctas), RT > 32 ? RT / 32 : 1, 1);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_merge_kernel<D, RT, STEP>, p);
+}
+
+// The tcgen05 kernel, for many query rows (fa_cache_prefill.cu): rows of a
+// unit, and its launch.
+int cache_prefill_rows(int d);
+cudaError_t launch_cache_prefill(const Cache& cache, FwdCacheParams& p, int sms,
+                                 cudaStream_t stream);
+
+}  // namespace fa

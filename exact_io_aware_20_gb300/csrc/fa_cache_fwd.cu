@@ -30,10 +30,7 @@
 #include <algorithm>
 #include <atomic>
 
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-
-#include "cache_seq.cuh"
+#include "cache_work.cuh"
 
 namespace fa {
 namespace {
@@ -41,9 +38,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;
-constexpr float kNoMax = -1e30f;    // running maximum before the first key
-constexpr float kGrow = 8.f;        // the maximum moves when it grows by more (log2 units)
-constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D>
 struct Tile {
@@ -54,29 +48,6 @@ struct Tile {
   static constexpr int kHalves = D / kPitch;             // 128-column parts, one after another
   static constexpr int kSub = kKeys / 16;                // pages that a tile can touch
 };
-
-struct FwdCacheParams {
-  SeqParams seq;
-  const uint16_t* q;
-  uint16_t* o;
-  float* lse;
-  Strides qs, os;
-  const float *k_scale, *v_scale;
-  const int* table;
-  int width, pages, page_log2;
-  int H, Hkv, rows;       // rows = G * Nq of a unit's key/value head
-  int row_tiles;
-  int bf16;
-  float scale_log2;
-  float* part_o;          // [CTA][2][row tile][D]
-  float2* part_ml;        // [CTA][2][row tile]
-  int ctas;
-};
-
-__device__ __forceinline__ uint32_t widen(uint32_t two) {   // two e4m3 codes -> f16x2
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
-}
 
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                     uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -91,11 +62,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-
-// Bytes that are NaN codes (0x7f, 0xff), as a byte mask.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-  return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
 }
 
 // The key of a 16-key fragment that row g (of 8) of the fragment's halves
@@ -114,109 +80,6 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   if constexpr (D == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
   else return r * 128 + ((c ^ (r & 7)) << 4);
 }
-
-// Steps of a tile of rows.
-template <int D>
-__device__ __forceinline__ int steps_of(int lim) {
-  return (lim + Tile<D>::kStep - 1) / Tile<D>::kStep;
-}
-
-// Limits of entry e = b * row_tiles + row tile.
-template <int NT>
-__device__ __forceinline__ TileLimits limits_of(const FwdCacheParams& p, int e, Sequence* s,
-                                                bool* bad) {
-  const int b = e / p.row_tiles, rt = e % p.row_tiles;
-  *s = sequence_at(p.seq, b, bad);
-  return tile_limits(p.seq, *s, rt * 8 * NT, min(p.rows, (rt + 1) * 8 * NT));
-}
-
-// Sum over the block's threads (every thread gets it); red: kWarps values.
-__device__ __forceinline__ long long block_sum(long long x, long long* red) {
-  #pragma unroll
-  for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = 0;
-  #pragma unroll
-  for (int i = 0; i < kWarps; ++i) x += red[i];
-  return x;
-}
-
-// All steps of the call, the key/value heads of an entry counted together.
-template <int D, int NT>
-__device__ long long total_steps(const FwdCacheParams& p, long long* red, bool* bad) {
-  long long mine = 0;
-  const int entries = p.seq.B * p.row_tiles;
-  for (int e = threadIdx.x; e < entries; e += kThreads) {
-    Sequence s;
-    mine += steps_of<D>(limits_of<NT>(p, e, &s, bad).lim);
-  }
-  return block_sum(mine, red);
-}
-
-// The entry in which step `at` (of all entries, one head) lies: found->x the
-// entry, found->y the steps before it.
-template <int D, int NT>
-__device__ void find_entry(const FwdCacheParams& p, long long at, long long* red,
-                           longlong2* found) {
-  const int entries = p.seq.B * p.row_tiles, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long before = 0;
-  for (int e0 = 0; e0 < entries; e0 += kThreads) {
-    const int e = e0 + threadIdx.x;
-    Sequence s;
-    bool bad = false;
-    const long long mine = e < entries ? steps_of<D>(limits_of<NT>(p, e, &s, &bad).lim) : 0;
-    long long upto = mine;
-    #pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, upto, m);
-      if (lane >= m) upto += x;
-    }
-    __syncthreads();
-    if (lane == 31) red[warp] = upto;
-    __syncthreads();
-    long long all = 0;
-    #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) upto += red[i];
-      all += red[i];
-    }
-    if (mine > 0 && before + upto - mine <= at && at < before + upto) {
-      found->x = e;
-      found->y = before + upto - mine;
-    }
-    before += all;
-    if (at < before) break;
-  }
-  __syncthreads();
-}
-
-// Where a walk over the steps of a share stands.
-template <int D, int NT>
-struct Walk {
-  int e, h, step, steps;   // entry, key/value head, step and steps of the unit
-  int lim, full;
-  Sequence seq;
-  __device__ __forceinline__ void enter(const FwdCacheParams& p) {
-    bool bad = false;
-    const TileLimits t = limits_of<NT>(p, e, &seq, &bad);
-    lim = t.lim;
-    full = t.full;
-    steps = steps_of<D>(lim);
-  }
-  __device__ __forceinline__ void next_unit(const FwdCacheParams& p) {
-    step = 0;
-    if (++h == p.Hkv) {
-      h = 0;
-      const int entries = p.seq.B * p.row_tiles;
-      do {
-        if (++e >= entries) { steps = lim = full = 0; return; }
-        enter(p);
-      } while (steps == 0);
-    }
-  }
-};
 
 template <int D, int NT>
 struct Smem {
@@ -242,6 +105,7 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                  const __grid_constant__ FwdCacheParams p) {
   using T = Tile<D>;
   using S = Smem<D, NT>;
+  constexpr int RT = 8 * NT;                   // rows of a unit
   constexpr int kMT = D / 16;                  // 16-column fragments of O^T
   constexpr int kChunks = D / 64;              // 64-column parts of a row
   constexpr bool kQRegs = kChunks * 8 * NT <= 32;
@@ -270,29 +134,21 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     tma_prefetch_desc(&tm_v);
   }
   bool bad = false;
-  const long long total = total_steps<D, NT>(p, red, &bad) * p.Hkv;
+  const long long total = total_steps<RT, T::kStep, kThreads>(p, red, &bad) * p.Hkv;
   if (bad && blockIdx.x == 0) atomicOr(p.seq.err, kErrCache);
   const long long share = (total + p.ctas - 1) / p.ctas;
   const long long lo = blockIdx.x * share, hi = min(total, lo + share);
   if (lo >= hi) return;
-  find_entry<D, NT>(p, lo / p.Hkv, red, found);
-  // found holds the entry by its steps of one head: entry e's Hkv units stand
-  // one after another from step found->y * Hkv on
-  Walk<D, NT> at;
-  at.e = static_cast<int>(found->x);
-  {
-    at.enter(p);
-    const long long rest = lo - found->y * p.Hkv;
-    at.h = static_cast<int>(rest / at.steps);
-    at.step = static_cast<int>(rest % at.steps);
-  }
+  find_entry<RT, T::kStep, kThreads>(p, lo / p.Hkv, red, found);
+  Walk<RT, T::kStep> at;
+  at.start(p, found, lo);
   __syncthreads();   // found is read; its place is the join buffer's
 
   // ---------------------------------------------------------------- loads
   const int sub_log2 = min(p.page_log2, 31 - __clz(T::kKeys));   // keys of a box
   const int subs = T::kKeys >> sub_log2;                         // boxes (pages) of a tile
   const uint32_t box_bytes = static_cast<uint32_t>(T::kPitch) << sub_log2;
-  Walk<D, NT> f = at;
+  Walk<RT, T::kStep> f = at;
   long long f_left = hi - lo;
   int fetched = 0, done = 0;
   int tb_first = 0, tb_steps = 0;      // steps of f's unit that the table registers cover
@@ -398,10 +254,9 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           }
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23), 1), 253);
-        const bool plain = !(amax > 0.f) || !(amax < __uint_as_float(0x7f800000u));
-        down = plain ? 1.f : __uint_as_float(static_cast<uint32_t>(254 - e) << 23);   // 2^(127 - e)
-        if (t == 0) q_pow[nt * 8 + g] = plain ? 1.f : __uint_as_float(static_cast<uint32_t>(e) << 23);
+        float up;
+        row_power(amax, &up, &down);
+        if (t == 0) q_pow[nt * 8 + g] = up;
       } else if (t == 0) {
         q_pow[nt * 8 + g] = 1.f;
       }
@@ -491,9 +346,7 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             if (partial) {
               const int r = row0 + nt * 8 + 2 * t + (k & 1);
               const int key = k0 + kr + (k >> 1) * 8;
-              const int sees = p.seq.causal ? min(at.seq.len, at.seq.len - at.seq.n + r / p.seq.G + 1)
-                                            : at.seq.len;
-              if (key >= sees) s[nt][k] = -INFINITY;
+              if (key >= row_limit(p.seq, at.seq, r)) s[nt][k] = -INFINITY;
             }
             grow |= s[nt][k] > m[nt][k & 1] + kGrow;
           }
@@ -715,7 +568,7 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
               }
               if (g == 0)
                 p.lse[(static_cast<long long>(b) * p.H + head) * p.seq.Nq + i] =
-                    sum == 0.f ? -INFINITY : (m[nt][c] + log2f(sum)) * kLn2;
+                    sum == 0.f ? -INFINITY : (m[nt][c] + log2f(sum)) * kLogE2;
             } else {
               #pragma unroll
               for (int half = 0; half < T::kHalves; ++half) {
@@ -738,96 +591,6 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     // the copies still in flight, before their shared memory goes away
     for (int i = done; i < fetched; ++i) drain_wait(bars + 8 * (i % kStages), (i / kStages) & 1);
     if (lane == 0 && *abort == 2) atomicOr(p.seq.err, kErrTimeout);
-  }
-}
-
-// Joins the pieces of the units that lie in several shares, and writes the
-// units that see no key.  One CTA a unit, a warp a row; the pieces' weights
-// first, then their O, four rows of loads in flight.
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads)
-cache_merge_kernel(const __grid_constant__ FwdCacheParams p) {
-  constexpr int kVec = D / 32;
-  __shared__ long long red[kWarps];
-  const int unit = blockIdx.x, e = unit / p.Hkv, h = unit % p.Hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  bool bad = false;
-  const long long total = total_steps<D, NT>(p, red, &bad) * p.Hkv;
-  Sequence seq;
-  const TileLimits lim = limits_of<NT>(p, e, &seq, &bad);
-  const int steps = steps_of<D>(lim.lim);
-  // the steps of the entries before this one
-  long long before = 0;
-  for (int x = threadIdx.x; x < e; x += kThreads) {
-    Sequence s;
-    before += steps_of<D>(limits_of<NT>(p, x, &s, &bad).lim);
-  }
-  before = block_sum(before, red);
-  const long long share = (total + p.ctas - 1) / p.ctas;
-  const long long first = before * p.Hkv + static_cast<long long>(h) * steps;
-  const int c0 = steps > 0 ? static_cast<int>(first / share) : 0;
-  const int c1 = steps > 0 ? static_cast<int>((first + steps - 1) / share) : 0;
-  const int row0 = e % p.row_tiles * 8 * NT, b = e / p.row_tiles;
-  grid_dependency_wait();   // (every CTA: this grid's end is to imply the other's)
-  if (steps > 0 && c0 == c1) return;      // whole: written by its CTA
-  for (int rr = warp; rr < 8 * NT && row0 + rr < p.rows; rr += kWarps) {
-    const int r = row0 + rr, i = r / p.seq.G, head = h * p.seq.G + r % p.seq.G;
-    float top = kNoMax, sum = 0.f;
-    float acc[kVec];
-    #pragma unroll
-    for (int k = 0; k < kVec; ++k) acc[k] = 0.f;
-    if (steps > 0) {
-      for (int c = c0 + lane; c <= c1; c += 32)
-        top = fmaxf(top, p.part_ml[(2ll * c + (c == c0)) * 8 * NT + rr].x);
-      #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      for (int cb = c0; cb <= c1; cb += 32) {
-        float2 ml = make_float2(kNoMax, 0.f);
-        const int mine = cb + lane;
-        if (mine <= c1) ml = p.part_ml[(2ll * mine + (mine == c0)) * 8 * NT + rr];
-        const float w = mine <= c1 ? ex2_approx(ml.x - top) : 0.f;
-        float part = ml.y * w;
-        #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) part += __shfl_xor_sync(0xffffffffu, part, x);
-        sum += part;
-        const int n = min(32, c1 - cb + 1);
-        for (int k0 = 0; k0 < n; k0 += 4) {
-          float x[4][kVec], wk[4];
-          #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            wk[k] = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
-            const int c = cb + k0 + k;
-            #pragma unroll
-            for (int v = 0; v < kVec; ++v) x[k][v] = 0.f;
-            if (k0 + k < n) {
-              const float* src = p.part_o + ((2ll * c + (c == c0)) * 8 * NT + rr) * D + lane * kVec;
-              #pragma unroll
-              for (int v = 0; v < kVec; v += 2) {
-                const float2 y = *reinterpret_cast<const float2*>(src + v);
-                x[k][v] = y.x;
-                x[k][v + 1] = y.y;
-              }
-            }
-          }
-          #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k0 + k < n)
-              #pragma unroll
-              for (int v = 0; v < kVec; ++v) acc[v] = fmaf(x[k][v], wk[k], acc[v]);
-        }
-      }
-    }
-    if (i >= seq.n) sum = 0.f;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + b * p.os.b + head * p.os.h + i * p.os.n + lane * kVec);
-    #pragma unroll
-    for (int v = 0; v < kVec; v += 2)
-      dst[v / 2] = sum == 0.f ? 0u
-                   : p.bf16 ? pack2<true>(acc[v] * inv, acc[v + 1] * inv)
-                            : pack2<false>(acc[v] * inv, acc[v + 1] * inv);
-    if (lane == 0)
-      p.lse[(static_cast<long long>(b) * p.H + head) * p.seq.Nq + i] =
-          sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
   }
 }
 
@@ -875,24 +638,32 @@ cudaError_t launch(const Cache& cache, FwdCacheParams& p, int sms, cudaStream_t 
     return e;
   cache_fwd_kernel<D, NT><<<p.ctas, kThreads, Smem<D, NT>::kAlloc, stream>>>(tk, tv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.seq.B) * p.row_tiles * p.Hkv);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_merge_kernel<D, NT>, p);
+  return launch_cache_merge<D, 8 * NT, Tile<D>::kStep>(p, stream);
 }
 
 }  // namespace
 
-// Two pieces of a row tile for each of at most two CTAs an SM.
+namespace {
+
+// Whether the tcgen05 kernel takes the call: from one row more than a tile of
+// this file's kernel holds.
+bool many_rows(long long rows, int d) { return rows > (d == 64 ? 64 : d == 128 ? 32 : 16); }
+
+// Rows of a unit, and CTAs at most.
+void unit_shape(long long rows, int d, int sms, size_t* unit_rows, size_t* ctas) {
+  const bool many = many_rows(rows, d);
+  *unit_rows = many ? cache_prefill_rows(d)
+                    : 8 * row_fragments(static_cast<int>(std::min(rows, 1ll << 20)), d);
+  *ctas = many ? sms : 2ull * sms;
+}
+
+}  // namespace
+
+// Two pieces of a unit's rows for each CTA.
 size_t cache_fwd_workspace_bytes(int, int H, int Hkv, int Nq, int d, int sms) {
-  const size_t rows = 8ull * row_fragments(static_cast<int>(std::min(1ll * H / Hkv * Nq, 1ll << 20)), d);
-  return 4ull * sms * rows * (d * sizeof(float) + sizeof(float2));
+  size_t rows, ctas;
+  unit_shape(1ll * H / Hkv * Nq, d, sms, &rows, &ctas);
+  return 2 * ctas * rows * (d * sizeof(float) + sizeof(float2));
 }
 
 cudaError_t launch_cache_fwd(const Cache& cache, const CacheFwdCall& c, int sms,
@@ -916,10 +687,17 @@ cudaError_t launch_cache_fwd(const Cache& cache, const CacheFwdCall& c, int sms,
   p.rows = p.seq.G * c.Nq;
   p.bf16 = c.bf16;
   p.scale_log2 = c.scale * 1.4426950408889634f;
-  const int nt = row_fragments(p.rows, cache.d);
-  p.row_tiles = (p.rows + 8 * nt - 1) / (8 * nt);
+  p.k = cache.k;
+  p.v = cache.v;
+  p.ks = cache.ks;
+  p.vs = cache.vs;
+  size_t unit_rows, ctas;
+  unit_shape(p.rows, cache.d, sms, &unit_rows, &ctas);
+  p.row_tiles = (p.rows + unit_rows - 1) / unit_rows;
   p.part_o = static_cast<float*>(c.workspace);
-  p.part_ml = reinterpret_cast<float2*>(p.part_o + 4ull * sms * 8 * nt * cache.d);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + 2 * ctas * unit_rows * cache.d);
+  if (many_rows(p.rows, cache.d)) return launch_cache_prefill(cache, p, sms, stream);
+  const int nt = static_cast<int>(unit_rows / 8);
   switch (cache.d * 16 + nt) {
     case 64 * 16 + 1: return launch<64, 1>(cache, p, sms, stream);
     case 64 * 16 + 2: return launch<64, 2>(cache, p, sms, stream);

@@ -226,6 +226,16 @@ def test_several_tokens(d, causal, H, Hkv, Nq):
     run_attention("bf16", d, 32, H, Hkv, Nq, [Nq, Nq + 1, 200, 333], causal=causal, layout="bnhd")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d,page", [(64, 64), (128, 16), (128, 256), (256, 32)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_chunks_of_prompts(dtype, d, page, causal):
+    """Many rows: more than one tile and one unit of them, sequences that begin
+    with this chunk and that are cached for the most part."""
+    run_attention(dtype, d, page, 6, 2, 130, [130, 131, 257, 900, 129], [130, 130, 128, 130, 1],
+                  causal=causal, layout="bnhd")
+
+
 @pytest.mark.parametrize("d,page", [(64, 16), (128, 64), (256, 16)])
 @pytest.mark.parametrize("causal", [True, False])
 def test_padded_queries_and_short_sequences(d, page, causal):

@@ -442,7 +442,7 @@ class Cache:
             raise ValueError("the cache's tensors must be on one CUDA device")
         self.pages, self.Hkv, self.page_size, self.d = pages, Hkv, page, d
         self.B, self.table_width = block_table.shape
-        self.device = k.device
+        self.device, self.device_index = k.device, k.get_device()
         self.struct = _FaCache(*(t.data_ptr() for t in self.tensors), pages, page, self.table_width,
                                Hkv, d, _view_strides(k), _view_strides(v))
         self._ref = ctypes.addressof(self.struct)
@@ -459,103 +459,92 @@ def _view_strides(t):
     return FaStrides(batch, head, row)
 
 
-_NO_STRIDES = FaStrides(0, 0, 0)
+_L6, _L12 = ctypes.c_longlong * 6, ctypes.c_longlong * 12   # two and four fa_strides
 
 
-def _view(t, like, heads, what):
-    """FaStrides of a [B, heads, N, d] view on like's device and of its dtype."""
-    if t is None:
-        return _NO_STRIDES
-    if (t.dim() != 4 or t.shape[0] != like.shape[0] or t.shape[1] != heads
-            or t.shape[2:] != like.shape[2:]):
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected "
-                         f"{(like.shape[0], heads) + tuple(like.shape[2:])}")
-    if t.dtype != like.dtype or t.device != like.device:
+def _view(t, shape, dtype, device, what):
+    """(batch, head, row) strides of a [B, heads, N, d] view that has to be of
+    the shape, dtype and device (an index) given."""
+    if t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype or t.get_device() != device:
         raise ValueError(f"{what} must have the dtype and device of the other tensors")
-    if t.stride(3) != 1:
+    s = t.stride()
+    B, heads, N, d = shape
+    if s[3] != 1:
         raise ValueError("the last (d) dimension must be contiguous")
-    return _view_strides(t)
+    # a dimension of one element has no stride of its own
+    return (s[0] if B > 1 else heads * N * d, s[1] if heads > 1 else N * d, s[2] if N > 1 else d)
 
 
 def _ints(t, shape, device, what):
     if t is None:
         return None
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+    if t.dtype != torch.int32 or t.shape != shape or t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous int32 {list(shape)} on the inputs' device")
     return t.data_ptr()
 
 
-class _On:
-    """The device and the stream of a call: makes the tensors' device current
-    where another one is, and takes that device's current stream unless one is
-    given.  On a given stream everything a call allocates comes from that
-    stream's memory, so that it is not handed out again before the call's work
-    is done; its outputs are marked as used on the caller's stream too."""
-
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError("expected CUDA tensors")
-        self.guard = None
-        self.caller = None
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError("the stream belongs to another device than the tensors")
-            current = torch.cuda.current_stream(device)
-            if stream != current:
-                self.guard, self.caller = torch.cuda.stream(stream), current
-        if self.guard is None and device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
-        self.stream = torch.cuda.current_stream(device) if stream is None else stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        self.ptr = self.stream.cuda_stream or None
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-    def made(self, t):
-        if self.caller is not None:
-            t.record_stream(self.caller)
-        return t
-
-
-def _positions(positions, rope_spec, B, N, device):
+def _positions(positions, axes, B, N, device):
     """(address, pos_batch) of positions [axes, B or 1, N] ([B or 1, N] on one axis)."""
     if positions is None:
         return None, 1
     shape = tuple(positions.shape)
-    if len(shape) == 2 and rope_spec is not None and rope_spec.axes == 1:
+    if len(shape) == 2 and axes == 1:
         shape = (1,) + shape
-    axes = 1 if rope_spec is None else rope_spec.axes
     if (positions.dtype != torch.int32 or len(shape) != 3 or shape[0] != axes or shape[1] not in (1, B)
-            or shape[2] != N or not positions.is_contiguous() or positions.device != device):
+            or shape[2] != N or positions.get_device() != device or not positions.is_contiguous()):
         raise ValueError(f"positions must be contiguous int32 [{axes}, {B} or 1, {N}] on the "
                          "inputs' device")
     return positions.data_ptr(), shape[1]
 
 
+def _on_stream(device, stream, call, *args):
+    """call(*args, raw stream) on the stream given, or on the current stream of
+    the tensors' device (an index), which is made current for the call.  On a
+    given stream everything the call allocates comes from that stream's memory,
+    so that it is not handed out again before the call's work is done; what it
+    returns is marked as used on the caller's stream too."""
+    if device < 0:
+        raise ValueError("expected CUDA tensors")
+    if stream is None:
+        if device == torch.cuda.current_device():
+            return call(*args, torch._C._cuda_getCurrentRawStream(device) or None)
+        with torch.cuda.device(device):
+            return call(*args, torch._C._cuda_getCurrentRawStream(device) or None)
+    if stream.device.index != device:
+        raise ValueError("the stream belongs to another device than the tensors")
+    caller = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        out = call(*args, stream.cuda_stream or None)
+    if stream != caller:
+        for t in out if isinstance(out, tuple) else (out,):
+            if t is not None:
+                t.record_stream(caller)
+    return out
+
+
 def _rope(q, k, positions, table, inverse, q_out, k_out, stream):
-    if q.dim() != 4:
-        raise ValueError("expected q [B, H, N, d]")
-    B, H, N, d = q.shape
-    Hkv = 0 if k is None else k.shape[1]
-    code = _dtype_code(q)
-    with _On(q.device, stream) as on:
-        st = (FaStrides * 4)()
-        st[0] = _view(q, q, H, "q")
-        st[1] = _view(k, q, Hkv, "k")
-        q_out = on.made(torch.empty_like(q)) if q_out is None else q_out
-        if k is not None and k_out is None:
-            k_out = on.made(torch.empty_like(k))
-        st[2] = _view(q_out, q, H, "q_out")
-        st[3] = _view(k_out, q, Hkv, "k_out")
-        pos, pos_batch = _positions(positions, table, B, N, q.device)
-        _check(load().fa_rope(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), B, H, Hkv, N, d,
-                              code, table._ref, pos, pos_batch, inverse, st, on.ptr), "fa_rope")
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise ValueError("expected q [B, H, N, d] and k [B, Hkv, N, d]")
+    qs = q.shape
+    B, H, N, d = qs
+    dtype, device = q.dtype, q.get_device()
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    a, b = _view(q, qs, dtype, device, "q"), _view(q_out, qs, dtype, device, "q_out")
+    pos, pos_batch = _positions(positions, table.axes, B, N, device)
+    if k is None:
+        Hkv, kp, kop, st = 0, None, None, _L12(*a, 0, 0, 0, *b)
+    else:
+        Hkv = k.shape[1]
+        ks = (B, Hkv, N, d)
+        if k_out is None:
+            k_out = torch.empty_like(k)
+        st = _L12(*a, *_view(k, ks, dtype, device, "k"), *b, *_view(k_out, ks, dtype, device, "k_out"))
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    _check(load().fa_rope(q.data_ptr(), kp, q_out.data_ptr(), kop, B, H, Hkv, N, d, _dtype_code(q),
+                          table._ref, pos, pos_batch, inverse, st, stream), "fa_rope")
     return q_out, k_out
 
 
@@ -564,12 +553,21 @@ def rope(q, k, positions, table: Rope, q_out=None, k_out=None, stream=None):
     `table` (fa_rope).  positions int32 [axes, B or 1, N] ([B or 1, N] on one
     axis), None: 0 .. N - 1.  Any views with d contiguous; outputs are
     allocated like the inputs unless given, and may be the inputs."""
-    return _rope(q, k, positions, table, 0, q_out, k_out, stream)
+    return _on_stream(q.get_device(), stream, _rope_forward, q, k, positions, table, q_out, k_out)
 
 
 def rope_backward(dq_out, dk_out, positions, table: Rope, dq=None, dk=None, stream=None):
     """(dq, dk) of `rope` from the gradients of its outputs."""
-    return _rope(dq_out, dk_out, positions, table, 1, dq, dk, stream)
+    return _on_stream(dq_out.get_device(), stream, _rope_inverse, dq_out, dk_out, positions, table, dq,
+                      dk)
+
+
+def _rope_forward(q, k, positions, table, q_out, k_out, stream):
+    return _rope(q, k, positions, table, 0, q_out, k_out, stream)
+
+
+def _rope_inverse(q, k, positions, table, q_out, k_out, stream):
+    return _rope(q, k, positions, table, 1, q_out, k_out, stream)
 
 
 def cache_append(cache: Cache, q, k, v, seq_lens, new_lens=None, rope: Rope | None = None,
@@ -579,29 +577,34 @@ def cache_append(cache: Cache, q, k, v, seq_lens, new_lens=None, rope: Rope | No
     (fa_cache_append).  seq_lens int32 [B]: lengths counting the new tokens;
     new_lens int32 [B]: how many of the N rows are tokens (None: all);
     positions as in `rope`, None: the tokens' numbers."""
-    if k.dim() != 4:
-        raise ValueError("expected k [B, Hkv, N, d]")
-    B, Hkv, N, d = k.shape
-    if Hkv != cache.Hkv or d != cache.d or B != cache.B or k.device != cache.device:
-        raise ValueError(f"k{tuple(k.shape)} does not belong to a cache of {cache.B} sequences, "
+    return _on_stream(k.get_device(), stream, _cache_append, cache, q, k, v, seq_lens, new_lens, rope,
+                      positions, q_out)
+
+
+def _cache_append(cache, q, k, v, seq_lens, new_lens, rope, positions, q_out, stream):
+    if k.dim() != 4 or (q is not None and q.dim() != 4):
+        raise ValueError("expected k and v [B, Hkv, N, d], q [B, H, N, d]")
+    ks = k.shape
+    B, Hkv, N, d = ks
+    dtype, device = k.dtype, k.get_device()
+    if Hkv != cache.Hkv or d != cache.d or B != cache.B or device != cache.device_index:
+        raise ValueError(f"k{tuple(ks)} does not belong to a cache of {cache.B} sequences, "
                          f"{cache.Hkv} heads, d {cache.d} on {cache.device}")
-    code = _dtype_code(k)
-    H = 0 if q is None else q.shape[1]
-    with _On(k.device, stream) as on:
-        st = (FaStrides * 4)()
-        st[0] = _view(q, k, H, "q")
-        st[1] = _view(k, k, Hkv, "k")
-        st[2] = _view(v, k, Hkv, "v")
-        if q is None:
-            q_out = None
-        elif q_out is None:
-            q_out = on.made(torch.empty_like(q))
-        st[3] = _view(q_out, k, H, "q_out")
-        pos, pos_batch = _positions(positions, rope, B, N, k.device)
-        _check(load().fa_cache_append(
-            cache._ref, _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out), B, H, N, code,
-            _ints(seq_lens, (B,), k.device, "seq_lens"), _ints(new_lens, (B,), k.device, "new_lens"),
-            None if rope is None else rope._ref, pos, pos_batch, st, on.ptr), "fa_cache_append")
+    kv = _view(k, ks, dtype, device, "k") + _view(v, ks, dtype, device, "v")
+    pos, pos_batch = _positions(positions, 1 if rope is None else rope.axes, B, N, device)
+    if q is None:
+        H, qp, qop, q_out, st = 0, None, None, None, _L12(0, 0, 0, *kv)
+    else:
+        H = q.shape[1]
+        qs = (B, H, N, d)
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        st = _L12(*_view(q, qs, dtype, device, "q"), *kv, *_view(q_out, qs, dtype, device, "q_out"))
+        qp, qop = q.data_ptr(), q_out.data_ptr()
+    _check(load().fa_cache_append(
+        cache._ref, qp, k.data_ptr(), v.data_ptr(), qop, B, H, N, _dtype_code(k),
+        _ints(seq_lens, (B,), device, "seq_lens"), _ints(new_lens, (B,), device, "new_lens"),
+        None if rope is None else rope._ref, pos, pos_batch, st, stream), "fa_cache_append")
     return q_out
 
 
@@ -610,34 +613,41 @@ def forward_cache(q, cache: Cache, seq_lens, causal: bool, scale: float, new_len
     """(o, lse) of q [B, H, Nq, d] against the first seq_lens[b] tokens of the
     cache (fa_fwd_cache).  causal: the new_lens[b] query rows (None: all Nq)
     are the sequence's last tokens."""
+    return _on_stream(q.get_device(), stream, _forward_cache, q, cache, seq_lens, causal, scale,
+                      new_lens, out, lse, workspace)
+
+
+def _forward_cache(q, cache, seq_lens, causal, scale, new_lens, out, lse, workspace, stream):
     if q.dim() != 4:
         raise ValueError("expected q [B, H, Nq, d]")
-    B, H, Nq, d = q.shape
-    if d != cache.d or B != cache.B or q.device != cache.device or H % cache.Hkv:
-        raise ValueError(f"q{tuple(q.shape)} does not fit a cache of {cache.B} sequences, "
+    qs = q.shape
+    B, H, Nq, d = qs
+    dtype, device = q.dtype, q.get_device()
+    if d != cache.d or B != cache.B or device != cache.device_index or H % cache.Hkv:
+        raise ValueError(f"q{tuple(qs)} does not fit a cache of {cache.B} sequences, "
                          f"{cache.Hkv} heads, d {cache.d} on {cache.device}")
-    code = _dtype_code(q)
     lib = load()
-    with _On(q.device, stream) as on:
-        st = (FaStrides * 2)()
-        st[0] = _view(q, q, H, "q")
-        out = on.made(torch.empty_like(q)) if out is None else out
-        st[1] = _view(out, q, H, "out")
-        if lse is None:
-            lse = on.made(torch.empty((B, H, Nq), dtype=torch.float32, device=q.device))
-        elif lse.dtype != torch.float32 or tuple(lse.shape) != (B, H, Nq) or \
-                not lse.is_contiguous() or lse.device != q.device:
-            raise ValueError(f"lse must be contiguous fp32 [{B}, {H}, {Nq}] on the inputs' device")
-        if workspace is None:
-            need = int(lib.fa_fwd_cache_workspace_size(B, H, cache.Hkv, Nq, d))
-            workspace = on.made(torch.empty(max(need, 256), dtype=torch.uint8, device=q.device))
-        elif workspace.device != q.device:
+    if out is None:
+        out = torch.empty_like(q)
+    st = _L6(*_view(q, qs, dtype, device, "q"), *_view(out, qs, dtype, device, "out"))
+    if lse is None:
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=cache.device)
+    elif (lse.dtype != torch.float32 or lse.shape != (B, H, Nq) or lse.get_device() != device
+          or not lse.is_contiguous()):
+        raise ValueError(f"lse must be contiguous fp32 [{B}, {H}, {Nq}] on the inputs' device")
+    if workspace is None:
+        need = lib.fa_fwd_cache_workspace_size(B, H, cache.Hkv, Nq, d)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=cache.device)
+        ws_bytes = need
+    else:
+        if workspace.get_device() != device:
             raise ValueError("the workspace must be on the inputs' device")
-        _check(lib.fa_fwd_cache(
-            q.data_ptr(), cache._ref, out.data_ptr(), lse.data_ptr(), B, H, Nq, int(causal),
-            float(scale), code, _ints(seq_lens, (B,), q.device, "seq_lens"),
-            _ints(new_lens, (B,), q.device, "new_lens"), st, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), on.ptr), "fa_fwd_cache")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _check(lib.fa_fwd_cache(
+        q.data_ptr(), cache._ref, out.data_ptr(), lse.data_ptr(), B, H, Nq, int(causal), scale,
+        _dtype_code(q), _ints(seq_lens, (B,), device, "seq_lens"),
+        _ints(new_lens, (B,), device, "new_lens"), st, workspace.data_ptr(), ws_bytes, stream),
+        "fa_fwd_cache")
     return out, lse
 
 

@@ -11,9 +11,6 @@
 // its unit, slot 1: it does), the units inside it as results.
 #pragma once
 
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-
 #include "fa_internal.h"
 #include "sm103_ptx.cuh"
 
@@ -92,9 +89,11 @@ __device__ __forceinline__ int row_limit(const SeqParams& p, const Sequence& s, 
   return p.causal ? min(s.len, s.len - s.n + r / p.G + 1) : s.len;
 }
 
-__device__ __forceinline__ uint32_t widen(uint32_t two) {   // two e4m3 codes -> f16x2
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
-  return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// Four e4m3 codes -> two f16x2.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(w));
 }
 
 // Bytes that are NaN codes (0x7f, 0xff), as a byte mask.

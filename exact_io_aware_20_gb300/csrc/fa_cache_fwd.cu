@@ -327,8 +327,9 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
           #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t a0 = widen(xs[j] & 0xffffu), a2 = widen(xs[j] >> 16);
-            const uint32_t a1 = widen(ys[j] & 0xffffu), a3 = widen(ys[j] >> 16);
+            uint32_t a0, a1, a2, a3;
+            widen4(xs[j], a0, a2);
+            widen4(ys[j], a1, a3);
             #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const uint2 q2 = kQRegs ? qr[kQRegs ? c * 4 + j : 0][kQRegs ? nt : 0]
@@ -423,8 +424,9 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
               const uint32_t sel = u ? 0x7362u : 0x5140u;
               const uint32_t x = __byte_perm(v[0][w], v[1][w], sel);
               const uint32_t y = __byte_perm(v[2][w], v[3][w], sel);
-              const uint32_t a0 = widen(x & 0xffffu), a1 = widen(x >> 16);
-              const uint32_t a2 = widen(y & 0xffffu), a3 = widen(y >> 16);
+              uint32_t a0, a1, a2, a3;
+              widen4(x, a0, a1);
+              widen4(y, a2, a3);
               #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
                 mma(acc[half * 8 + 2 * w + u][nt], a0, a1, a2, a3, p0[nt], p1[nt]);
@@ -462,8 +464,10 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float hits[4] = {0.f, 0.f, 0.f, 0.f};
-              mma(hits, widen(x & 0xffffu), widen(x >> 16), widen(y & 0xffffu), widen(y >> 16),
-                  c0[nt], c1[nt]);
+              uint32_t a0, a1, a2, a3;
+              widen4(x, a0, a1);
+              widen4(y, a2, a3);
+              mma(hits, a0, a1, a2, a3, c0[nt], c1[nt]);
               #pragma unroll
               for (int k = 0; k < 4; ++k)
                 if (hits[k] > 0.f) acc[im][nt][k] = __uint_as_float(0x7fffffffu);

@@ -19,10 +19,12 @@
 // multiplications a row and tile, and the exponent's multiply-add takes them
 // for the rest.
 //
-// Roles: warps 0-3 softmax of tile A, 4-7 of tile B (d = 256: idle), 8-11
-// conversion and q, 12 issues the products.  512 threads start with 128
-// registers each; the softmax groups rise to 192, the converters keep 88 and
-// the last group 40 (2 * 192 + 88 + 40 = 4 * 128).
+// Roles: warps 0-3 softmax of tile A, 4-7 of tile B (d = 256: conversion),
+// 8-11 conversion and q, 12 issues the products, 13 walks the share and
+// describes its pieces to the others.  512 threads start with 128 registers
+// each, which the groups then share out by their need.  With 192 KB of tiles
+// next to none of the SM's storage is left as L1, so a register that spills
+// costs a trip to L2: the walk lives in one warp for that reason.
 #include <algorithm>
 #include <atomic>
 
@@ -37,6 +39,9 @@ template <int D>
 struct Pre {
   static constexpr int kTiles = D == 256 ? 1 : 2;
   static constexpr int kRows = 128 * kTiles;        // of a unit
+  static constexpr int kSoftWarps = 4 * kTiles;
+  static constexpr int kConvWarps = 12 - kSoftWarps;
+  static constexpr int kConvRows = 128 / kConvWarps;   // keys of a tile that a warp converts
   static constexpr int kChunks = D / 64;            // 64-column parts
   static constexpr int kKPiece = 128 * 128;         // K: 128 keys x 64 columns, f16
   static constexpr int kKStages = 4;
@@ -50,16 +55,22 @@ struct Pre {
   static constexpr int kVOff = kKOff + kKStages * kKPiece;
   static constexpr int kMetaOff = kVOff + kVStages * kVPiece;   // [8 tiles][8 groups] ks, log2 vs, 1/vs
   static constexpr int kPowOff = kMetaOff + 8 * 8 * 16;         // [2 pieces][rows] of q
-  static constexpr int kBarOff = kPowOff + 2 * kRows * 4;
+  static constexpr int kRecOff = kPowOff + 2 * kRows * 4;       // [4 pieces] (Piece)
+  static constexpr int kBarOff = kRecOff + 4 * 64;
   static constexpr int kQFull = 0, kQEmpty = 1, kKFull = 2, kKEmpty = kKFull + kKStages,
                        kVFull = kKEmpty + kKStages, kVEmpty = kVFull + kVStages,
                        kSFull = kVEmpty + kVStages, kPFull = kSFull + 2, kODone = kPFull + 2,
-                       kDrain = kODone + 2, kNumBars = kDrain + 1;
+                       kDrain = kODone + 2, kRecFull = kDrain + 1, kRecEmpty = kRecFull + 4,
+                       kNumBars = kRecEmpty + 4;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   static constexpr int kRedOff = (kMiscOff + 32 + 15) / 16 * 16;   // start: sums and the found entry
   static constexpr int kBytes = kRedOff + 16 * 8 + 16;
   static constexpr int kAlloc = kBytes + 1024;
   static constexpr uint32_t kTS = 0, kTO = 256, kTmemCols = 512;
+  // registers a thread: the launch's 4 * 128 among the four warpgroups
+  static constexpr int kRegSoft = 176;
+  static constexpr int kRegMisc = kTiles == 1 ? 112 : 48;
+  static constexpr int kRegConv = kTiles == 1 ? (512 - kRegSoft - kRegMisc) / 2 : 512 - 2 * kRegSoft - kRegMisc;
   static_assert(kAlloc <= 227 * 1024, "shared memory budget");
   static_assert(256 + kTiles * D <= 512, "TMEM budget");
 };
@@ -73,40 +84,40 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// A piece of a unit: its steps [s0, s1) of the share, and for each of its row
-// tiles the end of the tile's steps and the keys that all its live rows see.
-template <int D>
-struct Piece {
-  int s0, s1;
-  int end[Pre<D>::kTiles], full[Pre<D>::kTiles];
-};
-template <int D>
-__device__ __forceinline__ Piece<D> piece_at(const FwdCacheParams& p,
-                                             const Walk<Pre<D>::kRows, 128>& at, long long left) {
-  Piece<D> w;
-  w.s0 = at.step;
-  w.s1 = static_cast<int>(min(static_cast<long long>(at.steps), at.step + left));
-  const int row0 = at.e % p.row_tiles * Pre<D>::kRows;
-  #pragma unroll
-  for (int u = 0; u < Pre<D>::kTiles; ++u) {
-    const int r0 = row0 + 128 * u, r1 = min(p.rows, r0 + 128);
-    TileLimits t = {0, 0};
-    if (r0 < r1) t = tile_limits(p.seq, at.seq, r0, r1);
-    w.end[u] = min(w.s1, (t.lim + 127) / 128);
-    w.full[u] = t.full;
-  }
-  return w;
+// 16 bytes of global memory, zeros where `on` is false; and four bytes, `other`
+// where it is false.  Kept in program order with the other volatile asm, so
+// that a load is issued where it stands, a tile ahead of its use: left to the
+// compiler the loads of a tile were waited for one by one.
+__device__ __forceinline__ void load_16(uint4& x, const void* src, bool on) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+      "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+      : "l"(src), "r"(static_cast<uint32_t>(on)));
+}
+__device__ __forceinline__ uint32_t load_4(const void* src, bool on, uint32_t other) {
+  uint32_t x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.u32 %0, %3;\n\t"
+      "@p ld.global.nc.u32 %0, [%1];\n\t}"
+      : "=r"(x)
+      : "l"(src), "r"(static_cast<uint32_t>(on)), "r"(other));
+  return x;
 }
 
-// The keys that every live row of a piece's tiles sees.
-template <int D>
-__device__ __forceinline__ int seen_by_all(const Piece<D>& w) {
-  int full = 0x7fffffff;
-  #pragma unroll
-  for (int u = 0; u < Pre<D>::kTiles; ++u)
-    if (w.end[u] > w.s0) full = min(full, w.full[u]);
-  return full;
-}
+// A piece of a unit, as the scheduling warp describes it to the others.
+struct Piece {
+  int s0, s1;          // its steps; s1 < 0: there are no more pieces
+  int end[2];          // end of each row tile's steps
+  int full[2];         // the keys that every live row of the tile sees
+  int all;             // ... that every live row of both tiles sees
+  int lim;             // the keys that any row sees
+  int b, h, row0;      // sequence, key/value head, first row
+  int len, n;          // of the sequence
+  int whole;           // the piece is a whole unit
+};
+static_assert(sizeof(Piece) <= 64, "a record's place");
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -129,14 +140,14 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
 
   grid_launch_dependents();
   if (threadIdx.x == 0) {
-    mbar_init(bar(L::kQFull), 4);       // one arrival per converting warp
+    mbar_init(bar(L::kQFull), L::kConvWarps);
     mbar_init(bar(L::kQEmpty), 1);
     for (int s = 0; s < L::kKStages; ++s) {
-      mbar_init(bar(L::kKFull + s), 4);
+      mbar_init(bar(L::kKFull + s), L::kConvWarps);
       mbar_init(bar(L::kKEmpty + s), 1);
     }
     for (int s = 0; s < L::kVStages; ++s) {
-      mbar_init(bar(L::kVFull + s), 4);
+      mbar_init(bar(L::kVFull + s), L::kConvWarps / L::kVParts);   // (a warp's rows lie in one piece)
       mbar_init(bar(L::kVEmpty + s), 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -144,7 +155,11 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
       mbar_init(bar(L::kPFull + s), 4);   // one arrival per softmax warp
       mbar_init(bar(L::kODone + s), 1);
     }
-    for (int s = 0; s < 4; ++s) nan_seen[s] = 0;
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(bar(L::kRecFull + s), 1);
+      mbar_init(bar(L::kRecEmpty + s), 1 + L::kConvWarps + L::kSoftWarps);
+      nan_seen[s] = 0;
+    }
     mbar_init(bar(L::kDrain), 1);
     *abort = 0;
     fence_barrier_init();
@@ -161,16 +176,59 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
   }
   find_entry<L::kRows, 128, kThreads>(p, lo / p.Hkv, red, found);
   W at;
-  at.start(p, found, lo);
+  if (warp == 13) at.start(p, found, lo);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  long long left = hi - lo;
+  // piece np, once it is there; and this warp has no more need of it
+  auto piece = [&](int np) { return reinterpret_cast<const volatile Piece*>(smem + L::kRecOff + (np & 3) * 64); };
+  auto piece_wait = [&](int np) { return wait_uniform(bar(L::kRecFull + (np & 3)), (np >> 2) & 1, abort); };
+  auto piece_done = [&](int np) { mbar_arrive_warp(bar(L::kRecEmpty + (np & 3))); };
 
   if (warp >= 12) {
-    fewer_registers<40>();
-    if (warp == 12) {
+    fewer_registers<L::kRegMisc>();
+    if (warp == 13) {
+      // -------------------------------------------------------- schedule
+      long long left = hi - lo;
+      for (int np = 0;; ++np) {
+        if (np >= 4 && !wait_uniform(bar(L::kRecEmpty + (np & 3)), ((np >> 2) + 1) & 1, abort)) break;
+        volatile Piece* w = reinterpret_cast<volatile Piece*>(smem + L::kRecOff + (np & 3) * 64);
+        const int s1 = left > 0 ? static_cast<int>(min(static_cast<long long>(at.steps), at.step + left)) : -1;
+        if (lane == 0) {
+          w->s0 = at.step;
+          w->s1 = s1;
+          if (s1 >= 0) {
+            const int row0 = at.e % p.row_tiles * L::kRows;
+            int all = 0x7fffffff;
+            #pragma unroll
+            for (int u = 0; u < L::kTiles; ++u) {
+              const int r0 = row0 + 128 * u, r1 = min(p.rows, r0 + 128);
+              TileLimits t = {0, 0};
+              if (r0 < r1) t = tile_limits(p.seq, at.seq, r0, r1);
+              const int end = min(s1, (t.lim + 127) / 128);
+              w->end[u] = end;
+              w->full[u] = t.full;
+              if (end > at.step) all = min(all, t.full);
+            }
+            w->all = all;
+            w->lim = at.lim;
+            w->b = at.e / p.row_tiles;
+            w->h = at.h;
+            w->row0 = row0;
+            w->len = at.seq.len;
+            w->n = at.seq.n;
+            w->whole = at.step == 0 && s1 == at.steps;
+          }
+        }
+        __syncwarp();
+        if (elect_one()) mbar_arrive(bar(L::kRecFull + (np & 3)));
+        __syncwarp();
+        if (s1 < 0) break;
+        left -= s1 - at.step;
+        if (left > 0) at.next_unit(p);
+      }
+    } else if (warp == 12) {
       // ---------------------------------------------------------- products
       constexpr uint32_t kIdS = idesc_f16(128, 128, 0, 0, 0);
       constexpr uint32_t kIdO = idesc_f16(128, D, 0, 0, 1);
@@ -215,8 +273,16 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
         return true;
       };
       int g = 0;   // tiles so far (d = 256: selects the score buffer)
-      for (int np = 0; ok && left > 0; ++np) {
-        const Piece<D> w = piece_at<D>(p, at, left);
+      for (int np = 0; ok; ++np) {
+        if (!piece_wait(np)) break;
+        // (read from lane 0: the same in every lane, on the uniform datapath)
+        struct { int s0, s1, end[2]; } w;
+        w.s0 = __shfl_sync(0xffffffffu, piece(np)->s0, 0);
+        w.s1 = __shfl_sync(0xffffffffu, piece(np)->s1, 0);
+        w.end[0] = __shfl_sync(0xffffffffu, piece(np)->end[0], 0);
+        w.end[1] = __shfl_sync(0xffffffffu, piece(np)->end[1], 0);
+        piece_done(np);
+        if (w.s1 < 0) break;
         ok = wait_uniform(bar(L::kQFull), np & 1, abort);
         if (!ok) break;
         tc_fence_after();
@@ -259,118 +325,101 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
             vp += L::kVParts;
           }
         }
-        left -= w.s1 - w.s0;
-        if (left > 0) at.next_unit(p);
       }
       mma_commit(bar(L::kDrain));
       drain_wait(bar(L::kDrain), 0);
     }
-  } else if (warp >= 8) {
+  } else if (warp >= L::kSoftWarps) {
     // ------------------------------------------------------------ conversion
-    fewer_registers<88>();
-    const int cw = warp - 8;
+    if constexpr (L::kRegConv > 128) more_registers<L::kRegConv>();
+    else fewer_registers<L::kRegConv>();
+    const int cw = warp - L::kSoftWarps;
     const int r8 = lane >> 2, c16 = lane & 3;   // row of eight, 16-column part of 64
-    const W begin = at;
-    W ld = begin;                 // of the loads, one piece ahead
-    long long ld_left = left;
-    int ld_j = at.step, ld_part = 0;   // ld_part: K pieces, then V pieces of a tile
-    constexpr int kParts = L::kChunks + L::kVParts;
-    auto row_of = [&](const Strides& st, const unsigned char* base, int e, int h, int key) {
-      const int b = e / p.row_tiles;
-      int page = p.table[static_cast<long long>(b) * p.width + (key >> p.page_log2)];
-      if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.pages)) {
-        atomicOr(p.seq.err, kErrCache);
-        page = 0;
-      }
-      return base + page * st.b + h * st.h + (key & ((1 << p.page_log2) - 1)) * st.n;
+    constexpr int kI = L::kConvRows / 8;
+    // Codes of one tile: rows kConvRows cw + 8 i + r8, 16 columns of each
+    // 64-column part.  Each part's registers are loaded again, for the next
+    // tile, as soon as it has been written: a tile's time hides the latency.
+    uint4 kr[L::kChunks][kI], vr[L::kChunks][kI];
+    int page[kI];
+    float ks = 1.f, vs = 1.f;
+    int tile = 0, lim = 0, b = 0, h = 0;      // the tile that is loaded next, and its piece
+    auto enter = [&](int np) {
+      tile = piece(np)->s0;
+      lim = piece(np)->lim;
+      b = piece(np)->b;
+      h = piece(np)->h;
     };
-    uint4 nxt[8];
-    float nks = 1.f, nvs = 1.f;
-    // loads of part ld_part of tile ld_j (rows past the keys that any row
-    // sees are zeros), and on to the next part
-    auto load = [&]() {
-      if (ld_left <= 0) return;
+    auto pages_of = [&]() {
+      const int* row = p.table + static_cast<long long>(b) * p.width;
       #pragma unroll
-      for (int i = 0; i < 8; ++i) nxt[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (ld_part < L::kChunks) {
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int key = ld_j * 128 + 32 * cw + 8 * i + r8;
-          if (key < ld.lim)
-            nxt[i] = *reinterpret_cast<const uint4*>(row_of(p.ks, p.k, ld.e, ld.h, key) +
-                                                     64 * ld_part + 16 * c16);
-        }
-        if (ld_part == 0) {
-          // the scales of the warp's two 16-key groups, in lanes 0 and 1
-          nks = nvs = 1.f;
-          const int key = ld_j * 128 + 32 * cw + 16 * lane;
-          if (lane < 2 && key < ld.lim) {
-            int page = p.table[static_cast<long long>(ld.e / p.row_tiles) * p.width + (key >> p.page_log2)];
-            if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.pages)) page = 0;
-            nks = p.k_scale[static_cast<long long>(page) * p.Hkv + ld.h];
-            nvs = p.v_scale[static_cast<long long>(page) * p.Hkv + ld.h];
-          }
-        }
-      } else {
-        constexpr int kRowsW = L::kVKeys / 4;      // rows of a warp
-        #pragma unroll
-        for (int i = 0; i < kRowsW / 8; ++i) {
-          const int key = ld_j * 128 + (ld_part - L::kChunks) * L::kVKeys + kRowsW * cw + 8 * i + r8;
-          if (key < ld.lim) {
-            const unsigned char* row = row_of(p.vs, p.v, ld.e, ld.h, key) + 16 * c16;
-            #pragma unroll
-            for (int c = 0; c < L::kChunks; ++c)
-              nxt[i * L::kChunks + c] = *reinterpret_cast<const uint4*>(row + 64 * c);
-          }
-        }
+      for (int i = 0; i < kI; ++i) {
+        const int key = tile * 128 + L::kConvRows * cw + 8 * i;   // (a page holds whole groups of 16)
+        page[i] = static_cast<int>(load_4(row + (key >> p.page_log2), key < lim, 0u));
       }
-      if (++ld_part == kParts) {
-        ld_part = 0;
-        --ld_left;
-        if (++ld_j == ld.steps && ld_left > 0) {
-          ld.next_unit(p);
-          ld_j = 0;
-        }
-      }
-    };
-    auto put = [&](uint32_t piece, int rows, int r, int c, const uint4& x) {
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      uint32_t h[8];
       #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        h[2 * i] = widen(w[i] & 0xffffu);
-        h[2 * i + 1] = widen(w[i] >> 16);
-      }
-      const uint32_t row = piece + c * rows * 128 + r * 128;
-      st_shared_v4(row + (((2 * c16) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-      st_shared_v4(row + (((2 * c16 + 1) ^ (r & 7)) << 4), h[4], h[5], h[6], h[7]);
+      for (int i = 0; i < kI; ++i)
+        if (static_cast<unsigned>(page[i]) >= static_cast<unsigned>(p.pages)) {
+          atomicOr(p.seq.err, kErrCache);
+          page[i] = 0;
+        }
+      // the scales of the warp's 16-key groups, one a lane
+      int mine = page[0];
+      if constexpr (kI > 2) mine = lane == 0 ? page[0] : page[2];
+      const long long sc = static_cast<long long>(mine) * p.Hkv + h;
+      const bool on = lane < kI / 2 && tile * 128 + L::kConvRows * cw + 16 * lane < lim;
+      ks = __uint_as_float(load_4(p.k_scale + sc, on, 0x3f800000u));
+      vs = __uint_as_float(load_4(p.v_scale + sc, on, 0x3f800000u));
     };
-    load();
+    // rows past the keys that any row sees are zeros
+    auto load = [&](const unsigned char* base, const Strides& st, int c, uint4 (&x)[kI]) {
+      const unsigned char* head = base + h * st.h + 64 * c + 16 * c16;
+      #pragma unroll
+      for (int i = 0; i < kI; ++i) {
+        const int key = tile * 128 + L::kConvRows * cw + 8 * i + r8;
+        load_16(x[i], head + page[i] * st.b + (key & ((1 << p.page_log2) - 1)) * st.n, key < lim);
+      }
+    };
+    auto put = [&](uint32_t rows, int r, const uint4& x) {
+      uint32_t w[8];
+      widen4(x.x, w[0], w[1]);
+      widen4(x.y, w[2], w[3]);
+      widen4(x.z, w[4], w[5]);
+      widen4(x.w, w[6], w[7]);
+      const uint32_t row = rows + r * 128;
+      st_shared_v4(row + (((2 * c16) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
+      st_shared_v4(row + (((2 * c16 + 1) ^ (r & 7)) << 4), w[4], w[5], w[6], w[7]);
+    };
+    bool ok = piece_wait(0);
+    bool more = ok;
+    if (ok) {
+      enter(0);
+      pages_of();
+      #pragma unroll
+      for (int c = 0; c < L::kChunks; ++c) load(p.k, p.ks, c, kr[c]);
+      #pragma unroll
+      for (int c = 0; c < L::kChunks; ++c) load(p.v, p.vs, c, vr[c]);
+    }
     int kp = 0, vp = 0, g = 0;
-    bool ok = true;
-    for (int np = 0; ok && left > 0; ++np) {
-      const Piece<D> w = piece_at<D>(p, at, left);
-      const int b = at.e / p.row_tiles, row0 = at.e % p.row_tiles * L::kRows;
-      // ---- q: rows as f16, once the last scores of the unit before are done
+    for (int np = 0; ok && more; ++np) {
+      // ---- q: rows as f16, once the last scores of the piece before are done
       if (np > 0 && !wait_uniform(bar(L::kQEmpty), (np - 1) & 1, abort)) break;
       // the next piece's flag: no converting warp is there before this one has
       // announced this piece's q, and the results of piece np - 3 are written
       if (cw == 0 && lane == 0) nan_seen[(np + 1) & 3] = 0;
       {
         constexpr int kLanes = D / 8, kPer = 32 / kLanes;        // lanes of a row, rows at a time
-        constexpr int kRowsW = L::kRows / 4, kBatch = 4;
+        constexpr int kRowsW = L::kRows / L::kConvWarps, kBatch = 4;
         const int rl = lane / kLanes, cl = lane % kLanes;
+        const int row0 = piece(np)->row0 + cw * kRowsW + rl, live = piece(np)->n;
+        const uint16_t* src = p.q + b * p.qs.b + h * p.seq.G * p.qs.h + 8 * cl;
         #pragma unroll 1
         for (int i0 = 0; i0 < kRowsW; i0 += kPer * kBatch) {
           uint4 x[kBatch];
           #pragma unroll
           for (int k = 0; k < kBatch; ++k) {
-            const int r = row0 + cw * kRowsW + i0 + k * kPer + rl;
-            x[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < p.rows && r / p.seq.G < at.seq.n)
-              x[k] = *reinterpret_cast<const uint4*>(
-                  p.q + b * p.qs.b + (at.h * p.seq.G + r % p.seq.G) * p.qs.h +
-                  (r / p.seq.G) * p.qs.n + 8 * cl);
+            const int r = row0 + i0 + k * kPer;
+            const int i = r / p.seq.G;
+            load_16(x[k], src + (r - i * p.seq.G) * p.qs.h + i * p.qs.n, r < p.rows && i < live);
           }
           #pragma unroll
           for (int k = 0; k < kBatch; ++k) {
@@ -404,94 +453,101 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
       }
       fence_proxy_async_smem();
       mbar_arrive_warp(bar(L::kQFull));
-      const int full = seen_by_all<D>(w);
-      for (int j = w.s0; ok && j < w.s1; ++j, ++g) {
+      const int full = piece(np)->all, s1 = piece(np)->s1;
+      for (int j = piece(np)->s0; j < s1; ++j, ++g) {
+        const float ks_now = ks, vs_now = vs;
+        // on to the next tile
+        if (j + 1 < s1) {
+          ++tile;
+        } else {
+          piece_done(np);
+          ok = piece_wait(np + 1);
+          more = ok && piece(np + 1)->s1 >= 0;
+          if (more) enter(np + 1);
+        }
+        if (!ok) break;
+        if (more) pages_of();
         #pragma unroll
-        for (int part = 0; part < kParts; ++part) {
-          const bool key = part < L::kChunks;
-          uint4 cur[8];
-          #pragma unroll
-          for (int i = 0; i < 8; ++i) cur[i] = nxt[i];
-          const float ks = nks, vs = nvs;
-          load();
-          if (key) {
-            const int s = kp % L::kKStages;
-            if (kp >= L::kKStages && !wait_uniform(bar(L::kKEmpty + s), (kp / L::kKStages + 1) & 1, abort)) {
-              ok = false;
-              break;
-            }
-            if (part == 0 && lane < 2) {
+        for (int c = 0; c < L::kChunks; ++c) {
+          const int s = kp % L::kKStages;
+          if (kp >= L::kKStages && ok)
+            ok = wait_uniform(bar(L::kKEmpty + s), (kp / L::kKStages + 1) & 1, abort);
+          if (ok) {
+            if (c == 0 && lane < kI / 2) {
               // when K of tile g is written the scores of tile g - 4 are done,
               // so P V of tile g - 5 is: eight tiles of these live at a time
-              const float lv = log2f(vs);
-              meta[(g & 7) * 8 + 2 * cw + lane] = make_float4(ks, lv, ex2_approx(-lv), 0.f);
+              const float lv = log2f(vs_now);
+              meta[(g & 7) * 8 + (kI / 2) * cw + lane] = make_float4(ks_now, lv, ex2_approx(-lv), 0.f);
             }
-            const uint32_t piece = sbase + L::kKOff + s * L::kKPiece;
             #pragma unroll
-            for (int i = 0; i < 4; ++i) put(piece, 128, 32 * cw + 8 * i + r8, 0, cur[i]);
+            for (int i = 0; i < kI; ++i)
+              put(sbase + L::kKOff + s * L::kKPiece, L::kConvRows * cw + 8 * i + r8, kr[c][i]);
             fence_proxy_async_smem();
             mbar_arrive_warp(bar(L::kKFull + s));
-            ++kp;
-          } else {
-            const int s = vp % L::kVStages;
-            if (vp >= L::kVStages && !wait_uniform(bar(L::kVEmpty + s), (vp / L::kVStages + 1) & 1, abort)) {
-              ok = false;
-              break;
-            }
-            constexpr int kRowsW = L::kVKeys / 4;
-            if (j * 128 + 128 > full) {
-              // NaN in a place that some row may not see: 0 instead, and the
-              // rows that see it are mended when they are written
-              uint32_t any = 0;
-              #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                uint32_t* c = reinterpret_cast<uint32_t*>(&cur[i]);
-                #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const uint32_t n = nan_bytes(c[k]);
-                  any |= n;
-                  c[k] &= ~n;
-                }
-              }
-              if (any != 0) nan_seen[np & 3] = 1;
-            }
-            const uint32_t piece = sbase + L::kVOff + s * L::kVPiece;
+          }
+          ++kp;
+          if (more) load(p.k, p.ks, c, kr[c]);
+        }
+        // V: this warp's rows lie in one piece of the tile
+        const int n = vp + L::kConvRows * cw / L::kVKeys, s = n % L::kVStages;
+        vp += L::kVParts;
+        if (n >= L::kVStages && ok)
+          ok = wait_uniform(bar(L::kVEmpty + s), (n / L::kVStages + 1) & 1, abort);
+        if (!ok) break;
+        if (j * 128 + 128 > full) {
+          // NaN in a place that some row may not see: 0 instead, and the rows
+          // that see it are mended when they are written
+          uint32_t any = 0;
+          #pragma unroll
+          for (int c = 0; c < L::kChunks; ++c)
             #pragma unroll
-            for (int i = 0; i < kRowsW / 8; ++i)
+            for (int i = 0; i < kI; ++i) {
+              uint32_t x[4] = {vr[c][i].x, vr[c][i].y, vr[c][i].z, vr[c][i].w};
               #pragma unroll
-              for (int c = 0; c < L::kChunks; ++c)
-                put(piece, L::kVKeys, kRowsW * cw + 8 * i + r8, c, cur[i * L::kChunks + c]);
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t nan = nan_bytes(x[k]);
+                any |= nan;
+                x[k] &= ~nan;
+              }
+              vr[c][i] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          if (any != 0) nan_seen[np & 3] = 1;
+        }
+        #pragma unroll
+        for (int c = 0; c < L::kChunks; ++c) {
+          #pragma unroll
+          for (int i = 0; i < kI; ++i)
+            put(sbase + L::kVOff + s * L::kVPiece + c * (L::kVKeys * 128),
+                (L::kConvRows * cw + 8 * i + r8) & (L::kVKeys - 1), vr[c][i]);
+          if (c + 1 == L::kChunks) {
             fence_proxy_async_smem();
             mbar_arrive_warp(bar(L::kVFull + s));
-            ++vp;
           }
+          if (more) load(p.v, p.vs, c, vr[c]);
         }
       }
-      left -= w.s1 - w.s0;
-      if (left > 0) at.next_unit(p);
     }
   } else {
     // ------------------------------------------------------------ softmax
-    more_registers<192>();
+    more_registers<L::kRegSoft>();
     const int u = warp >> 2;                      // row tile of this warpgroup
     const int r_tile = (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tO = tmem + L::kTO + (L::kTiles == 2 ? D * u : 0) + lane_off;
     int cs = 0, od = 0;     // S_FULL phases (d = 256: tiles), O_DONE phases consumed
     int g = 0;              // tiles of the CTA so far
-    bool ok = u < L::kTiles;
-    for (int np = 0; ok && left > 0; ++np) {
-      int s0, s1, end, full, all_see;   // all_see: the keys that every live row of the unit sees
+    bool ok = true;
+    for (int np = 0; ok; ++np) {
+      if (!piece_wait(np)) break;
+      const int s0 = piece(np)->s0;
+      if (piece(np)->s1 < 0) break;
+      const int end = piece(np)->end[u], full = piece(np)->full[u];
+      int sees;       // the keys that this thread's row sees
       {
-        const Piece<D> w = piece_at<D>(p, at, left);
-        s0 = w.s0;
-        s1 = w.s1;
-        end = (L::kTiles == 2 && u) ? w.end[L::kTiles - 1] : w.end[0];
-        full = (L::kTiles == 2 && u) ? w.full[L::kTiles - 1] : w.full[0];
-        all_see = seen_by_all<D>(w);
+        const int r = piece(np)->row0 + 128 * u + r_tile;
+        const Sequence seq = {piece(np)->len, piece(np)->n};
+        sees = r < p.rows ? max(0, row_limit(p.seq, seq, r)) : 0;
       }
-      const int r = at.e % p.row_tiles * L::kRows + 128 * u + r_tile;
-      const int sees = r < p.rows ? max(0, row_limit(p.seq, at.seq, r)) : 0;
       float m = kNoMax, l = 0.f, row_scale = 0.f;
       for (int j = s0; j < end; ++j) {
         const int buf = L::kTiles == 2 ? u : cs & 1;
@@ -594,14 +650,16 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
         ++od;
         tc_fence_after();
       }
-      const int b = at.e / p.row_tiles, i = r / p.seq.G, head = at.h * p.seq.G + r % p.seq.G;
-      const bool in = r < p.rows;
-      const float sum = (in && i < at.seq.n) ? l : 0.f;
-      const bool whole = s0 == 0 && s1 == at.steps;
+      const volatile Piece* w = piece(np);
+      const int r = w->row0 + 128 * u + r_tile, b = w->b, kh = w->h, s1 = w->s1;
+      const int i = r / p.seq.G, head = kh * p.seq.G + r % p.seq.G;
+      const bool in = r < p.rows, whole = w->whole != 0;
+      const float sum = (in && i < w->n) ? l : 0.f;
       const long long slot = 2ll * blockIdx.x + (s0 > 0 ? 0 : 1);
       const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
       const bool nans = nan_seen[np & 3] != 0;
-      const int nan_from = max(s0, all_see / 128) * 128, nan_to = min(s1 * 128, sees);
+      const int nan_from = max(s0, w->all / 128) * 128, nan_to = min(s1 * 128, sees);
+      piece_done(np);
       #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -619,7 +677,7 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
             int page = p.table[static_cast<long long>(b) * p.width + (key >> p.page_log2)];
             if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.pages)) page = 0;
             const uint32_t* row = reinterpret_cast<const uint32_t*>(
-                p.v + page * p.vs.b + at.h * p.vs.h + (key & ((1 << p.page_log2) - 1)) * p.vs.n + 32 * c);
+                p.v + page * p.vs.b + kh * p.vs.h + (key & ((1 << p.page_log2) - 1)) * p.vs.n + 32 * c);
             #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const uint32_t n = nan_bytes(row[k]);
@@ -660,8 +718,6 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
       }
       tc_fence_before();   // O has been read out before the next P_FULL allows P V over it
       g += s1 - s0;
-      left -= s1 - s0;
-      if (left > 0) at.next_unit(p);
     }
   }
 

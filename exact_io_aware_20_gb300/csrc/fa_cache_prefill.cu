@@ -21,7 +21,8 @@
 //
 // Roles: warps 0-3 softmax of tile A, 4-7 of tile B (d = 256: conversion),
 // 8-11 conversion and q, 12 issues the products, 13 walks the share and
-// describes its pieces to the others.  512 threads start with 128 registers
+// describes its pieces to the others, 14 finds the pages and scales of the
+// tiles to come.  512 threads start with 128 registers
 // each, which the groups then share out by their need.  With 192 KB of tiles
 // next to none of the SM's storage is left as L1, so a register that spills
 // costs a trip to L2: the walk lives in one warp for that reason.
@@ -43,25 +44,33 @@ struct Pre {
   static constexpr int kConvWarps = 12 - kSoftWarps;
   static constexpr int kConvRows = 128 / kConvWarps;   // keys of a tile that a warp converts
   static constexpr int kChunks = D / 64;            // 64-column parts
-  static constexpr int kKPiece = 128 * 128;         // K: 128 keys x 64 columns, f16
-  static constexpr int kKStages = 4;
-  static constexpr int kVKeys = D == 256 ? 64 : 128;   // V: kVKeys keys x D columns
+  static constexpr int kQParts = 3;                 // e4m3 parts of q at most
+  static constexpr int kQPart = 128 * D;            // one part of a tile of rows
+  static constexpr int kQTile = kQParts * kQPart;
+  static constexpr int kKCols = D < 128 ? D : 128;  // K: 128 keys x kKCols codes
+  static constexpr int kKParts = D / kKCols;
+  static constexpr int kKPiece = 128 * kKCols;
+  static constexpr int kKStages = D == 64 ? 4 : 3;
+  static constexpr int kVKeys = D == 256 ? 64 : 128;   // V: kVKeys keys x D columns, f16
   static constexpr int kVParts = 128 / kVKeys;
   static constexpr int kVPiece = kVKeys * D * 2;
   static constexpr int kVStages = D == 64 ? 4 : 2;
-  static constexpr int kQTile = 128 * D * 2;
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kTiles * kQTile;
   static constexpr int kVOff = kKOff + kKStages * kKPiece;
-  static constexpr int kMetaOff = kVOff + kVStages * kVPiece;   // [8 tiles][8 groups] ks, log2 vs, 1/vs
-  static constexpr int kPowOff = kMetaOff + 8 * 8 * 16;         // [2 pieces][rows] of q
+  // By 16-key group, of eight tiles: the scales (ks, log2 vs, 1 / vs); where
+  // the group's V begins, its page and its first row there
+  static constexpr int kMetaOff = kVOff + kVStages * kVPiece;
+  static constexpr int kWhereOff = kMetaOff + 8 * 8 * 16;
+  static constexpr int kPowOff = kWhereOff + 8 * 8 * 16;        // [2 pieces][rows] of q
   static constexpr int kRecOff = kPowOff + 2 * kRows * 4;       // [4 pieces] (Piece)
   static constexpr int kBarOff = kRecOff + 4 * 64;
   static constexpr int kQFull = 0, kQEmpty = 1, kKFull = 2, kKEmpty = kKFull + kKStages,
                        kVFull = kKEmpty + kKStages, kVEmpty = kVFull + kVStages,
                        kSFull = kVEmpty + kVStages, kPFull = kSFull + 2, kODone = kPFull + 2,
                        kDrain = kODone + 2, kRecFull = kDrain + 1, kRecEmpty = kRecFull + 4,
-                       kNumBars = kRecEmpty + 4;
+                       kTileFull = kRecEmpty + 4, kTileEmpty = kTileFull + 8,
+                       kNumBars = kTileEmpty + 8;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   static constexpr int kRedOff = (kMiscOff + 32 + 15) / 16 * 16;   // start: sums and the found entry
   static constexpr int kBytes = kRedOff + 16 * 8 + 16;
@@ -69,8 +78,8 @@ struct Pre {
   static constexpr uint32_t kTS = 0, kTO = 256, kTmemCols = 512;
   // registers a thread: the launch's 4 * 128 among the four warpgroups
   static constexpr int kRegSoft = 176;
-  static constexpr int kRegMisc = kTiles == 1 ? 112 : 48;
-  static constexpr int kRegConv = kTiles == 1 ? (512 - kRegSoft - kRegMisc) / 2 : 512 - 2 * kRegSoft - kRegMisc;
+  static constexpr int kRegMisc = kTiles == 1 ? 80 : 64;
+  static constexpr int kRegConv = (512 - kTiles * kRegSoft - kRegMisc) / (3 - kTiles);
   static_assert(kAlloc <= 227 * 1024, "shared memory budget");
   static_assert(256 + kTiles * D <= 512, "TMEM budget");
 };
@@ -84,26 +93,21 @@ __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// 16 bytes of global memory, zeros where `on` is false; and four bytes, `other`
-// where it is false.  Kept in program order with the other volatile asm, so
-// that a load is issued where it stands, a tile ahead of its use: left to the
-// compiler the loads of a tile were waited for one by one.
-__device__ __forceinline__ void load_16(uint4& x, const void* src, bool on) {
+// 16 bytes of global memory (where `on` is false: zeros).  Kept in program
+// order with the other volatile asm, so that a load is issued where it stands,
+// a tile ahead of its use: left to the compiler the loads of a tile were
+// waited for one by one.
+__device__ __forceinline__ void load_16(uint4& x, const void* src) {
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(src));
+}
+__device__ __forceinline__ void load_16_if(uint4& x, const void* src, bool on) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
       "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
       "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
       : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
       : "l"(src), "r"(static_cast<uint32_t>(on)));
-}
-__device__ __forceinline__ uint32_t load_4(const void* src, bool on, uint32_t other) {
-  uint32_t x;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.u32 %0, %3;\n\t"
-      "@p ld.global.nc.u32 %0, [%1];\n\t}"
-      : "=r"(x)
-      : "l"(src), "r"(static_cast<uint32_t>(on)), "r"(other));
-  return x;
 }
 
 // A piece of a unit, as the scheduling warp describes it to the others.
@@ -118,10 +122,62 @@ struct Piece {
   int whole;           // the piece is a whole unit
 };
 static_assert(sizeof(Piece) <= 64, "a record's place");
+struct __align__(16) Where {
+  const unsigned char* v;
+  int page, row;
+};
+
+// D[tmem] (+)= A[smem] * B[smem], both e4m3 (32 columns a product).
+__device__ __forceinline__ void mma_ss_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor of kind::f8f6f4: fp32 sums, both operands e4m3 (type
+// 0) and K-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+// Shared-memory descriptor of K-major rows of COLS bytes (128: 128-byte
+// swizzle, 64: 64-byte swizzle), eight rows after eight.
+template <int COLS>
+__device__ __forceinline__ uint64_t rows_desc(uint32_t addr) {
+  uint64_t d = smem_desc_sw128(addr, 16, 8 * COLS);
+  if constexpr (COLS == 64) d = (d & ~(7ull << 61)) | (4ull << 61);
+  return d;
+}
+// Byte offset of 16-byte chunk c of row r there.
+template <int COLS>
+__device__ __forceinline__ uint32_t row_chunk(int r, int c) {
+  return COLS == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// Four fp32 -> four e4m3 codes; x becomes what the codes leave of it.
+__device__ __forceinline__ uint32_t take_e4m3(float (&x)[4]) {
+  uint32_t w = 0;
+  #pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint16_t two;
+    uint32_t back;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(two));
+    const float2 f = unpack2<false>(back);
+    x[2 * i] -= f.x;
+    x[2 * i + 1] -= f.y;
+    w |= static_cast<uint32_t>(two) << (16 * i);
+  }
+  return w;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
+cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ FwdCacheParams p) {
   using L = Pre<D>;
   using W = Walk<L::kRows, 128>;
   extern __shared__ uint8_t smem_raw[];
@@ -134,6 +190,7 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
   long long* red = reinterpret_cast<long long*>(smem + L::kRedOff);
   longlong2* found = reinterpret_cast<longlong2*>(smem + L::kRedOff + 128);
   float4* meta = reinterpret_cast<float4*>(smem + L::kMetaOff);
+  Where* where = reinterpret_cast<Where*>(smem + L::kWhereOff);
   float* q_pow = reinterpret_cast<float*>(smem + L::kPowOff);
   auto bar = [&](int i) -> uint32_t { return sbase + L::kBarOff + 8u * i; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -143,7 +200,7 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
     mbar_init(bar(L::kQFull), L::kConvWarps);
     mbar_init(bar(L::kQEmpty), 1);
     for (int s = 0; s < L::kKStages; ++s) {
-      mbar_init(bar(L::kKFull + s), L::kConvWarps);
+      mbar_init(bar(L::kKFull + s), 1);
       mbar_init(bar(L::kKEmpty + s), 1);
     }
     for (int s = 0; s < L::kVStages; ++s) {
@@ -157,8 +214,12 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(bar(L::kRecFull + s), 1);
-      mbar_init(bar(L::kRecEmpty + s), 1 + L::kConvWarps + L::kSoftWarps);
+      mbar_init(bar(L::kRecEmpty + s), 2 + L::kConvWarps + L::kSoftWarps);
       nan_seen[s] = 0;
+    }
+    for (int s = 0; s < 8; ++s) {
+      mbar_init(bar(L::kTileFull + s), 1);
+      mbar_init(bar(L::kTileEmpty + s), 1);
     }
     mbar_init(bar(L::kDrain), 1);
     *abort = 0;
@@ -228,12 +289,96 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
         left -= s1 - at.step;
         if (left > 0) at.next_unit(p);
       }
+    } else if (warp == 14) {
+      // ----------------------------------------------------------- pages
+      // Of every tile, up to eight ahead of the products.  Four tiles at a
+      // time: lane 8 t + i finds the page and scales of group i of tile t.
+      int g = 0;
+      bool ok = true;
+      for (int np = 0; ok; ++np) {
+        if (!piece_wait(np)) break;
+        const int s0 = piece(np)->s0, s1 = piece(np)->s1, lim = piece(np)->lim, h = piece(np)->h;
+        const int* row = p.table + static_cast<long long>(piece(np)->b) * p.width;
+        piece_done(np);
+        if (s1 < 0) break;
+        for (int j = s0; ok && j < s1; j += 4) {
+          const int key = j * 128 + 16 * lane;
+          const bool on = key < lim;
+          int page = 0;
+          if (on) {
+            page = row[key >> p.page_log2];
+            if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.pages)) {
+              atomicOr(p.seq.err, kErrCache);
+              page = 0;
+            }
+          }
+          const long long sc = static_cast<long long>(page) * p.Hkv + h;
+          const float ks = on ? p.k_scale[sc] : 1.f, lv = on ? log2f(p.v_scale[sc]) : 0.f;
+          const int r = key & ((1 << p.page_log2) - 1), i = lane & 7;
+          for (int t = 0; t < min(4, s1 - j); ++t, ++g) {
+            if (g >= 8 && !wait_uniform(bar(L::kTileEmpty + (g & 7)), ((g >> 3) + 1) & 1, abort)) {
+              ok = false;
+              break;
+            }
+            if (lane >> 3 == t) {
+              meta[(g & 7) * 8 + i] = make_float4(ks, lv, ex2_approx(-lv), 0.f);
+              Where* w = where + (g & 7) * 8 + i;
+              w->v = p.v + page * p.vs.b + h * p.vs.h + r * p.vs.n;
+              w->page = page;
+              w->row = r;
+            }
+            mbar_arrive_warp(bar(L::kTileFull + (g & 7)));
+          }
+        }
+      }
+    } else if (warp == 15) {
+      // ------------------------------------------------------------ keys
+      // Codes as they are, a box of a page (at most 128 rows) at a time; rows
+      // past the keys that any row sees are left as they were (their scores
+      // are masked).
+      if (elect_one()) tma_prefetch_desc(&tm_k);
+      __syncwarp();
+      const int box_log2 = min(p.page_log2, 7);
+      int g = 0, kp = 0;
+      bool ok = true;
+      for (int np = 0; ok; ++np) {
+        if (!piece_wait(np)) break;
+        const int s0 = piece(np)->s0, s1 = piece(np)->s1, lim = piece(np)->lim, h = piece(np)->h;
+        piece_done(np);
+        if (s1 < 0) break;
+        for (int j = s0; ok && j < s1; ++j, ++g) {
+          if (!wait_uniform(bar(L::kTileFull + (g & 7)), (g >> 3) & 1, abort)) { ok = false; break; }
+          const int boxes = min(128 >> box_log2, (lim - j * 128 + (1 << box_log2) - 1) >> box_log2);
+          #pragma unroll 1
+          for (int c = 0; c < L::kKParts; ++c) {
+            const int s = kp % L::kKStages;
+            if (kp >= L::kKStages && !wait_uniform(bar(L::kKEmpty + s), (kp / L::kKStages + 1) & 1, abort)) {
+              ok = false;
+              break;
+            }
+            if (elect_one()) {
+              const uint32_t full = bar(L::kKFull + s), dst = sbase + L::kKOff + s * L::kKPiece;
+              mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * L::kKCols) << box_log2);
+              for (int i = 0; i < boxes; ++i) {
+                const Where* w = where + (g & 7) * 8 + (i << (box_log2 - 4));
+                tma_load_4d(dst + (static_cast<uint32_t>(i * L::kKCols) << box_log2), &tm_k, full,
+                            c * L::kKCols, w->row, h, w->page);
+              }
+            }
+            __syncwarp();
+            ++kp;
+          }
+        }
+      }
+      for (int i = max(0, kp - L::kKStages); i < kp; ++i)
+        drain_wait(bar(L::kKFull + i % L::kKStages), (i / L::kKStages) & 1);
     } else if (warp == 12) {
       // ---------------------------------------------------------- products
-      constexpr uint32_t kIdS = idesc_f16(128, 128, 0, 0, 0);
+      constexpr uint32_t kIdS = idesc_e4m3(128, 128);
       constexpr uint32_t kIdO = idesc_f16(128, D, 0, 0, 1);
-      const uint64_t q_desc = smem_desc_sw128(sbase + L::kQOff, 16, 1024);
-      const uint64_t k_desc = smem_desc_sw128(sbase + L::kKOff, 16, 1024);
+      const uint64_t q_desc = rows_desc<L::kKCols>(sbase + L::kQOff);
+      const uint64_t k_desc = rows_desc<L::kKCols>(sbase + L::kKOff);
+      const int q_parts = p.bf16 ? 2 : 3;
       const uint64_t v_desc = smem_desc_sw128(sbase + L::kVOff, L::kVKeys * 128, 1024);
       int kp = 0, vp = 0;                 // pieces of K and V consumed
       int pf[2] = {0, 0};                 // P_FULL phases consumed, by score buffer
@@ -242,16 +387,19 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
       // `first` on; `free`: the pieces' last use
       auto scores = [&](int u, int buf, int first, bool free) -> bool {
         #pragma unroll 1
-        for (int c = 0; c < L::kChunks; ++c) {
+        for (int c = 0; c < L::kKParts; ++c) {
           const int n = first + c, s = n % L::kKStages;
           if (!wait_uniform(bar(L::kKFull + s), (n / L::kKStages) & 1, abort)) return false;
           tc_fence_after();
           const uint64_t ks = desc_add(k_desc, s * L::kKPiece);
-          const uint64_t qs = desc_add(q_desc, u * L::kQTile + c * (128 * 128));
-          #pragma unroll
-          for (int w = 0; w < 4; ++w)
-            mma_ss(tmem + L::kTS + 128 * buf, desc_add(qs, w * 32), desc_add(ks, w * 32), kIdS,
-                   (c > 0 || w > 0) ? 1u : 0u);
+          #pragma unroll 1
+          for (int q = 0; q < q_parts; ++q) {
+            const uint64_t qs = desc_add(q_desc, u * L::kQTile + q * L::kQPart + c * (128 * L::kKCols));
+            #pragma unroll
+            for (int w = 0; w < L::kKCols / 32; ++w)
+              mma_ss_e4m3(tmem + L::kTS + 128 * buf, desc_add(qs, w * 32), desc_add(ks, w * 32), kIdS,
+                          (c > 0 || q > 0 || w > 0) ? 1u : 0u);
+          }
           if (free) mma_commit(bar(L::kKEmpty + s));
         }
         mma_commit(bar(L::kSFull + buf));
@@ -272,7 +420,7 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
         }
         return true;
       };
-      int g = 0;   // tiles so far (d = 256: selects the score buffer)
+      int g = 0;   // tiles so far
       for (int np = 0; ok; ++np) {
         if (!piece_wait(np)) break;
         // (read from lane 0: the same in every lane, on the uniform datapath)
@@ -290,7 +438,7 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
           ok = scores(0, g & 1, kp, true);
           for (int j = w.s0; ok && j < w.s1; ++j, ++g) {
             if (j + 1 < w.s1) {
-              if (!scores(0, (g + 1) & 1, kp + L::kChunks, true)) { ok = false; break; }
+              if (!scores(0, (g + 1) & 1, kp + L::kKParts, true)) { ok = false; break; }
             } else {
               mma_commit(bar(L::kQEmpty));
             }
@@ -298,7 +446,8 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
             tc_fence_after();
             if (!values(0, g & 1, vp, j == w.s0, true)) { ok = false; break; }
             mma_commit(bar(L::kODone));
-            kp += L::kChunks;
+            mma_commit(bar(L::kTileEmpty + (g & 7)));
+            kp += L::kKParts;
             vp += L::kVParts;
           }
         } else {
@@ -306,7 +455,7 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
           if (a0) ok = scores(0, 0, kp, !b0);
           if (ok && b0) ok = scores(1, 1, kp, true);
           if (w.s1 - w.s0 == 1) mma_commit(bar(L::kQEmpty));
-          for (int j = w.s0; ok && j < w.s1; ++j) {
+          for (int j = w.s0; ok && j < w.s1; ++j, ++g) {
             // tile u takes part in this step (v) and in the next (n)
             const bool v0 = j < w.end[0], v1 = j < w.end[1];
             const bool n0 = j + 1 < w.end[0], n1 = j + 1 < w.end[1];
@@ -318,10 +467,11 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
               tc_fence_after();
               ok = values(u, u, vp, j == w.s0, u == 1 || !v1);
               if (ok && j + 1 == w.end[u]) mma_commit(bar(L::kODone + u));
-              if (ok && (u ? n1 : n0)) ok = scores(u, u, kp + L::kChunks, u == 1 || !n1);
+              if (ok && (u ? n1 : n0)) ok = scores(u, u, kp + L::kKParts, u == 1 || !n1);
             }
+            mma_commit(bar(L::kTileEmpty + (g & 7)));
             if (j + 2 == w.s1) mma_commit(bar(L::kQEmpty));
-            kp += L::kChunks;
+            kp += L::kKParts;
             vp += L::kVParts;
           }
         }
@@ -339,9 +489,7 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
     // Codes of one tile: rows kConvRows cw + 8 i + r8, 16 columns of each
     // 64-column part.  Each part's registers are loaded again, for the next
     // tile, as soon as it has been written: a tile's time hides the latency.
-    uint4 kr[L::kChunks][kI], vr[L::kChunks][kI];
-    int page[kI];
-    float ks = 1.f, vs = 1.f;
+    uint4 vr[L::kChunks][kI];
     int tile = 0, lim = 0, b = 0, h = 0;      // the tile that is loaded next, and its piece
     auto enter = [&](int np) {
       tile = piece(np)->s0;
@@ -349,57 +497,43 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
       b = piece(np)->b;
       h = piece(np)->h;
     };
-    auto pages_of = [&]() {
-      const int* row = p.table + static_cast<long long>(b) * p.width;
+    // Rows past the keys that any row sees are zeros.  at: this thread's place
+    // in the first of the warp's groups (of tile gn), by group and 8-row half.
+    const long long v_row = r8 * p.vs.n + 16 * c16, v_half = 8 * p.vs.n;
+    auto load = [&](int gn, int c) {
+      const Where* w = where + (gn & 7) * 8 + (kI / 2) * cw;
+      const bool whole = tile * 128 + 128 <= lim;
       #pragma unroll
       for (int i = 0; i < kI; ++i) {
-        const int key = tile * 128 + L::kConvRows * cw + 8 * i;   // (a page holds whole groups of 16)
-        page[i] = static_cast<int>(load_4(row + (key >> p.page_log2), key < lim, 0u));
-      }
-      #pragma unroll
-      for (int i = 0; i < kI; ++i)
-        if (static_cast<unsigned>(page[i]) >= static_cast<unsigned>(p.pages)) {
-          atomicOr(p.seq.err, kErrCache);
-          page[i] = 0;
-        }
-      // the scales of the warp's 16-key groups, one a lane
-      int mine = page[0];
-      if constexpr (kI > 2) mine = lane == 0 ? page[0] : page[2];
-      const long long sc = static_cast<long long>(mine) * p.Hkv + h;
-      const bool on = lane < kI / 2 && tile * 128 + L::kConvRows * cw + 16 * lane < lim;
-      ks = __uint_as_float(load_4(p.k_scale + sc, on, 0x3f800000u));
-      vs = __uint_as_float(load_4(p.v_scale + sc, on, 0x3f800000u));
-    };
-    // rows past the keys that any row sees are zeros
-    auto load = [&](const unsigned char* base, const Strides& st, int c, uint4 (&x)[kI]) {
-      const unsigned char* head = base + h * st.h + 64 * c + 16 * c16;
-      #pragma unroll
-      for (int i = 0; i < kI; ++i) {
-        const int key = tile * 128 + L::kConvRows * cw + 8 * i + r8;
-        load_16(x[i], head + page[i] * st.b + (key & ((1 << p.page_log2) - 1)) * st.n, key < lim);
+        const unsigned char* src = w[i / 2].v + v_row + (i & 1 ? v_half : 0) + 64 * c;
+        if (whole) load_16(vr[c][i], src);
+        else load_16_if(vr[c][i], src, tile * 128 + L::kConvRows * cw + 8 * i + r8 < lim);
       }
     };
-    auto put = [&](uint32_t rows, int r, const uint4& x) {
+    auto tile_wait = [&](int gn) {
+      return wait_uniform(bar(L::kTileFull + (gn & 7)), (gn >> 3) & 1, abort);
+    };
+    // this thread's two 16-byte places in a row of 64 f16 columns
+    const uint32_t place0 = r8 * 128 + (((2 * c16) ^ r8) << 4);
+    const uint32_t place1 = r8 * 128 + (((2 * c16 + 1) ^ r8) << 4);
+    auto put = [&](uint32_t rows, const uint4& x) {     // rows: of eight rows
       uint32_t w[8];
       widen4(x.x, w[0], w[1]);
       widen4(x.y, w[2], w[3]);
       widen4(x.z, w[4], w[5]);
       widen4(x.w, w[6], w[7]);
-      const uint32_t row = rows + r * 128;
-      st_shared_v4(row + (((2 * c16) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
-      st_shared_v4(row + (((2 * c16 + 1) ^ (r & 7)) << 4), w[4], w[5], w[6], w[7]);
+      st_shared_v4(rows + place0, w[0], w[1], w[2], w[3]);
+      st_shared_v4(rows + place1, w[4], w[5], w[6], w[7]);
     };
     bool ok = piece_wait(0);
     bool more = ok;
     if (ok) {
       enter(0);
-      pages_of();
+      ok = tile_wait(0);
       #pragma unroll
-      for (int c = 0; c < L::kChunks; ++c) load(p.k, p.ks, c, kr[c]);
-      #pragma unroll
-      for (int c = 0; c < L::kChunks; ++c) load(p.v, p.vs, c, vr[c]);
+      for (int c = 0; c < L::kChunks; ++c) load(0, c);
     }
-    int kp = 0, vp = 0, g = 0;
+    int vp = 0, g = 0;
     for (int np = 0; ok && more; ++np) {
       // ---- q: rows as f16, once the last scores of the piece before are done
       if (np > 0 && !wait_uniform(bar(L::kQEmpty), (np - 1) & 1, abort)) break;
@@ -419,35 +553,43 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
           for (int k = 0; k < kBatch; ++k) {
             const int r = row0 + i0 + k * kPer;
             const int i = r / p.seq.G;
-            load_16(x[k], src + (r - i * p.seq.G) * p.qs.h + i * p.qs.n, r < p.rows && i < live);
+            load_16_if(x[k], src + (r - i * p.seq.G) * p.qs.h + i * p.qs.n, r < p.rows && i < live);
           }
           #pragma unroll
           for (int k = 0; k < kBatch; ++k) {
             const int rr = cw * kRowsW + i0 + k * kPer + rl;
-            uint32_t y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-            float up = 1.f, down = 1.f;
-            if (p.bf16) {
-              float amax = 0.f;
-              #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const float2 f = unpack2<true>(y[c]);
-                amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-              }
-              #pragma unroll
-              for (int m = kLanes / 2; m > 0; m >>= 1)
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-              row_power(amax, &up, &down);
-              #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const float2 f = unpack2<true>(y[c]);
-                y[c] = pack2<false>(f.x * down, f.y * down);
-              }
+            const uint32_t y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            float f[2][4];
+            float amax = 0.f;
+            #pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const float2 t = p.bf16 ? unpack2<true>(y[c]) : unpack2<false>(y[c]);
+              f[c >> 1][2 * (c & 1)] = t.x;
+              f[c >> 1][2 * (c & 1) + 1] = t.y;
+              amax = fmaxf(amax, fmaxf(fabsf(t.x), fabsf(t.y)));
             }
-            if (cl == 0) q_pow[(np & 1) * L::kRows + rr] = up;
+            #pragma unroll
+            for (int m = kLanes / 2; m > 0; m >>= 1)
+              amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+            float up, down;
+            row_power(amax, &up, &down);
+            #pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              // infinities have no code: NaN, as their row's scores are
+              const float t = f[c >> 2][c & 3] * down * 128.f;
+              f[c >> 2][c & 3] = fabsf(t) < __uint_as_float(0x7f800000u) ? t : __uint_as_float(0x7fffffffu);
+            }
+            if (cl == 0) q_pow[(np & 1) * L::kRows + rr] = up * 0.0078125f;
             const int r = rr & 127;
-            st_shared_v4(sbase + L::kQOff + (rr >> 7) * L::kQTile + (cl >> 3) * (128 * 128) +
-                             r * 128 + (((cl & 7) ^ (r & 7)) << 4),
-                         y[0], y[1], y[2], y[3]);
+            const uint32_t to = sbase + L::kQOff + (rr >> 7) * L::kQTile +
+                                (8 * cl / L::kKCols) * (128 * L::kKCols) +
+                                row_chunk<L::kKCols>(r, (cl >> 1) % (L::kKCols / 16)) + 8 * (cl & 1);
+            #pragma unroll
+            for (int q = 0; q < 3; ++q) {
+              if (q == 2 && p.bf16) break;
+              const uint32_t w0 = take_e4m3(f[0]), w1 = take_e4m3(f[1]);
+              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to + q * L::kQPart), "r"(w0), "r"(w1) : "memory");
+            }
           }
         }
       }
@@ -455,7 +597,6 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
       mbar_arrive_warp(bar(L::kQFull));
       const int full = piece(np)->all, s1 = piece(np)->s1;
       for (int j = piece(np)->s0; j < s1; ++j, ++g) {
-        const float ks_now = ks, vs_now = vs;
         // on to the next tile
         if (j + 1 < s1) {
           ++tile;
@@ -465,29 +606,8 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
           more = ok && piece(np + 1)->s1 >= 0;
           if (more) enter(np + 1);
         }
+        if (more && ok) ok = tile_wait(g + 1);
         if (!ok) break;
-        if (more) pages_of();
-        #pragma unroll
-        for (int c = 0; c < L::kChunks; ++c) {
-          const int s = kp % L::kKStages;
-          if (kp >= L::kKStages && ok)
-            ok = wait_uniform(bar(L::kKEmpty + s), (kp / L::kKStages + 1) & 1, abort);
-          if (ok) {
-            if (c == 0 && lane < kI / 2) {
-              // when K of tile g is written the scores of tile g - 4 are done,
-              // so P V of tile g - 5 is: eight tiles of these live at a time
-              const float lv = log2f(vs_now);
-              meta[(g & 7) * 8 + (kI / 2) * cw + lane] = make_float4(ks_now, lv, ex2_approx(-lv), 0.f);
-            }
-            #pragma unroll
-            for (int i = 0; i < kI; ++i)
-              put(sbase + L::kKOff + s * L::kKPiece, L::kConvRows * cw + 8 * i + r8, kr[c][i]);
-            fence_proxy_async_smem();
-            mbar_arrive_warp(bar(L::kKFull + s));
-          }
-          ++kp;
-          if (more) load(p.k, p.ks, c, kr[c]);
-        }
         // V: this warp's rows lie in one piece of the tile
         const int n = vp + L::kConvRows * cw / L::kVKeys, s = n % L::kVStages;
         vp += L::kVParts;
@@ -517,13 +637,14 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
         for (int c = 0; c < L::kChunks; ++c) {
           #pragma unroll
           for (int i = 0; i < kI; ++i)
-            put(sbase + L::kVOff + s * L::kVPiece + c * (L::kVKeys * 128),
-                (L::kConvRows * cw + 8 * i + r8) & (L::kVKeys - 1), vr[c][i]);
+            put(sbase + L::kVOff + s * L::kVPiece + c * (L::kVKeys * 128) +
+                    ((L::kConvRows * cw + 8 * i) & (L::kVKeys - 1)) * 128,
+                vr[c][i]);
           if (c + 1 == L::kChunks) {
             fence_proxy_async_smem();
             mbar_arrive_warp(bar(L::kVFull + s));
           }
-          if (more) load(p.v, p.vs, c, vr[c]);
+          if (more) load(g + 1, c);
         }
       }
     }
@@ -732,7 +853,7 @@ cache_prefill_kernel(const __grid_constant__ FwdCacheParams p) {
 }
 
 template <int D>
-cudaError_t launch(FwdCacheParams& p, int sms, cudaStream_t stream) {
+cudaError_t launch(const Cache& cache, FwdCacheParams& p, int sms, cudaStream_t stream) {
   static std::atomic<bool> set[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -743,8 +864,12 @@ cudaError_t launch(FwdCacheParams& p, int sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     set[dev & 63] = true;
   }
+  CUtensorMap tk;
+  if ((e = make_tmap_u8_4d(&tk, cache.k, D, cache.page, cache.Hkv, cache.pages, cache.ks,
+                           Pre<D>::kKCols, std::min(cache.page, 128))) != cudaSuccess)
+    return e;
   p.ctas = sms;
-  kern<<<p.ctas, kThreads, Pre<D>::kAlloc, stream>>>(p);
+  kern<<<p.ctas, kThreads, Pre<D>::kAlloc, stream>>>(tk, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_cache_merge<D, Pre<D>::kRows, 128>(p, stream);
 }
@@ -756,9 +881,9 @@ int cache_prefill_rows(int d) { return d == 256 ? Pre<256>::kRows : Pre<128>::kR
 cudaError_t launch_cache_prefill(const Cache& cache, FwdCacheParams& p, int sms,
                                  cudaStream_t stream) {
   switch (cache.d) {
-    case 64: return launch<64>(p, sms, stream);
-    case 128: return launch<128>(p, sms, stream);
-    case 256: return launch<256>(p, sms, stream);
+    case 64: return launch<64>(cache, p, sms, stream);
+    case 128: return launch<128>(cache, p, sms, stream);
+    case 256: return launch<256>(cache, p, sms, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -120,12 +120,19 @@ def attend(q, k, v, table, lens, new, causal, scale):
                 L = torch.logsumexp(S, 0)
                 P = torch.exp(S - L)
                 o[b, h, i], lse[b, h, i] = P @ V[:see], L
-                # scores: products of 16-bit values summed in fp32 (2^-23 a
-                # step, in any order), q's elements to 2^-25 of the largest;
-                # exp2, the scaling and the running sums 2^-20 together
+                # scores: products summed in fp32 (2^-23 a step, in any
+                # order); exp2, the scaling and the running sums 2^-20
+                # together.  q is exact as two (bf16, 8 bits) or three (f16, 11
+                # bits) e4m3 values of 4 bits each where the last of them is a
+                # multiple of e4m3's step 2^-9: the row's largest element is
+                # brought to [2^7, 2^8), so for elements of at least 2, 2^-6 of
+                # the largest or more; smaller ones are off by half a step,
+                # 2^-10, at most, 2^-17 of the largest element
                 size = float((K[:see].abs() @ x.abs()).max()) * scale
-                tail = float(x.abs().max() * K[:see].abs().max()) * scale * d
-                ds = size * d * 2.0 ** -23 + tail * 2.0 ** -25 + 2.0 ** -20 * (1 + float(S.abs().max()))
+                top = float(x.abs().max())
+                small = (x.abs() < top * 2.0 ** -6).double()
+                tail = top * 2.0 ** -17 * float((K[:see].abs() @ small).max()) * scale
+                ds = size * d * 2.0 ** -23 + tail + 2.0 ** -20 * (1 + float(S.abs().max()))
                 # weights: half a step of f16, and 2^-25 of the largest for the small ones
                 o_slack[b, h, i] = (P @ V[:see].abs()) * (2.0 ** -11 + 2 * ds + see * 2.0 ** -24) \
                     + see * 2.0 ** -25 * 448 * float(v.scales.max())

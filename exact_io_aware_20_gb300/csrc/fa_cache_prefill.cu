@@ -157,6 +157,10 @@ __device__ __forceinline__ uint32_t row_chunk(int r, int c) {
   return COLS == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
+// The larger of two pairs of 16-bit patterns without sign (of bf16 and f16
+// magnitudes: NaN is the largest).
+__device__ __forceinline__ uint32_t max_16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+
 // Four fp32 -> four e4m3 codes; x becomes what the codes leave of it.
 __device__ __forceinline__ uint32_t take_e4m3(float (&x)[4]) {
   uint32_t w = 0;
@@ -526,87 +530,84 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
       st_shared_v4(rows + place1, w[4], w[5], w[6], w[7]);
     };
     bool ok = piece_wait(0);
-    bool more = ok;
-    if (ok) {
-      enter(0);
-      ok = tile_wait(0);
-      #pragma unroll
-      for (int c = 0; c < L::kChunks; ++c) load(0, c);
-    }
+    bool more = ok && piece(0)->s1 >= 0;
     int vp = 0, g = 0;
     for (int np = 0; ok && more; ++np) {
-      // ---- q: rows as f16, once the last scores of the piece before are done
+      enter(np);
+      // ---- q, once the last scores of the piece before are done.  A row is
+      // scaled by a power of two to [2^7, 2^8) and becomes e4m3 parts, each
+      // what the ones before have left.
+      constexpr int kLanes = D / 8, kPer = 32 / kLanes;        // lanes of a row, rows at a time
+      constexpr int kRowsW = L::kRows / L::kConvWarps, kBatch = 8;
+      const int rl = lane / kLanes, cl = lane % kLanes;
+      const uint32_t q_to = sbase + L::kQOff + (8 * cl / L::kKCols) * (128 * L::kKCols) + 8 * (cl & 1);
+      const int row0 = piece(np)->row0 + cw * kRowsW + rl, live = piece(np)->n;
+      const uint16_t* src = p.q + b * p.qs.b + h * p.seq.G * p.qs.h + 8 * cl;
+      auto q_load = [&](uint4 (&x)[kBatch], int i0) {
+        #pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int r = row0 + i0 + k * kPer, i = r / p.seq.G;
+          load_16_if(x[k], src + (r - i * p.seq.G) * p.qs.h + i * p.qs.n, r < p.rows && i < live);
+        }
+      };
+      uint4 x[kBatch];
+      q_load(x, 0);
       if (np > 0 && !wait_uniform(bar(L::kQEmpty), (np - 1) & 1, abort)) break;
       // the next piece's flag: no converting warp is there before this one has
       // announced this piece's q, and the results of piece np - 3 are written
       if (cw == 0 && lane == 0) nan_seen[(np + 1) & 3] = 0;
-      {
-        constexpr int kLanes = D / 8, kPer = 32 / kLanes;        // lanes of a row, rows at a time
-        constexpr int kRowsW = L::kRows / L::kConvWarps, kBatch = 4;
-        const int rl = lane / kLanes, cl = lane % kLanes;
-        const int row0 = piece(np)->row0 + cw * kRowsW + rl, live = piece(np)->n;
-        const uint16_t* src = p.q + b * p.qs.b + h * p.seq.G * p.qs.h + 8 * cl;
-        #pragma unroll 1
-        for (int i0 = 0; i0 < kRowsW; i0 += kPer * kBatch) {
-          uint4 x[kBatch];
+      #pragma unroll 1
+      for (int i0 = 0; i0 < kRowsW; i0 += kPer * kBatch) {
+        uint32_t top[kBatch];      // of the magnitudes, two lanes of 16 bits
+        #pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          top[k] = max_16x2(max_16x2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu),
+                            max_16x2(x[k].z & 0x7fff7fffu, x[k].w & 0x7fff7fffu));
+        #pragma unroll
+        for (int m = kLanes / 2; m > 0; m >>= 1)
           #pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const int r = row0 + i0 + k * kPer;
-            const int i = r / p.seq.G;
-            load_16_if(x[k], src + (r - i * p.seq.G) * p.qs.h + i * p.qs.n, r < p.rows && i < live);
+          for (int k = 0; k < kBatch; ++k) top[k] = max_16x2(top[k], __shfl_xor_sync(0xffffffffu, top[k], m));
+        #pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int rr = cw * kRowsW + i0 + k * kPer + rl, r = rr & 127;
+          const uint32_t top1 = max(top[k] & 0xffffu, top[k] >> 16);
+          float up, down;
+          const float amax = p.bf16 ? __uint_as_float(top1 << 16) : unpack2<false>(top1).x;
+          row_power(amax, &up, &down);
+          // (infinities have no code: their row is NaN, as its scores are)
+          down = amax < __uint_as_float(0x7f800000u) ? down * 128.f : __uint_as_float(0x7fffffffu);
+          if (cl == 0) q_pow[(np & 1) * L::kRows + rr] = up * 0.0078125f;
+          float f[2][4];
+          const uint32_t y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+          #pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float2 t = p.bf16 ? unpack2<true>(y[c]) : unpack2<false>(y[c]);
+            f[c >> 1][2 * (c & 1)] = t.x * down;
+            f[c >> 1][2 * (c & 1) + 1] = t.y * down;
           }
+          const uint32_t to = q_to + (rr >> 7) * L::kQTile + row_chunk<L::kKCols>(r, (cl >> 1) % (L::kKCols / 16));
           #pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            const int rr = cw * kRowsW + i0 + k * kPer + rl;
-            const uint32_t y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-            float f[2][4];
-            float amax = 0.f;
-            #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const float2 t = p.bf16 ? unpack2<true>(y[c]) : unpack2<false>(y[c]);
-              f[c >> 1][2 * (c & 1)] = t.x;
-              f[c >> 1][2 * (c & 1) + 1] = t.y;
-              amax = fmaxf(amax, fmaxf(fabsf(t.x), fabsf(t.y)));
-            }
-            #pragma unroll
-            for (int m = kLanes / 2; m > 0; m >>= 1)
-              amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-            float up, down;
-            row_power(amax, &up, &down);
-            #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              // infinities have no code: NaN, as their row's scores are
-              const float t = f[c >> 2][c & 3] * down * 128.f;
-              f[c >> 2][c & 3] = fabsf(t) < __uint_as_float(0x7f800000u) ? t : __uint_as_float(0x7fffffffu);
-            }
-            if (cl == 0) q_pow[(np & 1) * L::kRows + rr] = up * 0.0078125f;
-            const int r = rr & 127;
-            const uint32_t to = sbase + L::kQOff + (rr >> 7) * L::kQTile +
-                                (8 * cl / L::kKCols) * (128 * L::kKCols) +
-                                row_chunk<L::kKCols>(r, (cl >> 1) % (L::kKCols / 16)) + 8 * (cl & 1);
-            #pragma unroll
-            for (int q = 0; q < 3; ++q) {
-              if (q == 2 && p.bf16) break;
-              const uint32_t w0 = take_e4m3(f[0]), w1 = take_e4m3(f[1]);
-              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to + q * L::kQPart), "r"(w0), "r"(w1) : "memory");
-            }
+          for (int q = 0; q < 3; ++q) {
+            if (q == 2 && p.bf16) break;
+            const uint32_t w0 = take_e4m3(f[0]), w1 = take_e4m3(f[1]);
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to + q * L::kQPart), "r"(w0), "r"(w1) : "memory");
           }
         }
+        if (i0 + kPer * kBatch < kRowsW) q_load(x, i0 + kPer * kBatch);
       }
       fence_proxy_async_smem();
       mbar_arrive_warp(bar(L::kQFull));
+      // the first tile's values (they are not needed before its scores and
+      // weights are done)
+      ok = tile_wait(g);
+      if (!ok) break;
+      #pragma unroll
+      for (int c = 0; c < L::kChunks; ++c) load(g, c);
       const int full = piece(np)->all, s1 = piece(np)->s1;
       for (int j = piece(np)->s0; j < s1; ++j, ++g) {
-        // on to the next tile
-        if (j + 1 < s1) {
-          ++tile;
-        } else {
-          piece_done(np);
-          ok = piece_wait(np + 1);
-          more = ok && piece(np + 1)->s1 >= 0;
-          if (more) enter(np + 1);
-        }
-        if (more && ok) ok = tile_wait(g + 1);
+        const bool next = j + 1 < s1;      // the piece has another tile
+        ++tile;
+        if (next) ok = tile_wait(g + 1);
         if (!ok) break;
         // V: this warp's rows lie in one piece of the tile
         const int n = vp + L::kConvRows * cw / L::kVKeys, s = n % L::kVStages;
@@ -644,9 +645,13 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
             fence_proxy_async_smem();
             mbar_arrive_warp(bar(L::kVFull + s));
           }
-          if (more) load(g + 1, c);
+          if (next) load(g + 1, c);
         }
       }
+      if (!ok) break;
+      piece_done(np);
+      ok = piece_wait(np + 1);
+      more = ok && piece(np + 1)->s1 >= 0;
     }
   } else {
     // ------------------------------------------------------------ softmax

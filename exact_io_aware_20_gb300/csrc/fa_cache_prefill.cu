@@ -110,6 +110,21 @@ __device__ __forceinline__ void load_16_if(uint4& x, const void* src, bool on) {
       : "l"(src), "r"(static_cast<uint32_t>(on)));
 }
 
+// Reads of shared memory by its own address: through a generic pointer they
+// queue with the loads of global memory (the eight scales of a tile's first
+// pass took 600 clocks instead of 100).
+__device__ __forceinline__ float4 ld_shared_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ const unsigned char* ld_shared_ptr(uint32_t addr) {
+  unsigned long long v;
+  asm volatile("ld.shared.u64 %0, [%1];" : "=l"(v) : "r"(addr));
+  return reinterpret_cast<const unsigned char*>(v);
+}
+
 // A piece of a unit, as the scheduling warp describes it to the others.
 struct Piece {
   int s0, s1;          // its steps; s1 < 0: there are no more pieces
@@ -178,7 +193,9 @@ __device__ __forceinline__ uint32_t take_e4m3(float (&x)[4]) {
   return w;
 }
 
-template <int D>
+// SEG: keys that share their scales for certain (64 when a page holds at least
+// as many, 16 otherwise).
+template <int D, int SEG>
 __global__ void __launch_bounds__(kThreads, 1)
 cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ FwdCacheParams p) {
@@ -505,11 +522,11 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
     // in the first of the warp's groups (of tile gn), by group and 8-row half.
     const long long v_row = r8 * p.vs.n + 16 * c16, v_half = 8 * p.vs.n;
     auto load = [&](int gn, int c) {
-      const Where* w = where + (gn & 7) * 8 + (kI / 2) * cw;
+      const uint32_t w = sbase + L::kWhereOff + ((gn & 7) * 8 + (kI / 2) * cw) * 16;
       const bool whole = tile * 128 + 128 <= lim;
       #pragma unroll
       for (int i = 0; i < kI; ++i) {
-        const unsigned char* src = w[i / 2].v + v_row + (i & 1 ? v_half : 0) + 64 * c;
+        const unsigned char* src = ld_shared_ptr(w + 16 * (i / 2)) + v_row + (i & 1 ? v_half : 0) + 64 * c;
         if (whole) load_16(vr[c][i], src);
         else load_16_if(vr[c][i], src, tile * 128 + L::kConvRows * cw + 8 * i + r8 < lim);
       }
@@ -698,15 +715,20 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
           for (int i = 0; i < 128; ++i)
             if (i >= lim) s[i] = -INFINITY;
         }
-        const float4* mt = meta + ((g + j - s0) & 7) * 8;
+        const uint32_t mt = sbase + L::kMetaOff + ((g + j - s0) & 7) * 128;
         float top = kNoMax;
         #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const float* x = s + 16 * c;
-          const float a = fmax3(fmax3(x[0], x[1], x[2]), fmax3(x[3], x[4], x[5]), fmax3(x[6], x[7], x[8]));
-          const float b = fmax3(fmax3(x[9], x[10], x[11]), fmax3(x[12], x[13], x[14]), x[15]);
-          const float2 sc = *reinterpret_cast<const float2*>(mt + c);
-          top = fmaxf(top, fmaf(fmaxf(a, b), row_scale * sc.x, sc.y));
+        for (int c = 0; c < 128 / SEG; ++c) {
+          float part[4];
+          #pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float* x = s + SEG * c + SEG / 4 * k;
+            part[k] = fmax3(x[0], x[1], fmaxf(x[2], x[3]));
+            #pragma unroll
+            for (int i = 4; i < SEG / 4; i += 2) part[k] = fmax3(part[k], x[i], x[i + 1]);
+          }
+          const float4 sc = ld_shared_f4(mt + 16 * (SEG / 16) * c);
+          top = fmaxf(top, fmaf(fmax3(part[0], part[1], fmaxf(part[2], part[3])), row_scale * sc.x, sc.y));
         }
         const bool grow = top > m + kGrow;
         const bool any = __any_sync(0xffffffffu, grow);
@@ -719,25 +741,26 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         // the weights over S as f16, 32 columns at a time
         #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
+        for (int seg = 0; seg < 128 / SEG; ++seg) {
+          const float4 sc = ld_shared_f4(mt + 16 * (SEG / 16) * seg);
+          const float ksr = row_scale * sc.x, sub = sc.y - m;
+          const f2 k2 = {ksr, ksr}, m2 = {sub, sub};
+          f2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
           #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float4 sc = mt[2 * c + h];
-            const float ksr = row_scale * sc.x, sub = sc.y - m;
-            const f2 k2 = {ksr, ksr}, m2 = {sub, sub};
-            f2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+          for (int c = 0; c < SEG / 16; ++c) {
+            uint32_t pk[8];
             #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const f2 arg = ffma2(f2{s[32 * c + 16 * h + 2 * i], s[32 * c + 16 * h + 2 * i + 1]}, k2, m2);
+              const float* x = s + SEG * seg + 16 * c + 2 * i;
+              const f2 arg = ffma2(f2{x[0], x[1]}, k2, m2);
               const f2 pe = {ex2_approx(arg.x), ex2_approx(arg.y)};
-              pk[8 * h + i] = pack2<false>(pe.x, pe.y);
+              pk[i] = pack2<false>(pe.x, pe.y);
               sum[i & 1] = fadd2(sum[i & 1], pe);
             }
-            const f2 all = fadd2(sum[0], sum[1]);
-            l = fmaf(all.x + all.y, sc.z, l);
+            tmem_st8(tS + SEG / 2 * seg + 8 * c, pk);
           }
-          tmem_st16(tS + 16 * c, pk);
+          const f2 all = fadd2(sum[0], sum[1]);
+          l = fmaf(all.x + all.y, sc.z, l);
         }
         tmem_st_wait();
         if constexpr (L::kTiles == 1) {
@@ -857,13 +880,13 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
   }
 }
 
-template <int D>
-cudaError_t launch(const Cache& cache, FwdCacheParams& p, int sms, cudaStream_t stream) {
+template <int D, int SEG>
+cudaError_t launch_seg(const Cache& cache, FwdCacheParams& p, int sms, cudaStream_t stream) {
   static std::atomic<bool> set[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  auto kern = cache_prefill_kernel<D>;
+  auto kern = cache_prefill_kernel<D, SEG>;
   if (!set[dev & 63]) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Pre<D>::kAlloc);
     if (e != cudaSuccess) return e;
@@ -877,6 +900,12 @@ cudaError_t launch(const Cache& cache, FwdCacheParams& p, int sms, cudaStream_t 
   kern<<<p.ctas, kThreads, Pre<D>::kAlloc, stream>>>(tk, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_cache_merge<D, Pre<D>::kRows, 128>(p, stream);
+}
+
+template <int D>
+cudaError_t launch(const Cache& cache, FwdCacheParams& p, int sms, cudaStream_t stream) {
+  return cache.page >= 64 ? launch_seg<D, 64>(cache, p, sms, stream)
+                          : launch_seg<D, 16>(cache, p, sms, stream);
 }
 
 }  // namespace

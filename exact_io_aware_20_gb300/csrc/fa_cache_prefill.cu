@@ -176,21 +176,15 @@ __device__ __forceinline__ uint32_t row_chunk(int r, int c) {
 // magnitudes: NaN is the largest).
 __device__ __forceinline__ uint32_t max_16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
 
-// Four fp32 -> four e4m3 codes; x becomes what the codes leave of it.
-__device__ __forceinline__ uint32_t take_e4m3(float (&x)[4]) {
-  uint32_t w = 0;
-  #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint16_t two;
-    uint32_t back;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(two));
-    const float2 f = unpack2<false>(back);
-    x[2 * i] -= f.x;
-    x[2 * i + 1] -= f.y;
-    w |= static_cast<uint32_t>(two) << (16 * i);
-  }
-  return w;
+// Two f16 -> two e4m3 codes (the low 16 bits); x becomes what the codes leave
+// of it (exact in f16).
+__device__ __forceinline__ uint32_t take_e4m3(uint32_t& x) {
+  uint16_t two;
+  uint32_t back;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(two) : "r"(x));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(two));
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(back));
+  return two;
 }
 
 // SEG: keys that share their scales for certain (64 when a page holds at least
@@ -235,7 +229,8 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(bar(L::kRecFull + s), 1);
-      mbar_init(bar(L::kRecEmpty + s), 2 + L::kConvWarps + L::kSoftWarps);
+      // (read by the products, pages and keys warps, the converters and softmax)
+      mbar_init(bar(L::kRecEmpty + s), 3 + L::kConvWarps + L::kSoftWarps);
       nan_seen[s] = 0;
     }
     for (int s = 0; s < 8; ++s) {
@@ -555,7 +550,8 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
       // scaled by a power of two to [2^7, 2^8) and becomes e4m3 parts, each
       // what the ones before have left.
       constexpr int kLanes = D / 8, kPer = 32 / kLanes;        // lanes of a row, rows at a time
-      constexpr int kRowsW = L::kRows / L::kConvWarps, kBatch = 8;
+      constexpr int kRowsW = L::kRows / L::kConvWarps;
+      constexpr int kBatch = 4;
       const int rl = lane / kLanes, cl = lane % kLanes;
       const uint32_t q_to = sbase + L::kQOff + (8 * cl / L::kKCols) * (128 * L::kKCols) + 8 * (cl & 1);
       const int row0 = piece(np)->row0 + cw * kRowsW + rl, live = piece(np)->n;
@@ -564,7 +560,8 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
         #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
           const int r = row0 + i0 + k * kPer, i = r / p.seq.G;
-          load_16_if(x[k], src + (r - i * p.seq.G) * p.qs.h + i * p.qs.n, r < p.rows && i < live);
+          load_16_if(x[k], src + (r - i * p.seq.G) * p.qs.h + i * p.qs.n,
+                     i0 < kRowsW && r < p.rows && i < live);
         }
       };
       uint4 x[kBatch];
@@ -573,8 +570,12 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
       // the next piece's flag: no converting warp is there before this one has
       // announced this piece's q, and the results of piece np - 3 are written
       if (cw == 0 && lane == 0) nan_seen[(np + 1) & 3] = 0;
+      // (a small loop: unrolled, its instructions came from L2 once a piece, at
+      // 600 clocks a row)
       #pragma unroll 1
       for (int i0 = 0; i0 < kRowsW; i0 += kPer * kBatch) {
+        uint4 ahead[kBatch];
+        q_load(ahead, i0 + kPer * kBatch);
         uint32_t top[kBatch];      // of the magnitudes, two lanes of 16 bits
         #pragma unroll
         for (int k = 0; k < kBatch; ++k)
@@ -594,23 +595,25 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
           // (infinities have no code: their row is NaN, as its scores are)
           down = amax < __uint_as_float(0x7f800000u) ? down * 128.f : __uint_as_float(0x7fffffffu);
           if (cl == 0) q_pow[(np & 1) * L::kRows + rr] = up * 0.0078125f;
-          float f[2][4];
+          // (below 256 every f16 and bf16 is an f16 to 2^-25)
+          uint32_t f[4];
           const uint32_t y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
           #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const float2 t = p.bf16 ? unpack2<true>(y[c]) : unpack2<false>(y[c]);
-            f[c >> 1][2 * (c & 1)] = t.x * down;
-            f[c >> 1][2 * (c & 1) + 1] = t.y * down;
+            f[c] = pack2<false>(t.x * down, t.y * down);
           }
           const uint32_t to = q_to + (rr >> 7) * L::kQTile + row_chunk<L::kKCols>(r, (cl >> 1) % (L::kKCols / 16));
           #pragma unroll
           for (int q = 0; q < 3; ++q) {
             if (q == 2 && p.bf16) break;
-            const uint32_t w0 = take_e4m3(f[0]), w1 = take_e4m3(f[1]);
+            const uint32_t w0 = __byte_perm(take_e4m3(f[0]), take_e4m3(f[1]), 0x5410);
+            const uint32_t w1 = __byte_perm(take_e4m3(f[2]), take_e4m3(f[3]), 0x5410);
             asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to + q * L::kQPart), "r"(w0), "r"(w1) : "memory");
           }
         }
-        if (i0 + kPer * kBatch < kRowsW) q_load(x, i0 + kPer * kBatch);
+        #pragma unroll
+        for (int k = 0; k < kBatch; ++k) x[k] = ahead[k];
       }
       fence_proxy_async_smem();
       mbar_arrive_warp(bar(L::kQFull));

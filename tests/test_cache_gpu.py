@@ -236,6 +236,40 @@ def test_chunks_of_prompts(dtype, d, page, causal):
                   causal=causal, layout="bnhd")
 
 
+@pytest.mark.parametrize("d,page,B,Hkv,Nq,L", [
+    (256, 32, 48, 32, 128, 128), (256, 64, 3, 16, 1500, 1900), (128, 16, 48, 32, 256, 128),
+    (128, 128, 24, 16, 300, 700), (64, 64, 64, 32, 256, 128), (64, 16, 20, 16, 600, 640)])
+def test_many_units_for_every_cta(d, page, B, Hkv, Nq, L):
+    """Long runs of pieces of one key tile and of a few, every SM walking over
+    many of them (rings and phases wrap many times), against fp64 on the GPU."""
+    g = torch.Generator().manual_seed(d + L)
+    lens = [max(1, L - 37 * (b % 3)) for b in range(B)]
+    codes, scales, table = ref.make_cache(B * -(-L // page) + 1, Hkv, page, d, B, -(-L // page), g, lens)
+    cache = device_cache(codes, scales, table)
+    q = torch.randn(B, Hkv, Nq, d, device=DEV).half()
+    for causal in (True, False):
+        o, lse = binding.forward_cache(q, cache, ints(lens), causal, 0.06)
+        binding.device_status()
+        for b in range(0, B, 7):
+            ids = table[b, :-(-lens[b] // page)].long().to(DEV)
+            K, V = ((cache.tensors[i][ids].double() * cache.tensors[2 + i][ids].double()[..., None, None])
+                    .transpose(0, 1).reshape(Hkv, -1, d)[:, :lens[b]] for i in (0, 1))
+            S = q[b].double() @ K.transpose(-1, -2) * 0.06
+            if causal:
+                i = torch.arange(Nq, device=DEV)[:, None] + lens[b] - Nq
+                S.masked_fill_(torch.arange(lens[b], device=DEV) > i, -math.inf)
+            want_l = torch.logsumexp(S, -1)
+            some = torch.isfinite(want_l)
+            P = torch.where(some[..., None], (S - want_l[..., None]).exp(), 0.0)
+            want = P @ V
+            # weights to half a step of f16 and small ones to 2^-25, scores to
+            # fp32 (2^-13 together, sums of d = 256 products of size up to 2^5)
+            bound = (P @ V.abs()) * 2.0 ** -10 + 2.0 ** -11 * want.abs() + lens[b] * 2.0 ** -25 * 448 * 2.0 ** -5
+            assert ((o[b].double() - want).abs() <= bound).all()
+            assert torch.equal(torch.isneginf(lse[b]), ~some)
+            assert float((lse[b].double() - want_l)[some].abs().max()) < 1e-3
+
+
 @pytest.mark.parametrize("d,page", [(64, 16), (128, 64), (256, 16)])
 @pytest.mark.parametrize("causal", [True, False])
 def test_padded_queries_and_short_sequences(d, page, causal):

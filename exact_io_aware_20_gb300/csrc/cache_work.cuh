@@ -4,11 +4,14 @@
 //
 // A unit is a tile of RT query rows of one key/value head of one sequence, a
 // step STEP of its keys.  Units follow one another in the order (sequence, row
-// tile, head); CTA c takes steps [c * share, (c + 1) * share) of them all, so
-// that every CTA has the same number of steps whatever the lengths are.  A
-// CTA's first unit may have begun in the share before and its last may go on
-// in the next: it writes those as pieces (slot 0: the piece does not begin
-// its unit, slot 1: it does), the units inside it as results.
+// tile, head), each with OVER steps ahead of its own that stand for what a
+// unit costs besides them (its queries' load, its results); CTA c takes places
+// [c * share, (c + 1) * share) of them all, so that every CTA has the same
+// work whatever the lengths are (without OVER, CTAs whose share held many
+// short units took twice the average's time on a causal prompt).  A CTA's
+// first unit may have begun in the share before and its last may go on in the
+// next: it writes those as pieces (slot 0: the piece does not begin its unit,
+// slot 1: it does), the units inside it as results.
 #pragma once
 
 #include "fa_internal.h"
@@ -139,21 +142,27 @@ __device__ __forceinline__ long long block_sum(long long x, long long* red) {
   return x;
 }
 
-// All steps of the call, one key/value head counted.
-template <int RT, int STEP, int THREADS>
-__device__ long long total_steps(const FwdCacheParams& p, long long* red, bool* bad) {
+// Places that a unit of `lim` keys takes.
+template <int STEP, int OVER>
+__device__ __forceinline__ int places_of(int lim) {
+  return lim > 0 ? OVER + steps_of<STEP>(lim) : 0;
+}
+
+// All places of the call, one key/value head counted.
+template <int RT, int STEP, int OVER, int THREADS>
+__device__ long long total_places(const FwdCacheParams& p, long long* red, bool* bad) {
   long long mine = 0;
   const int entries = p.seq.B * p.row_tiles;
   for (int e = threadIdx.x; e < entries; e += THREADS) {
     Sequence s;
-    mine += steps_of<STEP>(limits_of<RT>(p, e, &s, bad).lim);
+    mine += places_of<STEP, OVER>(limits_of<RT>(p, e, &s, bad).lim);
   }
   return block_sum<THREADS>(mine, red);
 }
 
-// The entry in which step `at` (of all entries, one head) lies: found->x the
-// entry, found->y the steps before it.
-template <int RT, int STEP, int THREADS>
+// The entry in which place `at` (of all entries, one head) lies: found->x the
+// entry, found->y the places before it.
+template <int RT, int STEP, int OVER, int THREADS>
 __device__ void find_entry(const FwdCacheParams& p, long long at, long long* red,
                            longlong2* found) {
   const int entries = p.seq.B * p.row_tiles, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -162,7 +171,7 @@ __device__ void find_entry(const FwdCacheParams& p, long long at, long long* red
     const int e = e0 + threadIdx.x;
     Sequence s;
     bool bad = false;
-    const long long mine = e < entries ? steps_of<STEP>(limits_of<RT>(p, e, &s, &bad).lim) : 0;
+    const long long mine = e < entries ? places_of<STEP, OVER>(limits_of<RT>(p, e, &s, &bad).lim) : 0;
     long long upto = mine;
     #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -188,12 +197,15 @@ __device__ void find_entry(const FwdCacheParams& p, long long at, long long* red
   __syncthreads();
 }
 
-// Where a walk over the steps of a share stands.
-template <int RT, int STEP>
+// A walk over the pieces of a share.
+template <int RT, int STEP, int OVER>
 struct Walk {
-  int e, h, step, steps;   // entry, key/value head, step and steps of the unit
-  int lim, full;
+  int e, h;                // entry and key/value head of the unit
+  int steps, lim, full;    // its steps and limits
   Sequence seq;
+  int place;               // where the share is in it
+  long long left;          // places left of the share
+  int s0, s1;              // the piece: the unit's steps [s0, s1)
   __device__ __forceinline__ void enter(const FwdCacheParams& p) {
     bool bad = false;
     const TileLimits t = limits_of<RT>(p, e, &seq, &bad);
@@ -201,35 +213,48 @@ struct Walk {
     full = t.full;
     steps = steps_of<STEP>(lim);
   }
-  // found: of find_entry(lo / Hkv); entry e's Hkv units stand one after
-  // another from step found->y * Hkv on
+  // To place lo of all (found: of find_entry(lo / Hkv); entry e's Hkv units
+  // stand one after another from place found->y * Hkv on), for n places.
   __device__ __forceinline__ void start(const FwdCacheParams& p, const longlong2* found,
-                                        long long lo) {
+                                        long long lo, long long n) {
     e = static_cast<int>(found->x);
     enter(p);
     const long long rest = lo - found->y * p.Hkv;
-    h = static_cast<int>(rest / steps);
-    step = static_cast<int>(rest % steps);
+    h = static_cast<int>(rest / (OVER + steps));
+    place = static_cast<int>(rest % (OVER + steps));
+    left = n;
   }
-  __device__ __forceinline__ void next_unit(const FwdCacheParams& p) {
-    step = 0;
-    if (++h == p.Hkv) {
-      h = 0;
-      const int entries = p.seq.B * p.row_tiles;
-      do {
-        if (++e >= entries) { steps = lim = full = 0; return; }
-        enter(p);
-      } while (steps == 0);
+  // The next piece that has a step (s0, s1); false behind the last.
+  __device__ __forceinline__ bool next(const FwdCacheParams& p) {
+    while (left > 0) {
+      if (place == OVER + steps) {
+        place = 0;
+        if (++h == p.Hkv) {
+          h = 0;
+          const int entries = p.seq.B * p.row_tiles;
+          do {
+            if (++e >= entries) { left = 0; return false; }
+            enter(p);
+          } while (steps == 0);
+        }
+      }
+      const int to = static_cast<int>(min(static_cast<long long>(OVER + steps), place + left));
+      s0 = max(0, place - OVER);
+      s1 = to - OVER;
+      left -= to - place;
+      place = to;
+      if (s1 > s0) return true;
     }
+    return false;
   }
 };
 
 // Joins the pieces of units that lie in several shares, and writes the units
-// that see no key.  Block (c, y) looks for the unit that begins in share c and
-// goes on behind it; its warps take a row each: the pieces' weights first,
+// that see no key.  Block (c, y) looks for the unit whose steps begin in share
+// c and go on behind it; its warps take a row each: the pieces' weights first,
 // then their O, four loads in flight.
 constexpr int kMergeThreads = 128;
-template <int D, int RT, int STEP>
+template <int D, int RT, int STEP, int OVER>
 __global__ void __launch_bounds__(kMergeThreads)
 cache_merge_kernel(const __grid_constant__ FwdCacheParams p) {
   constexpr int kVec = D / 32, kWarps = kMergeThreads / 32;
@@ -238,18 +263,18 @@ cache_merge_kernel(const __grid_constant__ FwdCacheParams p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row_first = blockIdx.y * kWarps + warp, row_step = gridDim.y * kWarps;
   bool bad = false;
-  const long long total = total_steps<RT, STEP, kMergeThreads>(p, red, &bad) * p.Hkv;
+  const long long total = total_places<RT, STEP, OVER, kMergeThreads>(p, red, &bad) * p.Hkv;
   const long long share = (total + p.ctas - 1) / p.ctas;
   const int c0 = blockIdx.x;
   const long long end = (c0 + 1) * share;
   bool joins = end < total && share > 0;      // (share > 0 wherever a step is)
-  Walk<RT, STEP> at;
+  Walk<RT, STEP, OVER> at;
   int c1 = 0;
   if (joins) {
-    find_entry<RT, STEP, kMergeThreads>(p, (end - 1) / p.Hkv, red, &found);
-    at.start(p, &found, end - 1);
-    const long long first = end - 1 - at.step, last = first + at.steps - 1;
-    joins = last >= end && first >= end - share;
+    find_entry<RT, STEP, OVER, kMergeThreads>(p, (end - 1) / p.Hkv, red, &found);
+    at.start(p, &found, end - 1, 1);
+    const long long first = end - 1 - at.place + OVER, last = first + at.steps - 1;   // its steps
+    joins = last >= end && first >= end - share && first < end;
     c1 = static_cast<int>(last / share);
   }
   grid_dependency_wait();   // (every CTA: this grid's end is to imply the other's)
@@ -331,10 +356,10 @@ cache_merge_kernel(const __grid_constant__ FwdCacheParams p) {
 
 // Launches the join behind the attention kernel, as its programmatic
 // dependent.
-template <int D, int RT, int STEP>
+template <int D, int RT, int STEP, int OVER>
 cudaError_t launch_cache_merge(const FwdCacheParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.ctas), RT > 32 ? RT / 32 : 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.ctas), RT > 8 ? RT / 8 : 1, 1);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -342,7 +367,7 @@ cudaError_t launch_cache_merge(const FwdCacheParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_merge_kernel<D, RT, STEP>, p);
+  return cudaLaunchKernelEx(&cfg, cache_merge_kernel<D, RT, STEP, OVER>, p);
 }
 
 // The tcgen05 kernel, for many query rows (fa_cache_prefill.cu): rows of a

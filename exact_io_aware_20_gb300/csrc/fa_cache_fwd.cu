@@ -38,6 +38,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;
+constexpr int kOver = 1;            // a unit's cost besides its steps, in steps
 
 template <int D>
 struct Tile {
@@ -134,22 +135,23 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     tma_prefetch_desc(&tm_v);
   }
   bool bad = false;
-  const long long total = total_steps<RT, T::kStep, kThreads>(p, red, &bad) * p.Hkv;
+  const long long total = total_places<RT, T::kStep, kOver, kThreads>(p, red, &bad) * p.Hkv;
   if (bad && blockIdx.x == 0) atomicOr(p.seq.err, kErrCache);
   const long long share = (total + p.ctas - 1) / p.ctas;
   const long long lo = blockIdx.x * share, hi = min(total, lo + share);
   if (lo >= hi) return;
-  find_entry<RT, T::kStep, kThreads>(p, lo / p.Hkv, red, found);
-  Walk<RT, T::kStep> at;
-  at.start(p, found, lo);
+  find_entry<RT, T::kStep, kOver, kThreads>(p, lo / p.Hkv, red, found);
+  Walk<RT, T::kStep, kOver> at;
+  at.start(p, found, lo, hi - lo);
   __syncthreads();   // found is read; its place is the join buffer's
 
   // ---------------------------------------------------------------- loads
   const int sub_log2 = min(p.page_log2, 31 - __clz(T::kKeys));   // keys of a box
   const int subs = T::kKeys >> sub_log2;                         // boxes (pages) of a tile
   const uint32_t box_bytes = static_cast<uint32_t>(T::kPitch) << sub_log2;
-  Walk<RT, T::kStep> f = at;
-  long long f_left = hi - lo;
+  Walk<RT, T::kStep, kOver> f = at;
+  bool f_more = f.next(p);
+  int f_step = f_more ? f.s0 : 0;
   int fetched = 0, done = 0;
   int tb_first = 0, tb_steps = 0;      // steps of f's unit that the table registers cover
   int tb_page = 0;
@@ -157,15 +159,15 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   bool dead = false;                   // a wait gave up: no further loads
   // Issue the warp's next tile, if it has one left in the share.
   auto fetch = [&]() {
-    while (f_left > 0 && !dead) {
-      const int k0 = (f.step * kWarps + warp) * T::kKeys;
+    while (f_more && !dead) {
+      const int k0 = (f_step * kWarps + warp) * T::kKeys;
       const bool mine = k0 < f.lim;
       if (mine) {
-        if (f.step >= tb_first + tb_steps) {
+        if (f_step >= tb_first + tb_steps) {
           // the pages and scales of the next 32 / subs steps, one a lane
-          tb_first = f.step;
+          tb_first = f_step;
           tb_steps = 32 / subs;
-          const int key = ((f.step + lane / subs) * kWarps + warp) * T::kKeys +
+          const int key = ((f_step + lane / subs) * kWarps + warp) * T::kKeys +
                           ((lane & (subs - 1)) << sub_log2);
           tb_page = 0;
           tb_ks = tb_vs = 1.f;
@@ -182,7 +184,7 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           }
         }
         const int stage = fetched % kStages;
-        const int from = (f.step - tb_first) * subs;
+        const int from = (f_step - tb_first) * subs;
         const uint32_t bar = bars + 8 * stage;
         const uint32_t dst = ring + stage * 2 * T::kBytes;
         const int boxes = min(subs, (f.lim - k0 + (1 << sub_log2) - 1) >> sub_log2);
@@ -205,9 +207,9 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         __syncwarp();
         ++fetched;
       }
-      --f_left;
-      if (++f.step == f.steps && f_left > 0) {
-        f.next_unit(p);
+      if (++f_step == f.s1) {
+        f_more = f.next(p);
+        f_step = f.s0;
         tb_steps = 0;
         tb_first = 0;
       }
@@ -218,10 +220,8 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   for (int i = 0; i < kStages; ++i) fetch();
 
   // ---------------------------------------------------------------- units
-  long long left = hi - lo;
-  while (left > 0) {
+  while (at.next(p)) {
     const int b = at.e / p.row_tiles, row0 = at.e % p.row_tiles * 8 * NT;
-    const int end = static_cast<int>(min(static_cast<long long>(at.steps), at.step + left));
     // q of the unit's rows as B fragments of S^T = K Q^T: lane (g, t) of
     // fragment (64-column part c, j) holds row g, columns 64c + 16t + 4j ..+3
     for (int nt = warp; nt < NT; nt += kWarps) {
@@ -301,7 +301,7 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         #pragma unroll
         for (int k = 0; k < 4; ++k) acc[i][nt][k] = 0.f;
 
-    for (int step = at.step; step < end; ++step) {
+    for (int step = at.s0; step < at.s1; ++step) {
       const int k0 = (step * kWarps + warp) * T::kKeys;
       if (k0 >= at.lim) continue;
       const int stage = done % kStages;
@@ -541,8 +541,8 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       __syncthreads();
     }
     if (warp == 0) {
-      const bool whole = at.step == 0 && end == at.steps;
-      const long long slot = 2ll * blockIdx.x + (at.step > 0 ? 0 : 1);
+      const bool whole = at.s0 == 0 && at.s1 == at.steps;
+      const long long slot = 2ll * blockIdx.x + (at.s0 > 0 ? 0 : 1);
       constexpr int kVec = D == 64 ? 8 : 16;       // consecutive columns of a lane
       #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -588,8 +588,6 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           }
         }
     }
-    left -= end - at.step;
-    if (left > 0) at.next_unit(p);
   }
   if (dead) {
     // the copies still in flight, before their shared memory goes away
@@ -642,7 +640,7 @@ cudaError_t launch(const Cache& cache, FwdCacheParams& p, int sms, cudaStream_t 
     return e;
   cache_fwd_kernel<D, NT><<<p.ctas, kThreads, Smem<D, NT>::kAlloc, stream>>>(tk, tv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_cache_merge<D, 8 * NT, Tile<D>::kStep>(p, stream);
+  return launch_cache_merge<D, 8 * NT, Tile<D>::kStep, kOver>(p, stream);
 }
 
 }  // namespace

@@ -40,6 +40,7 @@ template <int D>
 struct Pre {
   static constexpr int kTiles = D == 256 ? 1 : 2;
   static constexpr int kRows = 128 * kTiles;        // of a unit
+  static constexpr int kOver = kTiles == 1 ? 3 : 4;    // a unit's cost besides its steps, in steps
   static constexpr int kSoftWarps = 4 * kTiles;
   static constexpr int kConvWarps = 12 - kSoftWarps;
   static constexpr int kConvRows = 128 / kConvWarps;   // keys of a tile that a warp converts
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ FwdCacheParams p) {
   using L = Pre<D>;
-  using W = Walk<L::kRows, 128>;
+  using W = Walk<L::kRows, 128, L::kOver>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -242,7 +243,7 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
     fence_barrier_init();
   }
   bool bad = false;
-  const long long total = total_steps<L::kRows, 128, kThreads>(p, red, &bad) * p.Hkv;
+  const long long total = total_places<L::kRows, 128, L::kOver, kThreads>(p, red, &bad) * p.Hkv;
   if (bad && blockIdx.x == 0) atomicOr(p.seq.err, kErrCache);
   const long long share = (total + p.ctas - 1) / p.ctas;
   const long long lo = blockIdx.x * share, hi = min(total, lo + share);
@@ -251,9 +252,9 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
     tmem_alloc(smem_u32(tmem_holder), L::kTmemCols);
     tmem_relinquish();
   }
-  find_entry<L::kRows, 128, kThreads>(p, lo / p.Hkv, red, found);
+  find_entry<L::kRows, 128, L::kOver, kThreads>(p, lo / p.Hkv, red, found);
   W at;
-  if (warp == 13) at.start(p, found, lo);
+  if (warp == 13) at.start(p, found, lo, hi - lo);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -267,13 +268,12 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
     fewer_registers<L::kRegMisc>();
     if (warp == 13) {
       // -------------------------------------------------------- schedule
-      long long left = hi - lo;
       for (int np = 0;; ++np) {
         if (np >= 4 && !wait_uniform(bar(L::kRecEmpty + (np & 3)), ((np >> 2) + 1) & 1, abort)) break;
         volatile Piece* w = reinterpret_cast<volatile Piece*>(smem + L::kRecOff + (np & 3) * 64);
-        const int s1 = left > 0 ? static_cast<int>(min(static_cast<long long>(at.steps), at.step + left)) : -1;
+        const int s1 = at.next(p) ? at.s1 : -1;
         if (lane == 0) {
-          w->s0 = at.step;
+          w->s0 = at.s0;
           w->s1 = s1;
           if (s1 >= 0) {
             const int row0 = at.e % p.row_tiles * L::kRows;
@@ -286,7 +286,7 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
               const int end = min(s1, (t.lim + 127) / 128);
               w->end[u] = end;
               w->full[u] = t.full;
-              if (end > at.step) all = min(all, t.full);
+              if (end > at.s0) all = min(all, t.full);
             }
             w->all = all;
             w->lim = at.lim;
@@ -295,15 +295,13 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
             w->row0 = row0;
             w->len = at.seq.len;
             w->n = at.seq.n;
-            w->whole = at.step == 0 && s1 == at.steps;
+            w->whole = at.s0 == 0 && s1 == at.steps;
           }
         }
         __syncwarp();
         if (elect_one()) mbar_arrive(bar(L::kRecFull + (np & 3)));
         __syncwarp();
         if (s1 < 0) break;
-        left -= s1 - at.step;
-        if (left > 0) at.next_unit(p);
       }
     } else if (warp == 14) {
       // ----------------------------------------------------------- pages
@@ -902,7 +900,7 @@ cudaError_t launch_seg(const Cache& cache, FwdCacheParams& p, int sms, cudaStrea
   p.ctas = sms;
   kern<<<p.ctas, kThreads, Pre<D>::kAlloc, stream>>>(tk, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_cache_merge<D, Pre<D>::kRows, 128>(p, stream);
+  return launch_cache_merge<D, Pre<D>::kRows, 128, Pre<D>::kOver>(p, stream);
 }
 
 template <int D>

@@ -443,6 +443,7 @@ class Cache:
         self.pages, self.Hkv, self.page_size, self.d = pages, Hkv, page, d
         self.B, self.table_width = block_table.shape
         self.device, self.device_index = k.device, k.get_device()
+        self.key = (self.B, Hkv, d, self.device_index)
         self.struct = _FaCache(*(t.data_ptr() for t in self.tensors), pages, page, self.table_width,
                                Hkv, d, _view_strides(k), _view_strides(v))
         self._ref = ctypes.addressof(self.struct)
@@ -460,21 +461,47 @@ def _view_strides(t):
 
 
 _L6, _L12 = ctypes.c_longlong * 6, ctypes.c_longlong * 12   # two and four fa_strides
+_plans: dict = {}   # what a call's shapes, strides, types and device come to, checked once
 
 
-def _view(t, shape, dtype, device, what):
+def _plan(make, *key):
+    """make(*key), kept: a call's checks and stride arrays depend on its
+    tensors' geometry alone, and a decoding loop repeats the same few."""
+    key = (make, *key)
+    plan = _plans.get(key)
+    if plan is None:
+        plan = make(*key[1:])
+        if len(_plans) >= 512:
+            _plans.clear()
+        _plans[key] = plan
+    return plan
+
+
+def _geometry(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+def _view(geometry, shape, dtype, device, what):
     """(batch, head, row) strides of a [B, heads, N, d] view that has to be of
     the shape, dtype and device (an index) given."""
-    if t.shape != shape:
-        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype or t.get_device() != device:
+    of, s, its_dtype, its_device = geometry
+    if of != shape:
+        raise ValueError(f"{what}: shape {tuple(of)}, expected {tuple(shape)}")
+    if its_dtype != dtype or its_device != device:
         raise ValueError(f"{what} must have the dtype and device of the other tensors")
-    s = t.stride()
     B, heads, N, d = shape
     if s[3] != 1:
         raise ValueError("the last (d) dimension must be contiguous")
     # a dimension of one element has no stride of its own
     return (s[0] if B > 1 else heads * N * d, s[1] if heads > 1 else N * d, s[2] if N > 1 else d)
+
+
+def _code(dtype):
+    if dtype == torch.float16:
+        return FA_F16
+    if dtype == torch.bfloat16:
+        return FA_BF16
+    raise TypeError(f"unsupported dtype {dtype}; fp16 and bf16 are supported")
 
 
 def _ints(t, shape, device, what):
@@ -524,26 +551,30 @@ def _on_stream(device, stream, call, *args):
     return out
 
 
-def _rope(q, k, positions, table, inverse, q_out, k_out, stream):
-    if q.dim() != 4 or (k is not None and k.dim() != 4):
+def _rope_plan(q, k, q_out, k_out):
+    if len(q[0]) != 4 or (k is not None and len(k[0]) != 4):
         raise ValueError("expected q [B, H, N, d] and k [B, Hkv, N, d]")
-    qs = q.shape
-    B, H, N, d = qs
-    dtype, device = q.dtype, q.get_device()
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out belong together")
+    B, H, N, d = q[0]
+    Hkv = 0 if k is None else k[0][1]
+
+    def view(t, heads, what):
+        return (0, 0, 0) if t is None else _view(t, (B, heads, N, d), q[2], q[3], what)
+
+    return B, H, Hkv, N, d, _code(q[2]), _L12(*view(q, H, "q"), *view(k, Hkv, "k"),
+                                              *view(q_out, H, "q_out"), *view(k_out, Hkv, "k_out"))
+
+
+def _rope(q, k, positions, table, inverse, q_out, k_out, stream):
     if q_out is None:
         q_out = torch.empty_like(q)
-    a, b = _view(q, qs, dtype, device, "q"), _view(q_out, qs, dtype, device, "q_out")
-    pos, pos_batch = _positions(positions, table.axes, B, N, device)
-    if k is None:
-        Hkv, kp, kop, st = 0, None, None, _L12(*a, 0, 0, 0, *b)
-    else:
-        Hkv = k.shape[1]
-        ks = (B, Hkv, N, d)
-        if k_out is None:
-            k_out = torch.empty_like(k)
-        st = _L12(*a, *_view(k, ks, dtype, device, "k"), *b, *_view(k_out, ks, dtype, device, "k_out"))
-        kp, kop = k.data_ptr(), k_out.data_ptr()
-    _check(load().fa_rope(q.data_ptr(), kp, q_out.data_ptr(), kop, B, H, Hkv, N, d, _dtype_code(q),
+    if k is not None and k_out is None:
+        k_out = torch.empty_like(k)
+    B, H, Hkv, N, d, code, st = _plan(_rope_plan, _geometry(q), _geometry(k), _geometry(q_out),
+                                      _geometry(k_out))
+    pos, pos_batch = _positions(positions, table.axes, B, N, q.get_device())
+    _check(load().fa_rope(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), B, H, Hkv, N, d, code,
                           table._ref, pos, pos_batch, inverse, st, stream), "fa_rope")
     return q_out, k_out
 
@@ -581,28 +612,33 @@ def cache_append(cache: Cache, q, k, v, seq_lens, new_lens=None, rope: Rope | No
                       positions, q_out)
 
 
-def _cache_append(cache, q, k, v, seq_lens, new_lens, rope, positions, q_out, stream):
-    if k.dim() != 4 or (q is not None and q.dim() != 4):
+def _append_plan(cache, q, k, v, q_out):
+    if len(k[0]) != 4 or (q is not None and len(q[0]) != 4):
         raise ValueError("expected k and v [B, Hkv, N, d], q [B, H, N, d]")
-    ks = k.shape
-    B, Hkv, N, d = ks
-    dtype, device = k.dtype, k.get_device()
-    if Hkv != cache.Hkv or d != cache.d or B != cache.B or device != cache.device_index:
-        raise ValueError(f"k{tuple(ks)} does not belong to a cache of {cache.B} sequences, "
-                         f"{cache.Hkv} heads, d {cache.d} on {cache.device}")
-    kv = _view(k, ks, dtype, device, "k") + _view(v, ks, dtype, device, "v")
-    pos, pos_batch = _positions(positions, 1 if rope is None else rope.axes, B, N, device)
+    B, Hkv, N, d = k[0]
+    if (B, Hkv, d, k[3]) != cache:
+        raise ValueError(f"k{tuple(k[0])} does not belong to a cache of {cache[0]} sequences, "
+                         f"{cache[1]} heads, d {cache[2]} on device {cache[3]}")
+    H = 0 if q is None else q[0][1]
+
+    def view(t, heads, what):
+        return (0, 0, 0) if t is None else _view(t, (B, heads, N, d), k[2], k[3], what)
+
+    return B, H, N, _code(k[2]), _L12(*view(q, H, "q"), *view(k, Hkv, "k"), *view(v, Hkv, "v"),
+                                      *view(q_out, H, "q_out"))
+
+
+def _cache_append(cache, q, k, v, seq_lens, new_lens, rope, positions, q_out, stream):
     if q is None:
-        H, qp, qop, q_out, st = 0, None, None, None, _L12(0, 0, 0, *kv)
-    else:
-        H = q.shape[1]
-        qs = (B, H, N, d)
-        if q_out is None:
-            q_out = torch.empty_like(q)
-        st = _L12(*_view(q, qs, dtype, device, "q"), *kv, *_view(q_out, qs, dtype, device, "q_out"))
-        qp, qop = q.data_ptr(), q_out.data_ptr()
+        q_out = None
+    elif q_out is None:
+        q_out = torch.empty_like(q)
+    B, H, N, code, st = _plan(_append_plan, cache.key, _geometry(q), _geometry(k), _geometry(v),
+                              _geometry(q_out))
+    device = cache.device_index
+    pos, pos_batch = _positions(positions, 1 if rope is None else rope.axes, B, N, device)
     _check(load().fa_cache_append(
-        cache._ref, qp, k.data_ptr(), v.data_ptr(), qop, B, H, N, _dtype_code(k),
+        cache._ref, _ptr(q), k.data_ptr(), v.data_ptr(), _ptr(q_out), B, H, N, code,
         _ints(seq_lens, (B,), device, "seq_lens"), _ints(new_lens, (B,), device, "new_lens"),
         None if rope is None else rope._ref, pos, pos_batch, st, stream), "fa_cache_append")
     return q_out
@@ -617,37 +653,37 @@ def forward_cache(q, cache: Cache, seq_lens, causal: bool, scale: float, new_len
                       new_lens, out, lse, workspace)
 
 
-def _forward_cache(q, cache, seq_lens, causal, scale, new_lens, out, lse, workspace, stream):
-    if q.dim() != 4:
+def _forward_plan(cache, q, out):
+    if len(q[0]) != 4:
         raise ValueError("expected q [B, H, Nq, d]")
-    qs = q.shape
-    B, H, Nq, d = qs
-    dtype, device = q.dtype, q.get_device()
-    if d != cache.d or B != cache.B or device != cache.device_index or H % cache.Hkv:
-        raise ValueError(f"q{tuple(qs)} does not fit a cache of {cache.B} sequences, "
-                         f"{cache.Hkv} heads, d {cache.d} on {cache.device}")
-    lib = load()
+    B, H, Nq, d = q[0]
+    if (B, d, q[3]) != (cache[0], cache[2], cache[3]) or H % cache[1]:
+        raise ValueError(f"q{tuple(q[0])} does not fit a cache of {cache[0]} sequences, {cache[1]} heads, "
+                         f"d {cache[2]} on device {cache[3]}")
+    return (B, H, Nq, _code(q[2]), _L6(*_view(q, q[0], q[2], q[3], "q"), *_view(out, q[0], q[2], q[3], "out")),
+            fwd_cache_workspace_size(B, H, cache[1], Nq, d))
+
+
+def _forward_cache(q, cache, seq_lens, causal, scale, new_lens, out, lse, workspace, stream):
     if out is None:
         out = torch.empty_like(q)
-    st = _L6(*_view(q, qs, dtype, device, "q"), *_view(out, qs, dtype, device, "out"))
+    B, H, Nq, code, st, ws_bytes = _plan(_forward_plan, cache.key, _geometry(q), _geometry(out))
+    device = cache.device_index
     if lse is None:
         lse = torch.empty((B, H, Nq), dtype=torch.float32, device=cache.device)
     elif (lse.dtype != torch.float32 or lse.shape != (B, H, Nq) or lse.get_device() != device
           or not lse.is_contiguous()):
         raise ValueError(f"lse must be contiguous fp32 [{B}, {H}, {Nq}] on the inputs' device")
     if workspace is None:
-        need = lib.fa_fwd_cache_workspace_size(B, H, cache.Hkv, Nq, d)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=cache.device)
-        ws_bytes = need
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=cache.device)
     else:
         if workspace.get_device() != device:
             raise ValueError("the workspace must be on the inputs' device")
         ws_bytes = workspace.numel() * workspace.element_size()
-    _check(lib.fa_fwd_cache(
-        q.data_ptr(), cache._ref, out.data_ptr(), lse.data_ptr(), B, H, Nq, int(causal), scale,
-        _dtype_code(q), _ints(seq_lens, (B,), device, "seq_lens"),
-        _ints(new_lens, (B,), device, "new_lens"), st, workspace.data_ptr(), ws_bytes, stream),
-        "fa_fwd_cache")
+    _check(load().fa_fwd_cache(
+        q.data_ptr(), cache._ref, out.data_ptr(), lse.data_ptr(), B, H, Nq, causal, scale, code,
+        _ints(seq_lens, (B,), device, "seq_lens"), _ints(new_lens, (B,), device, "new_lens"), st,
+        workspace.data_ptr(), ws_bytes, stream), "fa_fwd_cache")
     return out, lse
 
 

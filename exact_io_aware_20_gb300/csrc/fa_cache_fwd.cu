@@ -38,7 +38,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;
-constexpr int kOver = 1;            // a unit's cost besides its steps, in steps
+constexpr int kOver = 2;            // a unit's cost besides its steps, in steps
 
 template <int D>
 struct Tile {

@@ -40,7 +40,7 @@ template <int D>
 struct Pre {
   static constexpr int kTiles = D == 256 ? 1 : 2;
   static constexpr int kRows = 128 * kTiles;        // of a unit
-  static constexpr int kOver = kTiles == 1 ? 3 : 4;    // a unit's cost besides its steps, in steps
+  static constexpr int kOver = kTiles == 1 ? 5 : 6;    // a unit's cost besides its steps, in steps
   static constexpr int kSoftWarps = 4 * kTiles;
   static constexpr int kConvWarps = 12 - kSoftWarps;
   static constexpr int kConvRows = 128 / kConvWarps;   // keys of a tile that a warp converts

@@ -128,73 +128,71 @@ __device__ __forceinline__ TileLimits limits_of(const FwdCacheParams& p, int e, 
   return tile_limits(p.seq, *s, rt * RT, min(p.rows, (rt + 1) * RT));
 }
 
-// Sum over the block's threads (every thread gets it); red: a value a warp.
-template <int THREADS>
-__device__ __forceinline__ long long block_sum(long long x, long long* red) {
-  #pragma unroll
-  for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = 0;
-  #pragma unroll
-  for (int i = 0; i < THREADS / 32; ++i) x += red[i];
-  return x;
-}
-
 // Places that a unit of `lim` keys takes.
 template <int STEP, int OVER>
 __device__ __forceinline__ int places_of(int lim) {
   return lim > 0 ? OVER + steps_of<STEP>(lim) : 0;
 }
 
-// All places of the call, one key/value head counted.
-template <int RT, int STEP, int OVER, int THREADS>
-__device__ long long total_places(const FwdCacheParams& p, long long* red, bool* bad) {
-  long long mine = 0;
-  const int entries = p.seq.B * p.row_tiles;
-  for (int e = threadIdx.x; e < entries; e += THREADS) {
-    Sequence s;
-    mine += places_of<STEP, OVER>(limits_of<RT>(p, e, &s, bad).lim);
-  }
-  return block_sum<THREADS>(mine, red);
-}
-
-// The entry in which place `at` (of all entries, one head) lies: found->x the
-// entry, found->y the places before it.
-template <int RT, int STEP, int OVER, int THREADS>
-__device__ void find_entry(const FwdCacheParams& p, long long at, long long* red,
-                           longlong2* found) {
+// Counts the places of the call, one key/value head counted (the result, the
+// same in every thread), and finds the entry in which place `which(count)`
+// lies, if that is not negative: found->x the entry, found->y the places
+// before it.  All threads of the block; red: two values a warp.
+template <int RT, int STEP, int OVER, int THREADS, class Which>
+__device__ __forceinline__ long long find_place(const FwdCacheParams& p, long long* red,
+                                                longlong2* found, bool* bad, Which which) {
+  constexpr int kWarps = THREADS / 32;
   const int entries = p.seq.B * p.row_tiles, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long before = 0;
-  for (int e0 = 0; e0 < entries; e0 += THREADS) {
-    const int e = e0 + threadIdx.x;
+  // this thread's entry of the block of entries from e0 on: its places
+  auto places_at = [&](int e0) -> long long {
+    const int e = e0 + static_cast<int>(threadIdx.x);
+    if (e >= entries) return 0;
     Sequence s;
-    bool bad = false;
-    const long long mine = e < entries ? places_of<STEP, OVER>(limits_of<RT>(p, e, &s, &bad).lim) : 0;
-    long long upto = mine;
+    return places_of<STEP, OVER>(limits_of<RT>(p, e, &s, bad).lim);
+  };
+  // inclusive sum over the block's threads, and all of them
+  auto scan = [&](long long mine, long long* all, long long* space) -> long long {
     #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, upto, m);
-      if (lane >= m) upto += x;
+      const long long x = __shfl_up_sync(0xffffffffu, mine, m);
+      if (lane >= m) mine += x;
     }
+    if (lane == 31) space[warp] = mine;
     __syncthreads();
-    if (lane == 31) red[warp] = upto;
-    __syncthreads();
-    long long all = 0;
+    *all = 0;
     #pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) {
-      if (i < warp) upto += red[i];
-      all += red[i];
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) mine += space[i];
+      *all += space[i];
     }
-    if (mine > 0 && before + upto - mine <= at && at < before + upto) {
-      found->x = e;
-      found->y = before + upto - mine;
-    }
-    before += all;
-    if (at < before) break;
+    return mine;
+  };
+  long long all, mine = places_at(0);
+  long long upto = scan(mine, &all, red), count = all;
+  if (entries > THREADS) {
+    long long rest = 0, behind;
+    for (int e0 = THREADS; e0 < entries; e0 += THREADS) rest += places_at(e0);
+    scan(rest, &behind, red + kWarps);
+    count += behind;
   }
-  __syncthreads();
+  const long long at = which(count);
+  if (at >= 0) {
+    long long before = 0;
+    for (int e0 = 0;;) {
+      if (mine > 0 && before + upto - mine <= at && at < before + upto) {
+        found->x = e0 + static_cast<int>(threadIdx.x);
+        found->y = before + upto - mine;
+      }
+      before += all;
+      e0 += THREADS;
+      if (e0 >= entries || at < before) break;
+      __syncthreads();
+      mine = places_at(e0);
+      upto = scan(mine, &all, red);
+    }
+    __syncthreads();
+  }
+  return count;
 }
 
 // A walk over the pieces of a share.
@@ -213,8 +211,8 @@ struct Walk {
     full = t.full;
     steps = steps_of<STEP>(lim);
   }
-  // To place lo of all (found: of find_entry(lo / Hkv); entry e's Hkv units
-  // stand one after another from place found->y * Hkv on), for n places.
+  // To place lo of all (found: of place lo / Hkv; entry e's Hkv units stand
+  // one after another from place found->y * Hkv on), for n places.
   __device__ __forceinline__ void start(const FwdCacheParams& p, const longlong2* found,
                                         long long lo, long long n) {
     e = static_cast<int>(found->x);
@@ -258,20 +256,24 @@ template <int D, int RT, int STEP, int OVER>
 __global__ void __launch_bounds__(kMergeThreads)
 cache_merge_kernel(const __grid_constant__ FwdCacheParams p) {
   constexpr int kVec = D / 32, kWarps = kMergeThreads / 32;
-  __shared__ long long red[kWarps];
+  __shared__ long long red[2 * kWarps];
   __shared__ longlong2 found;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row_first = blockIdx.y * kWarps + warp, row_step = gridDim.y * kWarps;
   bool bad = false;
-  const long long total = total_places<RT, STEP, OVER, kMergeThreads>(p, red, &bad) * p.Hkv;
-  const long long share = (total + p.ctas - 1) / p.ctas;
   const int c0 = blockIdx.x;
-  const long long end = (c0 + 1) * share;
-  bool joins = end < total && share > 0;      // (share > 0 wherever a step is)
+  long long share = 0, end = 0;
+  bool joins = false;
+  find_place<RT, STEP, OVER, kMergeThreads>(p, red, &found, &bad, [&](long long count) {
+    const long long total = count * p.Hkv;
+    share = (total + p.ctas - 1) / p.ctas;
+    end = (c0 + 1) * share;
+    joins = end < total && share > 0;      // (share > 0 wherever a step is)
+    return joins ? (end - 1) / p.Hkv : -1ll;
+  });
   Walk<RT, STEP, OVER> at;
   int c1 = 0;
   if (joins) {
-    find_entry<RT, STEP, OVER, kMergeThreads>(p, (end - 1) / p.Hkv, red, &found);
     at.start(p, &found, end - 1, 1);
     const long long first = end - 1 - at.place + OVER, last = first + at.steps - 1;   // its steps
     joins = last >= end && first >= end - share && first < end;

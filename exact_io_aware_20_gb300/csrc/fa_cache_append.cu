@@ -21,6 +21,8 @@
 namespace fa {
 namespace {
 
+constexpr int kUnitsWanted = 4 * 152;   // block-wide units that fill the chip
+
 struct AppendParams {
   const uint16_t *q, *k, *v;
   uint16_t* q_out;
@@ -31,6 +33,7 @@ struct AppendParams {
   int page_log2;
   int span;             // pages that N tokens can touch
   int units, unit_blocks;
+  int unit_heads;       // heads that a block-wide unit does one after another
   int q_heads_per;      // heads of a thread of q's blocks
   long long q_items;    // B * N * slots
   const int *seq_lens, *new_lens;
@@ -95,45 +98,6 @@ __device__ __forceinline__ uint4 rescaled(uint4 v, float ratio) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One slot of one new row: its 16 values in fp32 (keys rotated), in the order
-// of its two chunks.
-template <bool BF16>
-__device__ __forceinline__ void slot_values(const AppendParams& p, const uint16_t* rows,
-                                            long long row_stride, bool key, int b, int start,
-                                            int i, int slot, const Slot& at, float (&x)[16]) {
-  const uint16_t* src = rows + i * row_stride;
-  const uint4 a = *reinterpret_cast<const uint4*>(src + at.col_a);
-  const uint4 c = *reinterpret_cast<const uint4*>(src + at.col_b);
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
-  #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float2 f = unpack2<BF16>(w[j]);
-    x[2 * j] = f.x;
-    x[2 * j + 1] = f.y;
-  }
-  if (key && at.turns) {
-    int pos[4];
-    load_positions(p.r, b, i, p.N, start + i, pos);
-    float cs[8], sn[8];
-    slot_cos_sin(p.r, slot, pos, cs, sn);
-    if (p.r.interleaved) {
-      #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float u = x[2 * j], v = x[2 * j + 1];
-        x[2 * j] = fmaf(u, cs[j], -(v * sn[j]));
-        x[2 * j + 1] = fmaf(v, cs[j], u * sn[j]);
-      }
-    } else {
-      #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float u = x[j], v = x[8 + j];
-        x[j] = fmaf(u, cs[j], -(v * sn[j]));
-        x[8 + j] = fmaf(v, cs[j], u * sn[j]);
-      }
-    }
-  }
-}
-
 __device__ __forceinline__ float finite_max(float m, const float (&x)[16]) {
   #pragma unroll
   for (int j = 0; j < 16; ++j) {
@@ -143,16 +107,89 @@ __device__ __forceinline__ float finite_max(float m, const float (&x)[16]) {
   return m;
 }
 
-// GROUP threads do a unit (32: four units a block, no block barrier).  HOLD:
-// slots that a thread keeps in registers between the two passes over the new
-// rows; 0: it reads (from L2) and rotates them again, for pages of more slots
-// than registers.
+// The 16 values of a slot from its two chunks as loaded.
+template <bool BF16>
+__device__ __forceinline__ void unpack16(const uint4& a, const uint4& c, float (&x)[16]) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+  #pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float2 f = unpack2<BF16>(w[j]);
+    x[2 * j] = f.x;
+    x[2 * j + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void turn16(float (&x)[16], const float (&c)[8], const float (&s)[8],
+                                       bool interleaved) {
+  #pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (interleaved) {
+      const float u = x[2 * j], v = x[2 * j + 1];
+      x[2 * j] = fmaf(u, c[j], -(v * s[j]));
+      x[2 * j + 1] = fmaf(v, c[j], u * s[j]);
+    } else {
+      const float u = x[j], v = x[8 + j];
+      x[j] = fmaf(u, c[j], -(v * s[j]));
+      x[8 + j] = fmaf(v, c[j], u * s[j]);
+    }
+  }
+}
+
+// What a unit's threads know of its page.
+struct Target {
+  int r0, rows;         // rows that stay, and new rows behind them
+  int i0, start;        // the first new row's number in k and v, and the sequence's first new token
+  int phys;             // the page
+};
+__device__ __forceinline__ bool target_of(const AppendParams& p, int b, int j, bool report, Target& t) {
+  Sequence s;
+  if (!sequence_of(p, b, s)) {
+    if (report && j == 0) atomicOr(p.err, kErrCache);
+    return false;
+  }
+  t.start = s.len - s.n;
+  const int number = (t.start >> p.page_log2) + j;      // page of the sequence
+  const long long first = static_cast<long long>(number) << p.page_log2;   // its first token
+  if (first >= s.len || s.n == 0) return false;
+  t.phys = p.cache.table[static_cast<long long>(b) * p.cache.width + number];
+  if (static_cast<unsigned>(t.phys) >= static_cast<unsigned>(p.cache.pages)) {
+    if (report) atomicOr(p.err, kErrCache);
+    return false;
+  }
+  t.r0 = first < t.start ? t.start - static_cast<int>(first) : 0;
+  t.rows = min(1 << p.page_log2, s.len - static_cast<int>(first)) - t.r0;
+  t.i0 = static_cast<int>(first) + t.r0 - t.start;
+  return true;
+}
+
+// Codes of a slot's 16 values, at its two places in a row.
+__device__ __forceinline__ void put16(unsigned char* row, const Slot& where, const float (&x)[16],
+                                      float inv) {
+  const uint2 a = to_codes(x, inv), c = to_codes(x + 8, inv);
+  if (where.col_b == where.col_a + 8) {
+    *reinterpret_cast<uint4*>(row + where.col_a) = make_uint4(a.x, a.y, c.x, c.y);
+  } else {
+    *reinterpret_cast<uint2*>(row + where.col_a) = a;
+    *reinterpret_cast<uint2*>(row + where.col_b) = c;
+  }
+}
+
+// A unit: one page, K or V, of one head for a warp (GROUP 32, four units a
+// block) and of unit_heads heads, one after another, for a block.  A thread
+// keeps up to HOLD slots of the new rows between the two passes over them, as
+// they were loaded; a block's keeps the angles' cos and sin, which every head
+// shares, in shared memory of its own (16 floats a slot: with them in
+// registers too few threads were resident to keep memory busy, and worked out
+// anew for each head they took as long as the loads), and has the next head's
+// rows in flight.  HOLD 0: rows are read (from L2) and rotated again, for
+// pages of more slots than that.
 template <bool BF16, int GROUP, int HOLD>
-__global__ void __launch_bounds__(GROUP == 32 ? 128 : GROUP)
+__global__ void __launch_bounds__(GROUP == 32 ? 128 : GROUP, GROUP == 256 || GROUP == 32 ? 4 : 2)
 append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kThreads = GROUP == 32 ? 128 : GROUP;
   constexpr int kUnits = kThreads / GROUP;
-  __shared__ float red[32];
+  constexpr bool kAngles = GROUP > 32 && HOLD > 0;     // in shared memory
+  __shared__ float red[2][GROUP > 32 ? GROUP / 32 : 1];
+  extern __shared__ float4 angles[];                   // [HOLD][4][thread]
   const int tid = threadIdx.x;
   if (static_cast<int>(blockIdx.x) >= p.unit_blocks) {
     // q: rotated (or copied), zeros behind a sequence's new tokens
@@ -169,117 +206,168 @@ append_kernel(const __grid_constant__ AppendParams p) {
     const bool ok = sequence_of(p, b, s);
     int pos[4];
     load_positions(p.r, b, n, p.N, s.len - s.n + n, pos);
-    RopeRows w;
-    w.in[0] = w.in[1] = p.q + b * p.qs.b + n * p.qs.n;
-    w.out[0] = w.out[1] = p.q_out + b * p.qos.b + n * p.qos.n;
-    w.in_h[0] = w.in_h[1] = p.qs.h;
-    w.out_h[0] = w.out_h[1] = p.qos.h;
-    w.H = p.H;
+    uint16_t* to = p.q_out + b * p.qos.b + n * p.qos.n;
+    const uint16_t* from = p.q + b * p.qs.b + n * p.qs.n;
+    const RopeRows w = {from, from, to, to, p.qs.h, p.qs.h, p.qos.h, p.qos.h, p.H};
     const int h0 = group * p.q_heads_per;
-    rope_heads<BF16>(p.r, w, slot, h0, min(p.H, h0 + p.q_heads_per), pos, ok && n < s.n);
+    rope_heads<BF16, 2>(p.r, w, slot, h0, min(p.H, h0 + p.q_heads_per), pos, ok && n < s.n);
     return;
   }
   const int unit = blockIdx.x * kUnits + tid / GROUP;
   const int t = tid % GROUP;
   if (unit >= p.units) return;   // (whole groups; a block-wide group never has one left over)
-  // units in the order (b, page of the span, K or V, head)
+  // units in the order (b, page of the span, K or V, head group)
   const Cache& ca = p.cache;
-  const int h = unit % ca.Hkv;
-  const bool key = (unit / ca.Hkv & 1) == 0;
-  const int j = unit / (2 * ca.Hkv) % p.span;
-  const int b = unit / (2 * ca.Hkv) / p.span;
-  Sequence s;
-  if (!sequence_of(p, b, s)) {
-    if (t == 0 && j == 0) atomicOr(p.err, kErrCache);
-    return;
-  }
-  const int start = s.len - s.n, page = 1 << p.page_log2;
-  const int number = (start >> p.page_log2) + j;      // page of the sequence
-  const long long first = static_cast<long long>(number) << p.page_log2;   // its first token
-  if (first >= s.len || s.n == 0) return;
-  const int phys = ca.table[static_cast<long long>(b) * ca.width + number];
-  if (static_cast<unsigned>(phys) >= static_cast<unsigned>(ca.pages)) {
-    if (t == 0) atomicOr(p.err, kErrCache);
-    return;
-  }
-  const int r0 = first < start ? start - static_cast<int>(first) : 0;      // rows that stay
-  const int rows = min(page, s.len - static_cast<int>(first)) - r0;        // new rows
-  const int i0 = static_cast<int>(first) + r0 - start;                     // the first of them in k, v
+  const int groups = (ca.Hkv + p.unit_heads - 1) / p.unit_heads;
+  const int h0 = unit % groups * p.unit_heads, h1 = min(ca.Hkv, h0 + p.unit_heads);
+  const bool key = (unit / groups & 1) == 0;
+  const int b = unit / (2 * groups) / p.span;
+  Target at;
+  if (!target_of(p, b, unit / (2 * groups) % p.span, t == 0, at)) return;
   const Strides in = key ? p.ks : p.vs, to = key ? ca.ks : ca.vs;
-  const uint16_t* src = (key ? p.k : p.v) + b * in.b + h * in.h;
-  unsigned char* dst = (key ? ca.k : ca.v) + phys * to.b + h * to.h;
-  float* scale = (key ? ca.k_scale : ca.v_scale) + static_cast<long long>(phys) * ca.Hkv + h;
-  const float was = r0 > 0 ? *scale : 0.f;
-  const int count = rows * p.slots;
+  const uint16_t* src = (key ? p.k : p.v) + b * in.b + at.i0 * in.n;
+  unsigned char* page = (key ? ca.k : ca.v) + at.phys * to.b;
+  float* scales = (key ? ca.k_scale : ca.v_scale) + static_cast<long long>(at.phys) * ca.Hkv;
+  const int count = at.rows * p.slots;
   const bool turn = key && p.r.pairs > 0;
   auto slot_at = [&](int slot) -> Slot {
     if (turn) return slot_of(p.r, slot);
     return {16 * slot, 16 * slot + 8, false};
   };
-
-  float amax = 0.f;
-  float held[HOLD > 0 ? HOLD : 1][16];
-  if constexpr (HOLD > 0) {
-    #pragma unroll
-    for (int u = 0; u < HOLD; ++u) {
-      const int at = t + u * GROUP;
-      if (at < count) {
-        const int slot = at % p.slots;
-        slot_values<BF16>(p, src, in.n, turn, b, start, i0 + at / p.slots, slot, slot_at(slot),
-                          held[u]);
-        amax = finite_max(amax, held[u]);
-      }
-    }
-  } else {
-    for (int at = t; at < count; at += GROUP) {
-      const int slot = at % p.slots;
-      float x[16];
-      slot_values<BF16>(p, src, in.n, turn, b, start, i0 + at / p.slots, slot, slot_at(slot), x);
-      amax = finite_max(amax, x);
-    }
-  }
-  #pragma unroll
-  for (int m = 16; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-  if constexpr (GROUP > 32) {
-    if ((tid & 31) == 0) red[tid >> 5] = amax;
-    __syncthreads();   // (and every thread has read the old scale)
-    #pragma unroll
-    for (int i = 0; i < GROUP / 32; ++i) amax = fmaxf(amax, red[i]);
-  } else {
-    __syncwarp();
-  }
-  const float now = fmaxf(scale_for(amax), was);
-  const float inv = 1.f / now;
-  if (t == 0) *scale = now;
-  if (r0 > 0 && now > was) {
-    const float ratio = was * inv;
-    for (int at = t; at < r0 * p.slots; at += GROUP) {
-      uint4* code = reinterpret_cast<uint4*>(dst + (at / p.slots) * to.n + (at % p.slots) * 16);
-      *code = rescaled(*code, ratio);
-    }
-  }
-  auto put = [&](int at, const float (&x)[16]) {
-    const int slot = at % p.slots;
-    const Slot where = slot_at(slot);
-    unsigned char* row = dst + (r0 + at / p.slots) * to.n;
-    const uint2 a = to_codes(x, inv), c = to_codes(x + 8, inv);
-    if (where.col_b == where.col_a + 8) {
-      *reinterpret_cast<uint4*>(row + where.col_a) = make_uint4(a.x, a.y, c.x, c.y);
-    } else {
-      *reinterpret_cast<uint2*>(row + where.col_a) = a;
-      *reinterpret_cast<uint2*>(row + where.col_b) = c;
+  auto cos_sin = [&](int i, int slot, float (&c)[8], float (&s)[8]) {
+    int pos[4];
+    load_positions(p.r, b, at.i0 + i, p.N, at.start + at.i0 + i, pos);
+    slot_cos_sin(p.r, slot, pos, c, s);
+  };
+  // one slot of one new row of head h, rotated
+  auto values = [&](int h, int n, float (&x)[16]) {
+    const int i = n / p.slots, slot = n % p.slots;
+    const Slot w = slot_at(slot);
+    const uint16_t* row = src + h * in.h + i * in.n;
+    unpack16<BF16>(*reinterpret_cast<const uint4*>(row + w.col_a),
+                   *reinterpret_cast<const uint4*>(row + w.col_b), x);
+    if (w.turns) {
+      float c[8], s[8];
+      cos_sin(i, slot, c, s);
+      turn16(x, c, s, p.r.interleaved);
     }
   };
-  if constexpr (HOLD > 0) {
+
+  constexpr int kHold = HOLD > 0 ? HOLD : 1;
+  uint4 raw[kHold][2];
+  auto load = [&](int h) {
     #pragma unroll
-    for (int u = 0; u < HOLD; ++u)
-      if (t + u * GROUP < count) put(t + u * GROUP, held[u]);
-  } else {
-    for (int at = t; at < count; at += GROUP) {
-      const int slot = at % p.slots;
-      float x[16];
-      slot_values<BF16>(p, src, in.n, turn, b, start, i0 + at / p.slots, slot, slot_at(slot), x);
-      put(at, x);
+    for (int u = 0; u < kHold; ++u) {
+      const int n = t + u * GROUP;
+      if (n < count) {
+        const Slot w = slot_at(n % p.slots);
+        const uint16_t* row = src + h * in.h + (n / p.slots) * in.n;
+        raw[u][0] = *reinterpret_cast<const uint4*>(row + w.col_a);
+        raw[u][1] = *reinterpret_cast<const uint4*>(row + w.col_b);
+      }
+    }
+  };
+  if constexpr (HOLD > 0) load(h0);
+  if constexpr (kAngles) {
+    if (turn) {
+      #pragma unroll
+      for (int u = 0; u < kHold; ++u) {
+        const int n = t + u * GROUP;
+        if (n < count && slot_at(n % p.slots).turns) {
+          float c[8], s[8];
+          cos_sin(n / p.slots, n % p.slots, c, s);
+          #pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            angles[(4 * u + i) * GROUP + t] = make_float4(c[4 * i], c[4 * i + 1], c[4 * i + 2], c[4 * i + 3]);
+            angles[(4 * u + 2 + i) * GROUP + t] = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+          }
+        }
+      }
+    }
+  }
+  // slot u of the head held, rotated
+  auto held = [&](const uint4 (&v)[2], int u, float (&x)[16]) {
+    unpack16<BF16>(v[0], v[1], x);
+    const int n = t + u * GROUP;
+    if (turn && slot_at(n % p.slots).turns) {
+      float c[8], s[8];
+      if constexpr (kAngles) {
+        #pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float4 a = angles[(4 * u + i) * GROUP + t], e = angles[(4 * u + 2 + i) * GROUP + t];
+          c[4 * i] = a.x, c[4 * i + 1] = a.y, c[4 * i + 2] = a.z, c[4 * i + 3] = a.w;
+          s[4 * i] = e.x, s[4 * i + 1] = e.y, s[4 * i + 2] = e.z, s[4 * i + 3] = e.w;
+        }
+      } else {
+        cos_sin(n / p.slots, n % p.slots, c, s);
+      }
+      turn16(x, c, s, p.r.interleaved);
+    }
+  };
+  for (int h = h0; h < h1; ++h) {
+    uint4 now_raw[kHold][2];
+    float kept[kHold][16];      // a warp's unit has one head: its rows stay as rotated
+    const float was = at.r0 > 0 ? scales[h] : 0.f;
+    float amax = 0.f;
+    if constexpr (HOLD > 0) {
+      #pragma unroll
+      for (int u = 0; u < kHold; ++u) {
+        now_raw[u][0] = raw[u][0];
+        now_raw[u][1] = raw[u][1];
+      }
+      if (h + 1 < h1) load(h + 1);
+      #pragma unroll
+      for (int u = 0; u < kHold; ++u)
+        if (t + u * GROUP < count) {
+          held(now_raw[u], u, kept[u]);
+          amax = finite_max(amax, kept[u]);
+        }
+    } else {
+      for (int n = t; n < count; n += GROUP) {
+        float x[16];
+        values(h, n, x);
+        amax = finite_max(amax, x);
+      }
+    }
+    #pragma unroll
+    for (int m = 16; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+    if constexpr (GROUP > 32) {
+      // (two places by turns: one barrier a head; it also says that every
+      // thread has read the old scale)
+      float* mine = red[(h - h0) & 1];
+      if ((tid & 31) == 0) mine[tid >> 5] = amax;
+      __syncthreads();
+      #pragma unroll
+      for (int i = 0; i < GROUP / 32; ++i) amax = fmaxf(amax, mine[i]);
+    } else {
+      __syncwarp();
+    }
+    const float now = fmaxf(scale_for(amax), was);
+    const float inv = 1.f / now;
+    unsigned char* dst = page + h * to.h;
+    if (t == 0) scales[h] = now;
+    if (at.r0 > 0 && now > was) {
+      const float ratio = was * inv;
+      for (int n = t; n < at.r0 * p.slots; n += GROUP) {
+        uint4* code = reinterpret_cast<uint4*>(dst + (n / p.slots) * to.n + (n % p.slots) * 16);
+        *code = rescaled(*code, ratio);
+      }
+    }
+    if constexpr (HOLD > 0) {
+      #pragma unroll
+      for (int u = 0; u < kHold; ++u) {
+        const int n = t + u * GROUP;
+        if (n < count) {
+          if constexpr (kAngles) held(now_raw[u], u, kept[u]);
+          put16(dst + (at.r0 + n / p.slots) * to.n, slot_at(n % p.slots), kept[u], inv);
+        }
+      }
+    } else {
+      for (int n = t; n < count; n += GROUP) {
+        float x[16];
+        values(h, n, x);
+        put16(dst + (at.r0 + n / p.slots) * to.n, slot_at(n % p.slots), x, inv);
+      }
     }
   }
 }
@@ -287,16 +375,33 @@ append_kernel(const __grid_constant__ AppendParams p) {
 template <int GROUP, int HOLD>
 cudaError_t launch(AppendParams& p, int bf16, cudaStream_t stream) {
   constexpr int kThreads = GROUP == 32 ? 128 : GROUP;
+  // Heads of a unit: all of them when there are pages enough to fill the chip
+  // without (angles are then worked out once a page), one when there are few.
+  const long long pages = 2ll * p.B * p.span;
+  p.unit_heads = GROUP == 32 || HOLD == 0
+                     ? 1
+                     : static_cast<int>(std::max(1ll, std::min<long long>(
+                           p.cache.Hkv, pages * p.cache.Hkv / kUnitsWanted)));
+  const int groups = (p.cache.Hkv + p.unit_heads - 1) / p.unit_heads;
+  const long long units = pages * groups;
+  if (units > INT32_MAX) return cudaErrorInvalidValue;
+  p.units = static_cast<int>(units);
   p.unit_blocks = (p.units + kThreads / GROUP - 1) / (kThreads / GROUP);
   long long blocks = p.unit_blocks;
   if (p.q != nullptr) {
-    const long long groups = (p.H + p.q_heads_per - 1) / p.q_heads_per;
-    blocks += (p.q_items * groups + kThreads - 1) / kThreads;
+    const long long q_groups = (p.H + p.q_heads_per - 1) / p.q_heads_per;
+    blocks += (p.q_items * q_groups + kThreads - 1) / kThreads;
   }
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   const unsigned grid = static_cast<unsigned>(blocks);
-  if (bf16) append_kernel<true, GROUP, HOLD><<<grid, kThreads, 0, stream>>>(p);
-  else append_kernel<false, GROUP, HOLD><<<grid, kThreads, 0, stream>>>(p);
+  constexpr size_t smem = GROUP > 32 ? HOLD * 64 * GROUP : 0;
+  auto kern = bf16 ? append_kernel<true, GROUP, HOLD> : append_kernel<false, GROUP, HOLD>;
+  if constexpr (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  kern<<<grid, kThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -320,9 +425,6 @@ cudaError_t launch_cache_append(const Cache& cache, const AppendCall& c, const R
   p.slots = cache.d / 16;
   while ((1 << p.page_log2) < cache.page) ++p.page_log2;
   p.span = (c.N - 1 + cache.page - 1) / cache.page + 1;
-  const long long units = 2ll * c.B * p.span * cache.Hkv;
-  if (units > INT32_MAX) return cudaErrorInvalidValue;
-  p.units = static_cast<int>(units);
   p.q_items = static_cast<long long>(c.B) * c.N * p.slots;
   const long long groups =
       std::max(1ll, std::min<long long>(std::max(c.H, 1), 2048ll * 152 / p.q_items));

@@ -38,7 +38,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;
-constexpr int kOver = 2;            // a unit's cost besides its steps, in steps
+constexpr int kOver = 3;            // a unit's cost besides its steps, in steps
 
 template <int D>
 struct Tile {
@@ -117,7 +117,7 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   long long* red = reinterpret_cast<long long*>(smem + S::kBufOff);
-  longlong2* found = reinterpret_cast<longlong2*>(smem + S::kBufOff + 64);
+  longlong2* found = reinterpret_cast<longlong2*>(smem + S::kBufOff + 128);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + S::kMiscOff);
   uint2* q_frag = reinterpret_cast<uint2*>(smem + S::kQOff);
   float2* stat = reinterpret_cast<float2*>(smem + S::kStatOff);
@@ -135,12 +135,15 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     tma_prefetch_desc(&tm_v);
   }
   bool bad = false;
-  const long long total = total_places<RT, T::kStep, kOver, kThreads>(p, red, &bad) * p.Hkv;
+  long long lo = 0, hi = 0;
+  find_place<RT, T::kStep, kOver, kThreads>(p, red, found, &bad, [&](long long count) {
+    const long long total = count * p.Hkv, share = (total + p.ctas - 1) / p.ctas;
+    lo = blockIdx.x * share;
+    hi = min(total, lo + share);
+    return lo < hi ? lo / p.Hkv : -1ll;
+  });
   if (bad && blockIdx.x == 0) atomicOr(p.seq.err, kErrCache);
-  const long long share = (total + p.ctas - 1) / p.ctas;
-  const long long lo = blockIdx.x * share, hi = min(total, lo + share);
   if (lo >= hi) return;
-  find_entry<RT, T::kStep, kOver, kThreads>(p, lo / p.Hkv, red, found);
   Walk<RT, T::kStep, kOver> at;
   at.start(p, found, lo, hi - lo);
   __syncthreads();   // found is read; its place is the join buffer's
@@ -156,6 +159,23 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   int tb_first = 0, tb_steps = 0;      // steps of f's unit that the table registers cover
   int tb_page = 0;
   float tb_ks = 1.f, tb_vs = 1.f;
+  // The scales of a tile go to shared memory when the tile is first needed or
+  // the registers are loaded anew, not when its copies are issued: the wait
+  // for them is then behind the copies of the tiles that follow.
+  int scaled = 0;                      // tiles whose scales are there
+  int tile_from[kStages];              // the register lane of each stage's tile
+  auto scales = [&]() {
+    for (; scaled < fetched; ++scaled) {
+      const int stage = scaled % kStages;
+      int from = tile_from[0];
+      #pragma unroll
+      for (int i = 1; i < kStages; ++i) from = stage == i ? tile_from[i] : from;
+      const float ks = __shfl_sync(0xffffffffu, tb_ks, from + (lane & (subs - 1)));
+      const float vs = __shfl_sync(0xffffffffu, tb_vs, from + (lane & (subs - 1)));
+      if (lane < subs) meta[stage * T::kSub + lane] = make_float2(ks, log2f(vs));
+    }
+    __syncwarp();
+  };
   bool dead = false;                   // a wait gave up: no further loads
   // Issue the warp's next tile, if it has one left in the share.
   auto fetch = [&]() {
@@ -165,6 +185,7 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       if (mine) {
         if (f_step >= tb_first + tb_steps) {
           // the pages and scales of the next 32 / subs steps, one a lane
+          scales();
           tb_first = f_step;
           tb_steps = 32 / subs;
           const int key = ((f_step + lane / subs) * kWarps + warp) * T::kKeys +
@@ -201,9 +222,8 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             }
           }
         }
-        const float ks = __shfl_sync(0xffffffffu, tb_ks, from + (lane & (subs - 1)));
-        const float vs = __shfl_sync(0xffffffffu, tb_vs, from + (lane & (subs - 1)));
-        if (lane < subs) meta[stage * T::kSub + lane] = make_float2(ks, log2f(vs));
+        #pragma unroll
+        for (int i = 0; i < kStages; ++i) tile_from[i] = stage == i ? from : tile_from[i];
         __syncwarp();
         ++fetched;
       }
@@ -305,6 +325,7 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       const int k0 = (step * kWarps + warp) * T::kKeys;
       if (k0 >= at.lim) continue;
       const int stage = done % kStages;
+      if (scaled <= done) scales();
       if (!dead && !wait_uniform(bars + 8 * stage, (done / kStages) & 1, abort)) dead = true;
       if (dead) continue;
       const uint32_t kt = ring + stage * 2 * T::kBytes, vt = kt + T::kBytes;

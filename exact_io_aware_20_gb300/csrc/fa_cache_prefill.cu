@@ -74,7 +74,7 @@ struct Pre {
                        kNumBars = kTileEmpty + 8;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   static constexpr int kRedOff = (kMiscOff + 32 + 15) / 16 * 16;   // start: sums and the found entry
-  static constexpr int kBytes = kRedOff + 16 * 8 + 16;
+  static constexpr int kBytes = kRedOff + 2 * 16 * 8 + 16;
   static constexpr int kAlloc = kBytes + 1024;
   static constexpr uint32_t kTS = 0, kTO = 256, kTmemCols = 512;
   // registers a thread: the launch's 4 * 128 among the four warpgroups
@@ -204,7 +204,7 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
   volatile int* nan_seen = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 8);   // [4 pieces]
   long long* red = reinterpret_cast<long long*>(smem + L::kRedOff);
-  longlong2* found = reinterpret_cast<longlong2*>(smem + L::kRedOff + 128);
+  longlong2* found = reinterpret_cast<longlong2*>(smem + L::kRedOff + 256);
   float4* meta = reinterpret_cast<float4*>(smem + L::kMetaOff);
   Where* where = reinterpret_cast<Where*>(smem + L::kWhereOff);
   float* q_pow = reinterpret_cast<float*>(smem + L::kPowOff);
@@ -243,16 +243,19 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
     fence_barrier_init();
   }
   bool bad = false;
-  const long long total = total_places<L::kRows, 128, L::kOver, kThreads>(p, red, &bad) * p.Hkv;
+  long long lo = 0, hi = 0;
+  find_place<L::kRows, 128, L::kOver, kThreads>(p, red, found, &bad, [&](long long count) {
+    const long long total = count * p.Hkv, share = (total + p.ctas - 1) / p.ctas;
+    lo = blockIdx.x * share;
+    hi = min(total, lo + share);
+    return lo < hi ? lo / p.Hkv : -1ll;
+  });
   if (bad && blockIdx.x == 0) atomicOr(p.seq.err, kErrCache);
-  const long long share = (total + p.ctas - 1) / p.ctas;
-  const long long lo = blockIdx.x * share, hi = min(total, lo + share);
   if (lo >= hi) return;
   if (warp == 12) {
     tmem_alloc(smem_u32(tmem_holder), L::kTmemCols);
     tmem_relinquish();
   }
-  find_entry<L::kRows, 128, L::kOver, kThreads>(p, lo / p.Hkv, red, found);
   W at;
   if (warp == 13) at.start(p, found, lo, hi - lo);
   tc_fence_before();

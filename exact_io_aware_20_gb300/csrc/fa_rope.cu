@@ -34,18 +34,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const int b = static_cast<int>(tok / p.N), n = static_cast<int>(tok % p.N);
   int pos[4];
   load_positions(p.r, b, n, p.N, n, pos);
-  RopeRows w;
-  w.in[0] = p.q + b * p.qs.b + n * p.qs.n;
-  w.in[1] = p.k + b * p.ks.b + n * p.ks.n;
-  w.out[0] = p.q_out + b * p.qos.b + n * p.qos.n;
-  w.out[1] = p.k_out + b * p.kos.b + n * p.kos.n;
-  w.in_h[0] = p.qs.h;
-  w.in_h[1] = p.ks.h;
-  w.out_h[0] = p.qos.h;
-  w.out_h[1] = p.kos.h;
-  w.H = p.H;
+  const RopeRows w = {p.q + b * p.qs.b + n * p.qs.n,
+                      p.k + b * p.ks.b + n * p.ks.n,
+                      p.q_out + b * p.qos.b + n * p.qos.n,
+                      p.k_out + b * p.kos.b + n * p.kos.n,
+                      p.qs.h, p.ks.h, p.qos.h, p.kos.h, p.H};
   const int h0 = blockIdx.y * p.heads_per;
-  rope_heads<BF16>(p.r, w, slot, h0, min(p.heads, h0 + p.heads_per), pos, true);
+  rope_heads<BF16, 4>(p.r, w, slot, h0, min(p.heads, h0 + p.heads_per), pos, true);
 }
 
 }  // namespace

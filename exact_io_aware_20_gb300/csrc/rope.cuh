@@ -128,15 +128,14 @@ __device__ __forceinline__ void turn_slot(uint4& a, uint4& b, const float (&c)[8
 // token: heads below H are q's, the others k's.  Loads of kAhead heads are in
 // flight together.  `live` false: zeros are written instead.
 struct RopeRows {
-  const uint16_t* in[2];   // q, k of this token's sequence and row (head 0, column 0)
-  uint16_t* out[2];
-  long long in_h[2], out_h[2];   // head strides
+  const uint16_t *q, *k;         // of this token's sequence and row (head 0, column 0)
+  uint16_t *q_out, *k_out;
+  long long q_h, k_h, q_out_h, k_out_h;   // head strides
   int H;
 };
-template <bool BF16>
+template <bool BF16, int kAhead>
 __device__ __forceinline__ void rope_heads(const RopeArgs& r, const RopeRows& w, int slot, int h0,
                                            int h1, const int (&pos)[4], bool live) {
-  constexpr int kAhead = 4;
   const Slot at = slot_of(r, slot);
   float c[8], s[8];
   if (at.turns) slot_cos_sin(r, slot, pos, c, s);
@@ -144,13 +143,11 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& r, const RopeRows& w,
     uint4 a[kAhead], b[kAhead];
     #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
+      a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
       if (h + u < h1 && live) {
-        const int which = h + u >= w.H;
-        const uint16_t* src = w.in[which] + (h + u - (which ? w.H : 0)) * w.in_h[which];
+        const uint16_t* src = h + u < w.H ? w.q + (h + u) * w.q_h : w.k + (h + u - w.H) * w.k_h;
         a[u] = *reinterpret_cast<const uint4*>(src + at.col_a);
         b[u] = *reinterpret_cast<const uint4*>(src + at.col_b);
-      } else {
-        a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
       }
     }
     #pragma unroll
@@ -160,8 +157,7 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& r, const RopeRows& w,
           if (r.interleaved) turn_slot<BF16, true>(a[u], b[u], c, s);
           else turn_slot<BF16, false>(a[u], b[u], c, s);
         }
-        const int which = h + u >= w.H;
-        uint16_t* dst = w.out[which] + (h + u - (which ? w.H : 0)) * w.out_h[which];
+        uint16_t* dst = h + u < w.H ? w.q_out + (h + u) * w.q_out_h : w.k_out + (h + u - w.H) * w.k_out_h;
         *reinterpret_cast<uint4*>(dst + at.col_a) = a[u];
         *reinterpret_cast<uint4*>(dst + at.col_b) = b[u];
       }

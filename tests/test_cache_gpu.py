@@ -270,6 +270,24 @@ def test_many_units_for_every_cta(d, page, B, Hkv, Nq, L):
             assert float((lse[b].double() - want_l)[some].abs().max()) < 1e-3
 
 
+@pytest.mark.parametrize("d,B,Nq", [(64, 700, 1), (128, 300, 2), (256, 1100, 1), (64, 600, 70),
+                                    (128, 1100, 40)])
+def test_more_sequences_than_a_block_has_threads(d, B, Nq):
+    """The walk over the sequences' lengths takes several rounds of a block."""
+    g = torch.Generator().manual_seed(B)
+    lens = [Nq + int(x) for x in torch.randint(0, 90, (B,), generator=g)]
+    lens[3] = lens[B - 2] = 0
+    codes, scales, table = ref.make_cache(B * 12 + 1, 1, 16, d, B, 12, g, lens)
+    q = torch.randn(B, 1, Nq, d, generator=g).bfloat16()
+    cache = device_cache(codes, scales, table)
+    o, lse = binding.forward_cache(dev(q), cache, ints(lens), False, 0.1)
+    binding.device_status()
+    some = list(range(0, B, 37)) + [3, B - 2, B - 1]
+    check_attention(o[some], lse[some], q[some], ref.Paged(codes[0], scales[0]),
+                    ref.Paged(codes[1], scales[1]), table[some], [lens[b] for b in some],
+                    [Nq] * len(some), False, 0.1)
+
+
 @pytest.mark.parametrize("d,page", [(64, 16), (128, 64), (256, 16)])
 @pytest.mark.parametrize("causal", [True, False])
 def test_padded_queries_and_short_sequences(d, page, causal):

@@ -29,6 +29,7 @@
 // m16n8k16 costs nothing that shows beside the loads.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "cache_work.cuh"
 
@@ -93,8 +94,8 @@ struct Smem {
   static constexpr int kStatOff = kBufOff + kBufBytes;     // (maximum, sum) [warp][row]
   static constexpr int kStatBytes = kWarps * 8 * NT * 8;
   static constexpr int kQsOff = kStatOff + kStatBytes;     // [row] power of two taken off q
-  static constexpr int kMetaOff = kQsOff + 8 * NT * 4;     // (ks, log2 vs) [warp][stage][page]
-  static constexpr int kMetaBytes = kWarps * kStages * T::kSub * 8;
+  static constexpr int kMetaOff = kQsOff + 8 * NT * 4;     // (ks, log2 vs, 1 / vs) [warp][stage][page]
+  static constexpr int kMetaBytes = kWarps * kStages * T::kSub * 16;
   static constexpr int kBarOff = kMetaOff + kMetaBytes;
   static constexpr int kMiscOff = kBarOff + kWarps * kStages * 8;
   static constexpr int kAlloc = kMiscOff + 64 + 1024;      // slack to align the base
@@ -122,7 +123,7 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   uint2* q_frag = reinterpret_cast<uint2*>(smem + S::kQOff);
   float2* stat = reinterpret_cast<float2*>(smem + S::kStatOff);
   float* q_pow = reinterpret_cast<float*>(smem + S::kQsOff);
-  float2* meta = reinterpret_cast<float2*>(smem + S::kMetaOff) + warp * kStages * T::kSub;
+  const uint32_t meta = base + S::kMetaOff + warp * kStages * T::kSub * 16;
   const uint32_t ring = base + warp * kStages * 2 * T::kBytes;
   const uint32_t bars = base + S::kBarOff + warp * kStages * 8;
 
@@ -158,7 +159,7 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   int fetched = 0, done = 0;
   int tb_first = 0, tb_steps = 0;      // steps of f's unit that the table registers cover
   int tb_page = 0;
-  float tb_ks = 1.f, tb_vs = 1.f;
+  float tb_ks = 1.f, tb_lv = 0.f;
   // The scales of a tile go to shared memory when the tile is first needed or
   // the registers are loaded anew, not when its copies are issued: the wait
   // for them is then behind the copies of the tiles that follow.
@@ -171,8 +172,10 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       #pragma unroll
       for (int i = 1; i < kStages; ++i) from = stage == i ? tile_from[i] : from;
       const float ks = __shfl_sync(0xffffffffu, tb_ks, from + (lane & (subs - 1)));
-      const float vs = __shfl_sync(0xffffffffu, tb_vs, from + (lane & (subs - 1)));
-      if (lane < subs) meta[stage * T::kSub + lane] = make_float2(ks, log2f(vs));
+      const float lv = __shfl_sync(0xffffffffu, tb_lv, from + (lane & (subs - 1)));
+      if (lane < subs)
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(meta + (stage * T::kSub + lane) * 16),
+                     "f"(ks), "f"(lv), "f"(ex2_approx(-lv)), "f"(0.f) : "memory");
     }
     __syncwarp();
   };
@@ -191,7 +194,8 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           const int key = ((f_step + lane / subs) * kWarps + warp) * T::kKeys +
                           ((lane & (subs - 1)) << sub_log2);
           tb_page = 0;
-          tb_ks = tb_vs = 1.f;
+          tb_ks = 1.f;
+          tb_lv = 0.f;
           if (key < f.lim) {
             const int b = f.e / p.row_tiles;
             tb_page = p.table[static_cast<long long>(b) * p.width + (key >> p.page_log2)];
@@ -201,7 +205,7 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             }
             const long long sc = static_cast<long long>(tb_page) * p.Hkv + f.h;
             tb_ks = p.k_scale[sc];
-            tb_vs = p.v_scale[sc];
+            tb_lv = log2f(p.v_scale[sc]);
           }
         }
         const int stage = fetched % kStages;
@@ -210,9 +214,10 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         const uint32_t dst = ring + stage * 2 * T::kBytes;
         const int boxes = min(subs, (f.lim - k0 + (1 << sub_log2) - 1) >> sub_log2);
         if (lane == 0) mbar_arrive_expect_tx(bar, boxes * T::kHalves * 2 * box_bytes);
+        const int row = subs > 1 ? 0 : k0 & ((1 << p.page_log2) - 1);
+        #pragma unroll 1
         for (int i = 0; i < boxes; ++i) {
           const int page = __shfl_sync(0xffffffffu, tb_page, from + i);
-          const int row = subs > 1 ? 0 : k0 & ((1 << p.page_log2) - 1);
           if (lane == 0) {
             #pragma unroll
             for (int c = 0; c < T::kHalves; ++c) {
@@ -238,6 +243,14 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   };
   #pragma unroll 1
   for (int i = 0; i < kStages; ++i) fetch();
+
+  // This lane's places in a tile: of the K rows that it holds (64-column part
+  // 0; part 1 is the same with bit 6 turned), of the even and odd V rows
+  const uint32_t k_at = chunk_at<D>(key_of<D>(g), t);
+  const uint32_t v_at[2] = {
+      chunk_at<D>(key_of<D>(2 * t), D == 64 ? g >> 1 : g) + (D == 64 ? (g & 1) * 8 : 0),
+      chunk_at<D>(key_of<D>(2 * t + 1), D == 64 ? g >> 1 : g) + (D == 64 ? (g & 1) * 8 : 0)};
+  constexpr uint32_t kFrag = 16 * T::kPitch;    // bytes of 16 rows
 
   // ---------------------------------------------------------------- units
   while (at.next(p)) {
@@ -329,22 +342,23 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       if (!dead && !wait_uniform(bars + 8 * stage, (done / kStages) & 1, abort)) dead = true;
       if (dead) continue;
       const uint32_t kt = ring + stage * 2 * T::kBytes, vt = kt + T::kBytes;
-      const bool partial = k0 + T::kKeys > at.full;
-      #pragma unroll
-      for (int mt = 0; mt < T::kKeys / 16; ++mt) {
-        if (k0 + mt * 16 >= at.lim) break;
-        const float2 sc = meta[stage * T::kSub + ((mt * 16) >> sub_log2)];
-        const float inv_vs = ex2_approx(-sc.y);
-        // S^T of 16 keys
+      // 16 keys, the mt-th of the tile; PARTIAL: some row may not see some of
+      // them (a branch of its own, so that the common one stays short)
+      auto fragment = [&](auto is_partial, int mt) {
+        constexpr bool PARTIAL = decltype(is_partial)::value;
+        float sc[4];
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(sc[0]), "=f"(sc[1]), "=f"(sc[2]), "=f"(sc[3])
+                     : "r"(meta + (stage * T::kSub + ((mt * 16) >> sub_log2)) * 16));
+        // S^T of the 16 keys
         float s[NT][4];
         #pragma unroll
         for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-        const int kr = mt * 16 + key_of<D>(g);
         #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-          const uint32_t part = kt + (c >> 1) * T::kKeys * T::kPitch;
-          const uint4 x = ld_shared_v4(part + chunk_at<D>(kr, 4 * (c & 1) + t));
-          const uint4 y = ld_shared_v4(part + chunk_at<D>(kr + 8, 4 * (c & 1) + t));
+          const uint32_t from = kt + (c >> 1) * T::kKeys * T::kPitch + mt * kFrag + (k_at ^ ((c & 1) << 6));
+          const uint4 x = ld_shared_v4(from);
+          const uint4 y = ld_shared_v4(from + kFrag / 2);
           const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
           #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -361,17 +375,19 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
         bool grow = false;
         #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          const float f[2] = {qscale[nt][0] * sc[0], qscale[nt][1] * sc[0]};
           #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            s[nt][k] = fmaf(s[nt][k], qscale[nt][k & 1] * sc.x, sc.y);
-            if (partial) {
+            s[nt][k] = fmaf(s[nt][k], f[k & 1], sc[1]);
+            if constexpr (PARTIAL) {
               const int r = row0 + nt * 8 + 2 * t + (k & 1);
-              const int key = k0 + kr + (k >> 1) * 8;
+              const int key = k0 + mt * 16 + key_of<D>(g) + (k >> 1) * 8;
               if (key >= row_limit(p.seq, at.seq, r)) s[nt][k] = -INFINITY;
             }
-            grow |= s[nt][k] > m[nt][k & 1] + kGrow;
           }
+          grow |= fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + kGrow || fmaxf(s[nt][1], s[nt][3]) > m[nt][1] + kGrow;
+        }
         if (__any_sync(0xffffffffu, grow)) {
           #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -397,35 +413,32 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         for (int nt = 0; nt < NT; ++nt) {
           float w[4];
           #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            w[k] = ex2_approx(s[nt][k] - m[nt][k & 1]);
-            l[nt][k & 1] = fmaf(w[k], inv_vs, l[nt][k & 1]);
-          }
+          for (int k = 0; k < 4; ++k) w[k] = ex2_approx(s[nt][k] - m[nt][k & 1]);
+          l[nt][0] = fmaf(w[0] + w[2], sc[2], l[nt][0]);
+          l[nt][1] = fmaf(w[1] + w[3], sc[2], l[nt][1]);
           p0[nt] = transpose8x8(pack2<false>(w[0], w[1]));
           p1[nt] = transpose8x8(pack2<false>(w[2], w[3]));
         }
-        const int va = mt * 16 + key_of<D>(2 * t), vb = mt * 16 + key_of<D>(2 * t + 1);
         bool nans = false;
         #pragma unroll
         for (int half = 0; half < T::kHalves; ++half) {
-          const uint32_t part = vt + half * T::kKeys * T::kPitch;
+          const uint32_t part = vt + half * T::kKeys * T::kPitch + mt * kFrag;
           constexpr int kWords = D == 64 ? 2 : 4;    // 4-column words of a lane
           uint32_t v[4][kWords];
           #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int r = (i & 1 ? vb : va) + (i >> 1) * 8;
+            const uint32_t from = part + v_at[i & 1] + (i >> 1) * (kFrag / 2);
             if constexpr (D == 64) {
-              const uint32_t a = part + chunk_at<D>(r, g >> 1) + (g & 1) * 8;
-              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[i][0]), "=r"(v[i][1]) : "r"(a) : "memory");
+              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[i][0]), "=r"(v[i][1]) : "r"(from) : "memory");
             } else {
-              const uint4 x = ld_shared_v4(part + chunk_at<D>(r, g));
+              const uint4 x = ld_shared_v4(from);
               v[i][0] = x.x;
               v[i][1] = x.y;
               v[i][2] = x.z;
               v[i][3] = x.w;
             }
           }
-          if (partial) {
+          if constexpr (PARTIAL) {
             // a NaN in a masked place would turn 0 * NaN into NaN: NaN codes
             // are taken out here and their effect on the rows that see them
             // is added below
@@ -443,58 +456,62 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             #pragma unroll
             for (int u = 0; u < 2; ++u) {
               const uint32_t sel = u ? 0x7362u : 0x5140u;
-              const uint32_t x = __byte_perm(v[0][w], v[1][w], sel);
-              const uint32_t y = __byte_perm(v[2][w], v[3][w], sel);
               uint32_t a0, a1, a2, a3;
-              widen4(x, a0, a1);
-              widen4(y, a2, a3);
+              widen4(__byte_perm(v[0][w], v[1][w], sel), a0, a1);
+              widen4(__byte_perm(v[2][w], v[3][w], sel), a2, a3);
               #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
                 mma(acc[half * 8 + 2 * w + u][nt], a0, a1, a2, a3, p0[nt], p1[nt]);
             }
         }
-        if (partial && __any_sync(0xffffffffu, nans)) {
-          // how many NaN values each row sees in each column: the product of
-          // the NaN places with the places that the rows see
-          uint32_t c0[NT], c1[NT];
-          #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float w[4];
-            #pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = s[nt][k] == -INFINITY ? 0.f : 1.f;
-            c0[nt] = transpose8x8(pack2<false>(w[0], w[1]));
-            c1[nt] = transpose8x8(pack2<false>(w[2], w[3]));
-          }
-          #pragma unroll
-          for (int im = 0; im < kMT; ++im) {
-            // columns of fragment im held by this lane: words of the loads above
-            const int half = im / 8, w = im % 8 / 2, u = im & 1;
-            const uint32_t part = vt + half * T::kKeys * T::kPitch;
-            uint32_t n[4];
-            #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = (i & 1 ? vb : va) + (i >> 1) * 8;
-              const uint32_t a = D == 64 ? part + chunk_at<D>(r, g >> 1) + (g & 1) * 8 + 4 * w
-                                         : part + chunk_at<D>(r, g) + 4 * w;
-              uint32_t x;
-              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(a) : "memory");
-              n[i] = nan_bytes(x) & 0x38383838u;     // 1.0 where the code is NaN
-            }
-            const uint32_t sel = u ? 0x7362u : 0x5140u;
-            const uint32_t x = __byte_perm(n[0], n[1], sel), y = __byte_perm(n[2], n[3], sel);
+        if constexpr (PARTIAL) {
+          if (__any_sync(0xffffffffu, nans)) {
+            // how many NaN values each row sees in each column: the product of
+            // the NaN places with the places that the rows see
+            uint32_t c0[NT], c1[NT];
             #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              float hits[4] = {0.f, 0.f, 0.f, 0.f};
-              uint32_t a0, a1, a2, a3;
-              widen4(x, a0, a1);
-              widen4(y, a2, a3);
-              mma(hits, a0, a1, a2, a3, c0[nt], c1[nt]);
+              float w[4];
               #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (hits[k] > 0.f) acc[im][nt][k] = __uint_as_float(0x7fffffffu);
+              for (int k = 0; k < 4; ++k) w[k] = s[nt][k] == -INFINITY ? 0.f : 1.f;
+              c0[nt] = transpose8x8(pack2<false>(w[0], w[1]));
+              c1[nt] = transpose8x8(pack2<false>(w[2], w[3]));
+            }
+            #pragma unroll
+            for (int im = 0; im < kMT; ++im) {
+              // columns of fragment im held by this lane: words of the loads above
+              const int half = im / 8, w = im % 8 / 2, u = im & 1;
+              const uint32_t part = vt + half * T::kKeys * T::kPitch + mt * kFrag + 4 * w;
+              uint32_t n[4];
+              #pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint32_t x;
+                asm volatile("ld.shared.b32 %0, [%1];"
+                             : "=r"(x) : "r"(part + v_at[i & 1] + (i >> 1) * (kFrag / 2)) : "memory");
+                n[i] = nan_bytes(x) & 0x38383838u;     // 1.0 where the code is NaN
+              }
+              const uint32_t sel = u ? 0x7362u : 0x5140u;
+              uint32_t a0, a1, a2, a3;
+              widen4(__byte_perm(n[0], n[1], sel), a0, a1);
+              widen4(__byte_perm(n[2], n[3], sel), a2, a3);
+              #pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float hits[4] = {0.f, 0.f, 0.f, 0.f};
+                mma(hits, a0, a1, a2, a3, c0[nt], c1[nt]);
+                #pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  if (hits[k] > 0.f) acc[im][nt][k] = __uint_as_float(0x7fffffffu);
+              }
             }
           }
         }
+      };
+      if (k0 + T::kKeys <= at.full) {
+        #pragma unroll
+        for (int mt = 0; mt < T::kKeys / 16; ++mt) fragment(std::false_type{}, mt);
+      } else {
+        #pragma unroll 1
+        for (int mt = 0; mt < T::kKeys / 16 && k0 + mt * 16 < at.lim; ++mt) fragment(std::true_type{}, mt);
       }
       __syncwarp();
       ++done;

@@ -89,8 +89,9 @@ struct Smem {
   static constexpr int kRing = kWarps * kStages * 2 * T::kBytes;
   static constexpr int kQOff = kRing;
   static constexpr int kQBytes = D * NT * 16;              // q fragments, f16
-  static constexpr int kBufOff = kQOff + kQBytes;          // O of two warps while they are joined
-  static constexpr int kBufBytes = 2 * 8 * NT * D * 4;
+  static constexpr int kBufOff = kQOff + kQBytes;          // O of warps while they are joined:
+  static constexpr int kBufWarps = NT * D < 256 ? 2 : 1;   // of one where two CTAs would not fit an SM
+  static constexpr int kBufBytes = kBufWarps * 8 * NT * D * 4;
   static constexpr int kStatOff = kBufOff + kBufBytes;     // (maximum, sum) [warp][row]
   static constexpr int kStatBytes = kWarps * 8 * NT * 8;
   static constexpr int kQsOff = kStatOff + kStatBytes;     // [row] power of two taken off q
@@ -99,6 +100,7 @@ struct Smem {
   static constexpr int kBarOff = kMetaOff + kMetaBytes;
   static constexpr int kMiscOff = kBarOff + kWarps * kStages * 8;
   static constexpr int kAlloc = kMiscOff + 64 + 1024;      // slack to align the base
+  static_assert(2 * (kAlloc + 1024) <= 228 * 1024, "two CTAs an SM");
 };
 
 template <int D, int NT>
@@ -551,32 +553,43 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           acc[i][nt][c + 2] *= f;
         }
       }
-    float4* buf = reinterpret_cast<float4*>(smem + S::kBufOff);
-    #pragma unroll
-    for (int round = 2; round > 0; round >>= 1) {
-      if (warp >= round && warp < 2 * round) {
-        float4* to = buf + (warp - round) * kMT * NT * 32 + lane;
+    float4* buf = reinterpret_cast<float4*>(smem + S::kBufOff) + lane;
+    auto hand_over = [&](int place) {
+      #pragma unroll
+      for (int i = 0; i < kMT; ++i)
         #pragma unroll
-        for (int i = 0; i < kMT; ++i)
-          #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            to[(i * NT + nt) * 32] = make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]);
-      }
-      __syncthreads();
-      if (warp < round) {
-        const float4* from = buf + warp * kMT * NT * 32 + lane;
+        for (int nt = 0; nt < NT; ++nt)
+          buf[((place * kMT + i) * NT + nt) * 32] =
+              make_float4(acc[i][nt][0], acc[i][nt][1], acc[i][nt][2], acc[i][nt][3]);
+    };
+    auto take_over = [&](int place) {
+      #pragma unroll
+      for (int i = 0; i < kMT; ++i)
         #pragma unroll
-        for (int i = 0; i < kMT; ++i)
-          #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const float4 x = from[(i * NT + nt) * 32];
-            acc[i][nt][0] += x.x;
-            acc[i][nt][1] += x.y;
-            acc[i][nt][2] += x.z;
-            acc[i][nt][3] += x.w;
-          }
+        for (int nt = 0; nt < NT; ++nt) {
+          const float4 x = buf[((place * kMT + i) * NT + nt) * 32];
+          acc[i][nt][0] += x.x;
+          acc[i][nt][1] += x.y;
+          acc[i][nt][2] += x.z;
+          acc[i][nt][3] += x.w;
+        }
+    };
+    if constexpr (S::kBufWarps == 2) {
+      #pragma unroll
+      for (int round = 2; round > 0; round >>= 1) {
+        if (warp >= round && warp < 2 * round) hand_over(warp - round);
+        __syncthreads();
+        if (warp < round) take_over(warp);
+        __syncthreads();
       }
-      __syncthreads();
+    } else {
+      #pragma unroll 1
+      for (int from = 1; from < kWarps; ++from) {
+        if (warp == from) hand_over(0);
+        __syncthreads();
+        if (warp == 0) take_over(0);
+        __syncthreads();
+      }
     }
     if (warp == 0) {
       const bool whole = at.s0 == 0 && at.s1 == at.steps;
@@ -634,12 +647,13 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   }
 }
 
-// Rows of a unit's tile: the fewest 8-row fragments that hold all G * Nq rows,
-// up to what the accumulators of a warp allow (128 registers of O).
+// The rows that a unit of this kernel holds at most.
+int most_rows(int d) { return d == 64 ? 32 : d == 128 ? 16 : 8; }
+
+// Rows of a unit's tile: the fewest 8-row fragments that hold all G * Nq rows.
 int row_fragments(int rows, int d) {
-  const int most = d == 64 ? 8 : d == 128 ? 4 : 2;
   int nt = 1;
-  while (nt < most && 8 * nt < rows) nt *= 2;
+  while (8 * nt < most_rows(d) && 8 * nt < rows) nt *= 2;
   return nt;
 }
 
@@ -685,9 +699,12 @@ cudaError_t launch(const Cache& cache, FwdCacheParams& p, int sms, cudaStream_t 
 
 namespace {
 
-// Whether the tcgen05 kernel takes the call: from one row more than a tile of
-// this file's kernel holds.
-bool many_rows(long long rows, int d) { return rows > (d == 64 ? 64 : d == 128 ? 32 : 16); }
+// Whether the tcgen05 kernel takes the call: at d <= 128 from more rows than two
+// units of this file's kernel hold, at d = 256 than one.  Measured (B = 8,
+// 8 key/value heads, 8192 tokens), this kernel / the other: d = 64 at 64 rows
+// 57 / 63 us, at 128 rows 91 / 66; d = 128 at 32 rows 64 / 74, at 64 rows
+// 107 / 76; d = 256 at 8 rows 64 / 70, at 16 rows 103 / 71.
+bool many_rows(long long rows, int d) { return rows > (d == 256 ? 1 : 2) * most_rows(d); }
 
 // Rows of a unit, and CTAs at most.
 void unit_shape(long long rows, int d, int sms, size_t* unit_rows, size_t* ctas) {
@@ -742,12 +759,9 @@ cudaError_t launch_cache_fwd(const Cache& cache, const CacheFwdCall& c, int sms,
     case 64 * 16 + 1: return launch<64, 1>(cache, p, sms, stream);
     case 64 * 16 + 2: return launch<64, 2>(cache, p, sms, stream);
     case 64 * 16 + 4: return launch<64, 4>(cache, p, sms, stream);
-    case 64 * 16 + 8: return launch<64, 8>(cache, p, sms, stream);
     case 128 * 16 + 1: return launch<128, 1>(cache, p, sms, stream);
     case 128 * 16 + 2: return launch<128, 2>(cache, p, sms, stream);
-    case 128 * 16 + 4: return launch<128, 4>(cache, p, sms, stream);
     case 256 * 16 + 1: return launch<256, 1>(cache, p, sms, stream);
-    case 256 * 16 + 2: return launch<256, 2>(cache, p, sms, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -400,96 +400,142 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
       int kp = 0, vp = 0;                 // pieces of K and V consumed
       int pf[2] = {0, 0};                 // P_FULL phases consumed, by score buffer
       bool ok = true;
-      // S = Q K^T of row tile u into score buffer `buf`, from K pieces
-      // `first` on; `free`: the pieces' last use
-      auto scores = [&](int u, int buf, int first, bool free) -> bool {
+      // Products are issued by small loops: a tile's run of them unrolled does
+      // not stay in the instruction cache beside the other roles' loops, and
+      // issuing took longer than the products.
+      // S (+)= part c of Q K^T of row tile u, into score buffer `buf`, from the
+      // K piece in place s
+      auto scores = [&](int u, int buf, int c, int s) {
+        uint64_t qs = desc_add(q_desc, u * L::kQTile + c * (128 * L::kKCols));
+        uint32_t more = c > 0;
         #pragma unroll 1
-        for (int c = 0; c < L::kKParts; ++c) {
-          const int n = first + c, s = n % L::kKStages;
-          if (!wait_uniform(bar(L::kKFull + s), (n / L::kKStages) & 1, abort)) return false;
-          tc_fence_after();
-          const uint64_t ks = desc_add(k_desc, s * L::kKPiece);
-          #pragma unroll 1
-          for (int q = 0; q < q_parts; ++q) {
-            const uint64_t qs = desc_add(q_desc, u * L::kQTile + q * L::kQPart + c * (128 * L::kKCols));
-            #pragma unroll
-            for (int w = 0; w < L::kKCols / 32; ++w)
-              mma_ss_e4m3(tmem + L::kTS + 128 * buf, desc_add(qs, w * 32), desc_add(ks, w * 32), kIdS,
-                          (c > 0 || q > 0 || w > 0) ? 1u : 0u);
+        for (int q = 0; q < q_parts; ++q) {
+          uint64_t ks = desc_add(k_desc, s * L::kKPiece);
+          #pragma unroll 4
+          for (int w = 0; w < L::kKCols / 32; ++w) {
+            mma_ss_e4m3(tmem + L::kTS + 128 * buf, qs, ks, kIdS, more);
+            qs = desc_add(qs, 32);
+            ks = desc_add(ks, 32);
+            more = 1;
           }
-          if (free) mma_commit(bar(L::kKEmpty + s));
+          qs = desc_add(qs, L::kQPart - L::kKCols);
         }
-        mma_commit(bar(L::kSFull + buf));
-        return true;
       };
-      auto values = [&](int u, int buf, int first, bool fresh, bool free) -> bool {
-        #pragma unroll 1
-        for (int h = 0; h < L::kVParts; ++h) {
-          const int n = first + h, s = n % L::kVStages;
-          if (!wait_uniform(bar(L::kVFull + s), (n / L::kVStages) & 1, abort)) return false;
-          tc_fence_after();
-          const uint64_t vs = desc_add(v_desc, s * L::kVPiece);
-          #pragma unroll
-          for (int w = 0; w < L::kVKeys / 16; ++w)
-            mma_ts(tmem + L::kTO + D * u, tmem + L::kTS + 128 * buf + (h * (L::kVKeys / 16) + w) * 8,
-                   desc_add(vs, w * 2048), kIdO, (!fresh || h > 0 || w > 0) ? 1u : 0u);
-          if (free) mma_commit(bar(L::kVEmpty + s));
+      // O (+)= part h of P V of row tile u, P from score buffer `buf`, from the
+      // V piece in place s
+      auto values = [&](int u, int buf, int h, int s, bool fresh) {
+        uint64_t vs = desc_add(v_desc, s * L::kVPiece);
+        uint32_t from = tmem + L::kTS + 128 * buf + h * (L::kVKeys / 2);
+        uint32_t more = !fresh || h > 0;
+        #pragma unroll 4
+        for (int w = 0; w < L::kVKeys / 16; ++w) {
+          mma_ts(tmem + L::kTO + D * u, from, vs, kIdO, more);
+          vs = desc_add(vs, 2048);
+          from += 8;
+          more = 1;
         }
-        return true;
       };
+      auto k_wait = [&](int n) { return wait_uniform(bar(L::kKFull + n % L::kKStages), (n / L::kKStages) & 1, abort); };
+      auto v_wait = [&](int n) { return wait_uniform(bar(L::kVFull + n % L::kVStages), (n / L::kVStages) & 1, abort); };
+      auto lane0 = [&](int x) { return __shfl_sync(0xffffffffu, x, 0); };
       int g = 0;   // tiles so far
       for (int np = 0; ok; ++np) {
         if (!piece_wait(np)) break;
-        // (read from lane 0: the same in every lane, on the uniform datapath)
         struct { int s0, s1, end[2]; } w;
-        w.s0 = __shfl_sync(0xffffffffu, piece(np)->s0, 0);
-        w.s1 = __shfl_sync(0xffffffffu, piece(np)->s1, 0);
-        w.end[0] = __shfl_sync(0xffffffffu, piece(np)->end[0], 0);
-        w.end[1] = __shfl_sync(0xffffffffu, piece(np)->end[1], 0);
+        w.s0 = lane0(piece(np)->s0);
+        w.s1 = lane0(piece(np)->s1);
+        w.end[0] = lane0(piece(np)->end[0]);
+        w.end[1] = lane0(piece(np)->end[1]);
         piece_done(np);
         if (w.s1 < 0) break;
         ok = wait_uniform(bar(L::kQFull), np & 1, abort);
         if (!ok) break;
         tc_fence_after();
         if constexpr (L::kTiles == 1) {
-          ok = scores(0, g & 1, kp, true);
+          // one row tile, its scores a tile ahead in the other buffer
+          auto next_scores = [&](int buf) -> bool {
+            #pragma unroll 1
+            for (int c = 0; c < L::kKParts; ++c, ++kp) {
+              if (!k_wait(kp)) return false;
+              tc_fence_after();
+              const int s = lane0(kp % L::kKStages);
+              scores(0, buf, c, s);
+              mma_commit(bar(L::kKEmpty + s));
+            }
+            mma_commit(bar(L::kSFull + buf));
+            return true;
+          };
+          ok = next_scores(lane0(g & 1));
           for (int j = w.s0; ok && j < w.s1; ++j, ++g) {
             if (j + 1 < w.s1) {
-              if (!scores(0, (g + 1) & 1, kp + L::kKParts, true)) { ok = false; break; }
+              if (!next_scores(lane0((g + 1) & 1))) { ok = false; break; }
             } else {
               mma_commit(bar(L::kQEmpty));
             }
-            if (!wait_uniform(bar(L::kPFull + (g & 1)), (g >> 1) & 1, abort)) { ok = false; break; }
-            tc_fence_after();
-            if (!values(0, g & 1, vp, j == w.s0, true)) { ok = false; break; }
+            const int buf = lane0(g & 1);
+            if (!wait_uniform(bar(L::kPFull + buf), (g >> 1) & 1, abort)) { ok = false; break; }
+            #pragma unroll 1
+            for (int h = 0; h < L::kVParts; ++h, ++vp) {
+              if (ok) ok = v_wait(vp);
+              if (!ok) break;
+              tc_fence_after();
+              const int s = lane0(vp % L::kVStages);
+              values(0, buf, h, s, j == w.s0);
+              mma_commit(bar(L::kVEmpty + s));
+            }
+            if (!ok) break;
             mma_commit(bar(L::kODone));
             mma_commit(bar(L::kTileEmpty + (g & 7)));
-            kp += L::kKParts;
-            vp += L::kVParts;
           }
         } else {
+          // two row tiles by turns, P V of a tile and its next scores together
           const bool a0 = w.s0 < w.end[0], b0 = w.s0 < w.end[1];
-          if (a0) ok = scores(0, 0, kp, !b0);
-          if (ok && b0) ok = scores(1, 1, kp, true);
+          ok = k_wait(kp);
+          if (!ok) break;
+          tc_fence_after();
+          {
+            const int s = lane0(kp % L::kKStages);
+            if (a0) {
+              scores(0, 0, 0, s);
+              mma_commit(bar(L::kSFull));
+            }
+            if (b0) {
+              scores(1, 1, 0, s);
+              mma_commit(bar(L::kSFull + 1));
+            }
+            mma_commit(bar(L::kKEmpty + s));
+            ++kp;
+          }
           if (w.s1 - w.s0 == 1) mma_commit(bar(L::kQEmpty));
-          for (int j = w.s0; ok && j < w.s1; ++j, ++g) {
-            // tile u takes part in this step (v) and in the next (n)
-            const bool v0 = j < w.end[0], v1 = j < w.end[1];
-            const bool n0 = j + 1 < w.end[0], n1 = j + 1 < w.end[1];
+          for (int j = w.s0; ok && j < w.s1; ++j, ++g, ++vp) {
+            // the tile's V and the next tile's K before the waits for P, so
+            // that none sits between P V and the next scores
+            const bool next = j + 1 < w.s1;
+            ok = v_wait(vp) && (!next || k_wait(kp));
+            if (!ok) break;
+            const int sv = lane0(vp % L::kVStages), sk = lane0(kp % L::kKStages);
             #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              if (!ok || !(u ? v1 : v0)) continue;
+              if (!ok || j >= w.end[u]) continue;
               if (!wait_uniform(bar(L::kPFull + u), pf[u] & 1, abort)) { ok = false; continue; }
               ++pf[u];
               tc_fence_after();
-              ok = values(u, u, vp, j == w.s0, u == 1 || !v1);
-              if (ok && j + 1 == w.end[u]) mma_commit(bar(L::kODone + u));
-              if (ok && (u ? n1 : n0)) ok = scores(u, u, kp + L::kKParts, u == 1 || !n1);
+              values(u, u, 0, sv, j == w.s0);
+              if (j + 1 == w.end[u]) {
+                mma_commit(bar(L::kODone + u));
+              } else {
+                scores(u, u, 0, sk);
+                mma_commit(bar(L::kSFull + u));
+              }
             }
+            if (!ok) break;
+            mma_commit(bar(L::kVEmpty + sv));
             mma_commit(bar(L::kTileEmpty + (g & 7)));
-            if (j + 2 == w.s1) mma_commit(bar(L::kQEmpty));
-            kp += L::kKParts;
-            vp += L::kVParts;
+            if (next) {
+              mma_commit(bar(L::kKEmpty + sk));
+              ++kp;
+              if (j + 2 == w.s1) mma_commit(bar(L::kQEmpty));
+            }
           }
         }
       }

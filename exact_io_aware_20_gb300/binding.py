@@ -530,8 +530,9 @@ def _on_stream(device, stream, call, *args):
     """call(*args, raw stream) on the stream given, or on the current stream of
     the tensors' device (an index), which is made current for the call.  On a
     given stream everything the call allocates comes from that stream's memory,
-    so that it is not handed out again before the call's work is done; what it
-    returns is marked as used on the caller's stream too."""
+    and its inputs are marked as used there, so that neither is handed out
+    again before the call's work is done; what it returns is marked as used on
+    the caller's stream too."""
     if device < 0:
         raise ValueError("expected CUDA tensors")
     if stream is None:
@@ -545,6 +546,10 @@ def _on_stream(device, stream, call, *args):
     with torch.cuda.stream(stream):
         out = call(*args, stream.cuda_stream or None)
     if stream != caller:
+        for a in args:
+            for t in a.tensors if isinstance(a, Cache) else (a,):
+                if isinstance(t, torch.Tensor):
+                    t.record_stream(stream)
         for t in out if isinstance(out, tuple) else (out,):
             if t is not None:
                 t.record_stream(caller)
@@ -681,7 +686,7 @@ def _forward_cache(q, cache, seq_lens, causal, scale, new_lens, out, lse, worksp
             raise ValueError("the workspace must be on the inputs' device")
         ws_bytes = workspace.numel() * workspace.element_size()
     _check(load().fa_fwd_cache(
-        q.data_ptr(), cache._ref, out.data_ptr(), lse.data_ptr(), B, H, Nq, causal, scale, code,
+        q.data_ptr(), cache._ref, out.data_ptr(), lse.data_ptr(), B, H, Nq, int(causal), float(scale), code,
         _ints(seq_lens, (B,), device, "seq_lens"), _ints(new_lens, (B,), device, "new_lens"), st,
         workspace.data_ptr(), ws_bytes, stream), "fa_fwd_cache")
     return out, lse

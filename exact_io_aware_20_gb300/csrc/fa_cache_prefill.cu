@@ -28,6 +28,7 @@
 // costs a trip to L2: the walk lives in one warp for that reason.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "cache_work.cuh"
 
@@ -40,7 +41,7 @@ template <int D>
 struct Pre {
   static constexpr int kTiles = D == 256 ? 1 : 2;
   static constexpr int kRows = 128 * kTiles;        // of a unit
-  static constexpr int kOver = kTiles == 1 ? 5 : 6;    // a unit's cost besides its steps, in steps
+  static constexpr int kOver = kTiles == 1 ? 5 : 8;    // a unit's cost besides its steps, in steps
   static constexpr int kSoftWarps = 4 * kTiles;
   static constexpr int kConvWarps = 12 - kSoftWarps;
   static constexpr int kConvRows = 128 / kConvWarps;   // keys of a tile that a warp converts
@@ -188,8 +189,7 @@ __device__ __forceinline__ uint32_t take_e4m3(uint32_t& x) {
   return two;
 }
 
-// SEG: keys that share their scales for certain (64 when a page holds at least
-// as many, 16 otherwise).
+// SEG: keys that share their scales for certain (a page's, 64 at most).
 template <int D, int SEG>
 __global__ void __launch_bounds__(kThreads, 1)
 cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
@@ -859,8 +859,7 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
       const bool nans = nan_seen[np & 3] != 0;
       const int nan_from = max(s0, w->all / 128) * 128, nan_to = min(s1 * 128, sees);
       piece_done(np);
-      #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      auto write = [&](auto with_nans, int c) {
         uint32_t o[32];
         #pragma unroll
         for (int k = 0; k < 32; ++k) o[k] = 0u;
@@ -869,10 +868,10 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
           tmem_ld_wait();
           reg_fence(o);
         }
-        if (nans && in) {
+        if constexpr (decltype(with_nans)::value) {
           // NaN codes among the values that this row sees in tiles where the
           // conversion left them out (rare: a loop over those keys)
-          for (int key = nan_from; key < nan_to; ++key) {
+          for (int key = nan_from; in && key < nan_to; ++key) {
             int page = p.table[static_cast<long long>(b) * p.width + (key >> p.page_log2)];
             if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.pages)) page = 0;
             const uint32_t* row = reinterpret_cast<const uint32_t*>(
@@ -907,6 +906,13 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
               dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
         }
+      };
+      if (nans) {     // (the same for the whole CTA)
+        #pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) write(std::true_type{}, c);
+      } else {
+        #pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) write(std::false_type{}, c);
       }
       if (in) {
         if (whole)
@@ -940,6 +946,11 @@ cudaError_t launch_seg(const Cache& cache, FwdCacheParams& p, int sms, cudaStrea
   if (!set[dev & 63]) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Pre<D>::kAlloc);
     if (e != cudaSuccess) return e;
+    // the warpgroups share out the registers that the launch comes with: with
+    // fewer of them, those that ask for more would wait for ever
+    cudaFuncAttributes attr;
+    if ((e = cudaFuncGetAttributes(&attr, kern)) != cudaSuccess) return e;
+    if (attr.numRegs != 128) return cudaErrorInvalidConfiguration;
     set[dev & 63] = true;
   }
   CUtensorMap tk;
@@ -954,8 +965,9 @@ cudaError_t launch_seg(const Cache& cache, FwdCacheParams& p, int sms, cudaStrea
 
 template <int D>
 cudaError_t launch(const Cache& cache, FwdCacheParams& p, int sms, cudaStream_t stream) {
-  return cache.page >= 64 ? launch_seg<D, 64>(cache, p, sms, stream)
-                          : launch_seg<D, 16>(cache, p, sms, stream);
+  return cache.page >= 64   ? launch_seg<D, 64>(cache, p, sms, stream)
+         : cache.page == 32 ? launch_seg<D, 32>(cache, p, sms, stream)
+                            : launch_seg<D, 16>(cache, p, sms, stream);
 }
 
 }  // namespace

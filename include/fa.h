@@ -387,7 +387,8 @@ int fa_cache_append(const fa_cache *cache, const void *q, const void *k, const v
  * Scales must be positive and finite, between 2^-100 and 2^120.
  * strides[2]: of q, o; NULL: contiguous.  workspace: device memory of at
  * least fa_fwd_cache_workspace_size(...) bytes for the current device,
- * 256-byte aligned; its contents on entry do not matter.  Sequences with a
+ * 256-byte aligned; its contents on entry do not matter (calls whose work may
+ * overlap, two streams or two captured graphs, need one each).  Sequences with a
  * length outside 0 .. table_width * page_size or a new_lens entry outside
  * 0 .. Nq count as empty, and pages outside 0 .. pages - 1 give undefined
  * rows (nothing out of range is read): both are reported by the next

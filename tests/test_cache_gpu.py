@@ -493,3 +493,68 @@ def test_a_server_s_run(d, page, H, Hkv):
                 s = float(K.scales[int(table[b][(now[b] - 1) // page]), h])
                 lim = want[b, h, 0].abs() * 2.0 ** -4 + s * 2.0 ** -10 + 1e-5
                 assert ((got - want[b, h, 0]).abs() <= lim).all()
+
+
+def test_on_a_stream_of_its_own():
+    """Calls on a given stream: what they allocate is that stream's, and inputs
+    freed right after a call are not handed out under it."""
+    g = torch.Generator().manual_seed(14)
+    lens = [700, 130]
+    codes, scales, table = ref.make_cache(60, 2, 16, 128, 2, 45, g, lens)
+    cache = device_cache(codes, scales, table)
+    q = torch.randn(2, 4, 3, 128, generator=g).bfloat16()
+    k = torch.randn(2, 2, 3, 128, generator=g).bfloat16()
+    here = binding.Cache(*(t.clone() for t in cache.tensors))
+    rope = binding.Rope([10000.0 ** (-i / 64) for i in range(64)])
+    n = ints(lens)
+    qr = binding.cache_append(here, dev(q), dev(k), dev(k), n, rope=rope)
+    want = binding.forward_cache(qr, here, n, True, 0.1)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        a, b, c = dev(q), dev(k), dev(k)
+        s.wait_stream(torch.cuda.current_stream())
+        qs = binding.cache_append(cache, a, b, c, n, rope=rope, stream=s)
+        del a, b, c
+        torch.full((2, 4, 3, 128), 7.0, device=DEV, dtype=torch.bfloat16)
+        o, lse = binding.forward_cache(qs, cache, n, True, 0.1, stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    binding.device_status(s)
+
+
+def test_two_graphs_with_a_workspace_each_run_together():
+    g = torch.Generator().manual_seed(15)
+    lens = [3000, 2500]
+    codes, scales, table = ref.make_cache(400, 2, 16, 128, 2, 190, g, lens)
+    cache = device_cache(codes, scales, table)
+    n, runs = ints(lens), []
+    for i in range(2):
+        q = torch.randn(2, 8, 1 + 40 * i, 128, generator=g).bfloat16().to(DEV)
+        want = binding.forward_cache(q, cache, n, True, 0.1)
+        s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            out = binding.forward_cache(q, cache, n, True, 0.1)
+        runs.append((graph, s, out, want, q))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for graph, s, *_rest in runs:
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _graph, _s, out, want, _q in runs:
+        assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+    binding.device_status()
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs a second GPU")
+def test_tensors_of_another_device_than_the_current_one():
+    g = torch.Generator().manual_seed(16)
+    codes, scales, table = ref.make_cache(12, 2, 16, 64, 1, 10, g, [150])
+    q = torch.randn(1, 4, 1, 64, generator=g).half()
+    outs = []
+    for d in ("cuda:0", "cuda:1"):
+        c = binding.Cache(*(t.to(d) for t in (*codes, *scales, table)))
+        n = torch.tensor([150], dtype=torch.int32, device=d)
+        outs.append(binding.forward_cache(q.to(d), c, n, True, 0.1)[0].cpu())
+    assert torch.equal(*outs)

@@ -74,7 +74,7 @@ struct Pre {
                        kTileFull = kRecEmpty + 4, kTileEmpty = kTileFull + 8,
                        kNumBars = kTileEmpty + 8;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
-  static constexpr int kRedOff = (kMiscOff + 32 + 15) / 16 * 16;   // start: sums and the found entry
+  static constexpr int kRedOff = (kMiscOff + 48 + 15) / 16 * 16;   // start: sums and the found entry
   static constexpr int kBytes = kRedOff + 2 * 16 * 8 + 16;
   static constexpr int kAlloc = kBytes + 1024;
   static constexpr uint32_t kTS = 0, kTO = 256, kTmemCols = 512;
@@ -202,7 +202,7 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
   uint8_t* smem = smem_raw + (sbase - raw);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kMiscOff);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 4);
-  volatile int* nan_seen = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 8);   // [4 pieces]
+  volatile int* nan_seen = reinterpret_cast<volatile int*>(smem + L::kMiscOff + 8);   // [8 pieces]
   long long* red = reinterpret_cast<long long*>(smem + L::kRedOff);
   longlong2* found = reinterpret_cast<longlong2*>(smem + L::kRedOff + 256);
   float4* meta = reinterpret_cast<float4*>(smem + L::kMetaOff);
@@ -232,9 +232,9 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
       mbar_init(bar(L::kRecFull + s), 1);
       // (read by the products, pages and keys warps, the converters and softmax)
       mbar_init(bar(L::kRecEmpty + s), 3 + L::kConvWarps + L::kSoftWarps);
-      nan_seen[s] = 0;
     }
     for (int s = 0; s < 8; ++s) {
+      nan_seen[s] = 0;
       mbar_init(bar(L::kTileFull + s), 1);
       mbar_init(bar(L::kTileEmpty + s), 1);
     }
@@ -614,9 +614,11 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
       uint4 x[kBatch];
       q_load(x, 0);
       if (np > 0 && !wait_uniform(bar(L::kQEmpty), (np - 1) & 1, abort)) break;
-      // the next piece's flag: no converting warp is there before this one has
-      // announced this piece's q, and the results of piece np - 3 are written
-      if (cw == 0 && lane == 0) nan_seen[(np + 1) & 3] = 0;
+      // The next piece's flag: no converting warp is there before this one has
+      // announced this piece's q.  A softmax group whose row tile has no keys in
+      // the pieces between may be as far behind as the records let it, at piece
+      // np - 3: eight flags.
+      if (cw == 0 && lane == 0) nan_seen[(np + 1) & 7] = 0;
       // (a small loop: unrolled, its instructions came from L2 once a piece, at
       // 600 clocks a row)
       #pragma unroll 1
@@ -699,7 +701,7 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
               }
               vr[c][i] = make_uint4(x[0], x[1], x[2], x[3]);
             }
-          if (any != 0) nan_seen[np & 3] = 1;
+          if (any != 0) nan_seen[np & 7] = 1;
         }
         #pragma unroll
         for (int c = 0; c < L::kChunks; ++c) {
@@ -856,7 +858,8 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
       const float sum = (in && i < w->n) ? l : 0.f;
       const long long slot = 2ll * blockIdx.x + (s0 > 0 ? 0 : 1);
       const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-      const bool nans = nan_seen[np & 3] != 0;
+      // (a tile without keys in this piece may be here before the flag is reset)
+      const bool nans = some && nan_seen[np & 7] != 0;
       const int nan_from = max(s0, w->all / 128) * 128, nan_to = min(s1 * 128, sees);
       piece_done(np);
       auto write = [&](auto with_nans, int c) {
@@ -907,7 +910,7 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
           }
         }
       };
-      if (nans) {     // (the same for the whole CTA)
+      if (nans) {     // (the same for the whole warp)
         #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) write(std::true_type{}, c);
       } else {

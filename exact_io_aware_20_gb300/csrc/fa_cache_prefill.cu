@@ -596,73 +596,75 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
       // ---- q, once the last scores of the piece before are done.  A row is
       // scaled by a power of two to [2^7, 2^8) and becomes e4m3 parts, each
       // what the ones before have left.
-      constexpr int kLanes = D / 8, kPer = 32 / kLanes;        // lanes of a row, rows at a time
-      constexpr int kRowsW = L::kRows / L::kConvWarps;
-      constexpr int kBatch = 4;
-      const int rl = lane / kLanes, cl = lane % kLanes;
-      const uint32_t q_to = sbase + L::kQOff + (8 * cl / L::kKCols) * (128 * L::kKCols) + 8 * (cl & 1);
-      const int row0 = piece(np)->row0 + cw * kRowsW + rl, live = piece(np)->n;
-      const uint16_t* src = p.q + b * p.qs.b + h * p.seq.G * p.qs.h + 8 * cl;
-      auto q_load = [&](uint4 (&x)[kBatch], int i0) {
-        #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int r = row0 + i0 + k * kPer, i = r / p.seq.G;
-          load_16_if(x[k], src + (r - i * p.seq.G) * p.qs.h + i * p.qs.n,
-                     i0 < kRowsW && r < p.rows && i < live);
-        }
-      };
-      uint4 x[kBatch];
-      q_load(x, 0);
+      // A thread does kSeg columns of a row, 16 at a time, in a loop small
+      // enough to stay in the instruction cache; the row is read twice (for its
+      // largest element, then from L1 or L2 for its parts).
+      constexpr int kSeg = L::kKCols, kSegs = D / kSeg, kThreadsQ = 32 * L::kConvWarps;
+      const int live = piece(np)->n;
       if (np > 0 && !wait_uniform(bar(L::kQEmpty), (np - 1) & 1, abort)) break;
       // The next piece's flag: no converting warp is there before this one has
       // announced this piece's q.  A softmax group whose row tile has no keys in
       // the pieces between may be as far behind as the records let it, at piece
       // np - 3: eight flags.
       if (cw == 0 && lane == 0) nan_seen[(np + 1) & 7] = 0;
-      // (a small loop: unrolled, its instructions came from L2 once a piece, at
-      // 600 clocks a row)
       #pragma unroll 1
-      for (int i0 = 0; i0 < kRowsW; i0 += kPer * kBatch) {
-        uint4 ahead[kBatch];
-        q_load(ahead, i0 + kPer * kBatch);
-        uint32_t top[kBatch];      // of the magnitudes, two lanes of 16 bits
+      for (int n = 32 * cw + lane; n < L::kRows * kSegs; n += kThreadsQ) {
+        const int rr = n / kSegs, seg = n % kSegs, r = piece(np)->row0 + rr, i = r / p.seq.G;
+        const bool on = r < p.rows && i < live;
+        const uint16_t* src = p.q + b * p.qs.b + (h * p.seq.G + r - i * p.seq.G) * p.qs.h + i * p.qs.n + kSeg * seg;
+        uint32_t top = 0;      // of the magnitudes, two lanes of 16 bits
         #pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-          top[k] = max_16x2(max_16x2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu),
-                            max_16x2(x[k].z & 0x7fff7fffu, x[k].w & 0x7fff7fffu));
-        #pragma unroll
-        for (int m = kLanes / 2; m > 0; m >>= 1)
+        for (int c = 0; c < kSeg; c += 64) {
+          uint4 x[8];
           #pragma unroll
-          for (int k = 0; k < kBatch; ++k) top[k] = max_16x2(top[k], __shfl_xor_sync(0xffffffffu, top[k], m));
-        #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int rr = cw * kRowsW + i0 + k * kPer + rl, r = rr & 127;
-          const uint32_t top1 = max(top[k] & 0xffffu, top[k] >> 16);
-          float up, down;
-          const float amax = p.bf16 ? __uint_as_float(top1 << 16) : unpack2<false>(top1).x;
-          row_power(amax, &up, &down);
-          // (infinities have no code: their row is NaN, as its scores are)
-          down = amax < __uint_as_float(0x7f800000u) ? down * 128.f : __uint_as_float(0x7fffffffu);
-          if (cl == 0) q_pow[(np & 1) * L::kRows + rr] = up * 0.0078125f;
-          // (below 256 every f16 and bf16 is an f16 to 2^-25)
-          uint32_t f[4];
-          const uint32_t y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-          #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float2 t = p.bf16 ? unpack2<true>(y[c]) : unpack2<false>(y[c]);
-            f[c] = pack2<false>(t.x * down, t.y * down);
+          for (int k = 0; k < 8; ++k) {
+            x[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (on) x[k] = *reinterpret_cast<const uint4*>(src + c + 8 * k);
           }
-          const uint32_t to = q_to + (rr >> 7) * L::kQTile + row_chunk<L::kKCols>(r, (cl >> 1) % (L::kKCols / 16));
+          #pragma unroll
+          for (int k = 0; k < 8; ++k)
+            top = max_16x2(top, max_16x2(max_16x2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu),
+                                         max_16x2(x[k].z & 0x7fff7fffu, x[k].w & 0x7fff7fffu)));
+        }
+        if constexpr (kSegs == 2) top = max_16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        const uint32_t top1 = max(top & 0xffffu, top >> 16);
+        float up, down;
+        const float amax = p.bf16 ? __uint_as_float(top1 << 16) : unpack2<false>(top1).x;
+        row_power(amax, &up, &down);
+        // (infinities have no code: their row is NaN, as its scores are)
+        down = amax < __uint_as_float(0x7f800000u) ? down * 128.f : __uint_as_float(0x7fffffffu);
+        if (seg == 0) q_pow[(np & 1) * L::kRows + rr] = up * 0.0078125f;
+        const uint32_t to = sbase + L::kQOff + (rr >> 7) * L::kQTile + seg * (128 * kSeg);
+        uint4 ahead[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+        if (on) {
+          ahead[0] = *reinterpret_cast<const uint4*>(src);
+          ahead[1] = *reinterpret_cast<const uint4*>(src + 8);
+        }
+        #pragma unroll 1
+        for (int c = 0; c < kSeg / 16; ++c) {
+          const uint32_t y[8] = {ahead[0].x, ahead[0].y, ahead[0].z, ahead[0].w,
+                                 ahead[1].x, ahead[1].y, ahead[1].z, ahead[1].w};
+          if (on && c + 1 < kSeg / 16) {
+            ahead[0] = *reinterpret_cast<const uint4*>(src + 16 * c + 16);
+            ahead[1] = *reinterpret_cast<const uint4*>(src + 16 * c + 24);
+          }
+          uint32_t f[8];      // (below 256 every f16 and bf16 is an f16 to 2^-25)
+          #pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float2 t = p.bf16 ? unpack2<true>(y[k]) : unpack2<false>(y[k]);
+            f[k] = pack2<false>(t.x * down, t.y * down);
+          }
+          const uint32_t at = to + row_chunk<kSeg>(rr & 127, c);
           #pragma unroll
           for (int q = 0; q < 3; ++q) {
             if (q == 2 && p.bf16) break;
-            const uint32_t w0 = __byte_perm(take_e4m3(f[0]), take_e4m3(f[1]), 0x5410);
-            const uint32_t w1 = __byte_perm(take_e4m3(f[2]), take_e4m3(f[3]), 0x5410);
-            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(to + q * L::kQPart), "r"(w0), "r"(w1) : "memory");
+            uint32_t w[4];
+            #pragma unroll
+            for (int k = 0; k < 4; ++k)
+              w[k] = __byte_perm(take_e4m3(f[2 * k]), take_e4m3(f[2 * k + 1]), 0x5410);
+            st_shared_v4(at + q * L::kQPart, w[0], w[1], w[2], w[3]);
           }
         }
-        #pragma unroll
-        for (int k = 0; k < kBatch; ++k) x[k] = ahead[k];
       }
       fence_proxy_async_smem();
       mbar_arrive_warp(bar(L::kQFull));

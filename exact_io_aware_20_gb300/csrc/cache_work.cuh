@@ -43,6 +43,7 @@ struct FwdCacheParams {
   float scale_log2;
   float* part_o;          // [CTA][2][RT][D]: O of a piece, not divided by its sum
   float2* part_ml;        // [CTA][2][RT]: its running maximum (log2 units) and sum
+  int4* joins;            // [CTA], the many-row kernel's: its unit that goes on behind its share
   int ctas;
 };
 
@@ -249,96 +250,131 @@ struct Walk {
 
 // Joins the pieces of units that lie in several shares, and writes the units
 // that see no key.  Block (c, y) looks for the unit whose steps begin in share
-// c and go on behind it; its warps take a row each: the pieces' weights first,
-// then their O, four loads in flight.
-constexpr int kMergeThreads = 128;
-template <int D, int RT, int STEP, int OVER>
+// c and go on behind it; its warps take a row each, or with RECORDS four (there
+// are few pieces and many rows): the pieces' weights first, then their O, four
+// loads in flight.
+//
+// RECORDS: the attention kernel has left that unit in p.joins[c] (entry, head,
+// last CTA, tokens of the sequence; last CTA < 0: there is none).  With many
+// rows a unit is many blocks' work, and each block's own search was most of
+// this kernel's time (d = 128, 4 prompts of 2048 tokens: 20 us of the call's
+// 130; 10 with the records, 6 with four rows a warp).  With few rows the search
+// is over before the attention kernel's end, and a record would be one more
+// read behind it.
+constexpr int kMergeThreads = 128, kMergeRows = 4;
+template <int D, int RT, int STEP, int OVER, bool RECORDS>
 __global__ void __launch_bounds__(kMergeThreads)
 cache_merge_kernel(const __grid_constant__ FwdCacheParams p) {
   constexpr int kVec = D / 32, kWarps = kMergeThreads / 32;
+  constexpr int kRows = RECORDS ? kMergeRows : 1;      // of a warp at a time
+  constexpr int kLanes = 32 / kRows;                   // that share out a row's pieces
+  constexpr int kPieces = RECORDS ? 1 : 4;             // whose O is in flight at once
   __shared__ long long red[2 * kWarps];
   __shared__ longlong2 found;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row_first = blockIdx.y * kWarps + warp, row_step = gridDim.y * kWarps;
   bool bad = false;
   const int c0 = blockIdx.x;
-  long long share = 0, end = 0;
-  bool joins = false;
-  find_place<RT, STEP, OVER, kMergeThreads>(p, red, &found, &bad, [&](long long count) {
-    const long long total = count * p.Hkv;
-    share = (total + p.ctas - 1) / p.ctas;
-    end = (c0 + 1) * share;
-    joins = end < total && share > 0;      // (share > 0 wherever a step is)
-    return joins ? (end - 1) / p.Hkv : -1ll;
-  });
-  Walk<RT, STEP, OVER> at;
-  int c1 = 0;
-  if (joins) {
-    at.start(p, &found, end - 1, 1);
-    const long long first = end - 1 - at.place + OVER, last = first + at.steps - 1;   // its steps
-    joins = last >= end && first >= end - share && first < end;
-    c1 = static_cast<int>(last / share);
+  int4 join = make_int4(0, 0, -1, 0);
+  if constexpr (RECORDS) {
+    grid_dependency_wait();
+    join = p.joins[c0];
+  } else {
+    long long share = 0, end = 0;
+    bool joins = false;
+    find_place<RT, STEP, OVER, kMergeThreads>(p, red, &found, &bad, [&](long long count) {
+      const long long total = count * p.Hkv;
+      share = (total + p.ctas - 1) / p.ctas;
+      end = (c0 + 1) * share;
+      joins = end < total && share > 0;      // (share > 0 wherever a step is)
+      return joins ? (end - 1) / p.Hkv : -1ll;
+    });
+    if (joins) {
+      Walk<RT, STEP, OVER> at;
+      at.start(p, &found, end - 1, 1);
+      const long long first = end - 1 - at.place + OVER, last = first + at.steps - 1;   // its steps
+      if (last >= end && first >= end - share && first < end)
+        join = make_int4(at.e, at.h, static_cast<int>(last / share), at.seq.n);
+    }
+    grid_dependency_wait();   // (every CTA: this grid's end is to imply the other's)
   }
-  grid_dependency_wait();   // (every CTA: this grid's end is to imply the other's)
-  if (joins) {
-    const int row0 = at.e % p.row_tiles * RT, b = at.e / p.row_tiles;
-    for (int rr = row_first; rr < RT && row0 + rr < p.rows; rr += row_step) {
-      const int r = row0 + rr, i = r / p.seq.G, head = at.h * p.seq.G + r % p.seq.G;
+  const int c1 = join.z;
+  if (c1 > c0) {
+    const int b = join.x / p.row_tiles, row0 = (join.x - b * p.row_tiles) * RT;
+    const int own = lane / kLanes, pl = lane % kLanes;    // the weights that this lane works out
+    for (int first = kRows * row_first; first < RT && row0 + first < p.rows; first += kRows * row_step) {
+      const int rr = first + own;
+      const bool on = row0 + rr < p.rows;
       float top = kNoMax, sum = 0.f;
-      float acc[kVec];
+      float acc[kRows][kVec];
       #pragma unroll
-      for (int k = 0; k < kVec; ++k) acc[k] = 0.f;
-      for (int c = c0 + lane; c <= c1; c += 32)
+      for (int k = 0; k < kRows; ++k)
+        #pragma unroll
+        for (int v = 0; v < kVec; ++v) acc[k][v] = 0.f;
+      for (int c = c0 + pl; on && c <= c1; c += kLanes)
         top = fmaxf(top, p.part_ml[(2ll * c + (c == c0)) * RT + rr].x);
       #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      for (int cb = c0; cb <= c1; cb += 32) {
+      for (int x = kLanes / 2; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      for (int cb = c0; cb <= c1; cb += kLanes) {
         float2 ml = make_float2(kNoMax, 0.f);
-        const int mine = cb + lane;
-        if (mine <= c1) ml = p.part_ml[(2ll * mine + (mine == c0)) * RT + rr];
+        const int mine = cb + pl;
+        if (on && mine <= c1) ml = p.part_ml[(2ll * mine + (mine == c0)) * RT + rr];
         const float w = ex2_approx(ml.x - top);
         float part = ml.y == 0.f ? 0.f : ml.y * w;
         #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) part += __shfl_xor_sync(0xffffffffu, part, x);
+        for (int x = kLanes / 2; x > 0; x >>= 1) part += __shfl_xor_sync(0xffffffffu, part, x);
         sum += part;
         // a piece without keys for the row has left its O unwritten
         const uint32_t has = __ballot_sync(0xffffffffu, ml.y != 0.f);
-        const int n = min(32, c1 - cb + 1);
-        for (int k0 = 0; k0 < n; k0 += 4) {
-          float x[4][kVec], wk[4];
+        const int n = min(kLanes, c1 - cb + 1);
+        for (int k0 = 0; k0 < n; k0 += kPieces) {
+          float x[kRows][kPieces][kVec], wk[kRows][kPieces];
           #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            wk[k] = __shfl_sync(0xffffffffu, w, (k0 + k) & 31);
+          for (int k = 0; k < kPieces; ++k) {
             const int c = cb + k0 + k;
             #pragma unroll
-            for (int v = 0; v < kVec; ++v) x[k][v] = 0.f;
-            if (k0 + k < n && (has >> (k0 + k) & 1)) {
-              const float* src = p.part_o + ((2ll * c + (c == c0)) * RT + rr) * D + lane * kVec;
+            for (int y = 0; y < kRows; ++y) {
+              const int from = kLanes * y + ((k0 + k) & (kLanes - 1));
+              wk[y][k] = __shfl_sync(0xffffffffu, w, from);
               #pragma unroll
-              for (int v = 0; v < kVec; v += 2) {
-                const float2 y = *reinterpret_cast<const float2*>(src + v);
-                x[k][v] = y.x;
-                x[k][v + 1] = y.y;
+              for (int v = 0; v < kVec; ++v) x[y][k][v] = 0.f;
+              if (k0 + k < n && (has >> from & 1)) {
+                const float* src = p.part_o + ((2ll * c + (c == c0)) * RT + first + y) * D + lane * kVec;
+                #pragma unroll
+                for (int v = 0; v < kVec; v += 2) {
+                  const float2 z = *reinterpret_cast<const float2*>(src + v);
+                  x[y][k][v] = z.x;
+                  x[y][k][v + 1] = z.y;
+                }
               }
             }
           }
           #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < kPieces; ++k)
             #pragma unroll
-            for (int v = 0; v < kVec; ++v) acc[v] = fmaf(x[k][v], wk[k], acc[v]);
+            for (int y = 0; y < kRows; ++y)
+              #pragma unroll
+              for (int v = 0; v < kVec; ++v) acc[y][v] = fmaf(x[y][k][v], wk[y][k], acc[y][v]);
         }
       }
-      if (i >= at.seq.n) sum = 0.f;
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + b * p.os.b + head * p.os.h + i * p.os.n + lane * kVec);
+      if ((row0 + rr) / p.seq.G >= join.w) sum = 0.f;
       #pragma unroll
-      for (int v = 0; v < kVec; v += 2)
-        dst[v / 2] = sum == 0.f ? 0u
-                     : p.bf16 ? pack2<true>(acc[v] * inv, acc[v + 1] * inv)
-                              : pack2<false>(acc[v] * inv, acc[v + 1] * inv);
-      if (lane == 0)
-        p.lse[(static_cast<long long>(b) * p.H + head) * p.seq.Nq + i] =
-            sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLogE2;
+      for (int y = 0; y < kRows; ++y) {
+        const int r = row0 + first + y;
+        const float total = __shfl_sync(0xffffffffu, sum, kLanes * y), m = __shfl_sync(0xffffffffu, top, kLanes * y);
+        if (r >= p.rows) break;
+        const int i = r / p.seq.G, head = join.y * p.seq.G + r - i * p.seq.G;
+        const float inv = total == 0.f ? 0.f : 1.f / total;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + b * p.os.b + head * p.os.h + i * p.os.n + lane * kVec);
+        #pragma unroll
+        for (int v = 0; v < kVec; v += 2)
+          dst[v / 2] = total == 0.f ? 0u
+                       : p.bf16 ? pack2<true>(acc[y][v] * inv, acc[y][v + 1] * inv)
+                                : pack2<false>(acc[y][v] * inv, acc[y][v + 1] * inv);
+        if (lane == 0)
+          p.lse[(static_cast<long long>(b) * p.H + head) * p.seq.Nq + i] =
+              total == 0.f ? -INFINITY : (m + log2f(total)) * kLogE2;
+      }
     }
   }
   for (int e = blockIdx.x; e < p.seq.B * p.row_tiles; e += gridDim.x) {
@@ -358,10 +394,10 @@ cache_merge_kernel(const __grid_constant__ FwdCacheParams p) {
 
 // Launches the join behind the attention kernel, as its programmatic
 // dependent.
-template <int D, int RT, int STEP, int OVER>
+template <int D, int RT, int STEP, int OVER, bool RECORDS>
 cudaError_t launch_cache_merge(const FwdCacheParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.ctas), RT > 8 ? RT / 8 : 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.ctas), RECORDS ? RT / (kMergeThreads / 32 * kMergeRows) : RT > 8 ? RT / 8 : 1, 1);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -369,7 +405,7 @@ cudaError_t launch_cache_merge(const FwdCacheParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_merge_kernel<D, RT, STEP, OVER>, p);
+  return cudaLaunchKernelEx(&cfg, cache_merge_kernel<D, RT, STEP, OVER, RECORDS>, p);
 }
 
 // The tcgen05 kernel, for many query rows (fa_cache_prefill.cu): rows of a

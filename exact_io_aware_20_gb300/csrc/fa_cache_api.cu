@@ -190,7 +190,7 @@ extern "C" int fa_cache_append(const fa_cache* cache, const void* q, const void*
 
 extern "C" size_t fa_fwd_cache_workspace_size(int B, int H, int Hkv, int Nq, int d) {
   if (Hkv < 1 || fa::check_sizes(B, H, Nq, d, FA_BF16) != FA_OK || H % Hkv != 0) return 0;
-  return fa::cache_fwd_workspace_bytes(B, H, Hkv, Nq, d, fa::device_sms());
+  return fa::cache_fwd_workspace_bytes(H, Hkv, Nq, d, fa::device_sms());
 }
 
 extern "C" int fa_fwd_cache(const void* q, const fa_cache* cache, void* o, float* lse, int B,
@@ -219,7 +219,7 @@ extern "C" int fa_fwd_cache(const void* q, const fa_cache* cache, void* o, float
   if (!workspace || !fa::aligned(workspace, 256)) return FA_ERR_WORKSPACE;
   if ((st = fa::check_device(&c.err)) != FA_OK) return st;
   const int sms = fa::device_sms();
-  if (workspace_bytes < fa::cache_fwd_workspace_bytes(B, H, ca.Hkv, Nq, ca.d, sms))
+  if (workspace_bytes < fa::cache_fwd_workspace_bytes(H, ca.Hkv, Nq, ca.d, sms))
     return FA_ERR_WORKSPACE;
   c.B = B;
   c.H = H;

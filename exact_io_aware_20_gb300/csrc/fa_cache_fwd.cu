@@ -692,7 +692,7 @@ cudaError_t launch(const Cache& cache, FwdCacheParams& p, int sms, cudaStream_t 
     return e;
   cache_fwd_kernel<D, NT><<<p.ctas, kThreads, Smem<D, NT>::kAlloc, stream>>>(tk, tv, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_cache_merge<D, 8 * NT, Tile<D>::kStep, kOver>(p, stream);
+  return launch_cache_merge<D, 8 * NT, Tile<D>::kStep, kOver, false>(p, stream);
 }
 
 }  // namespace
@@ -716,11 +716,11 @@ void unit_shape(long long rows, int d, int sms, size_t* unit_rows, size_t* ctas)
 
 }  // namespace
 
-// Two pieces of a unit's rows for each CTA.
-size_t cache_fwd_workspace_bytes(int, int H, int Hkv, int Nq, int d, int sms) {
+// Two pieces of a unit's rows for each CTA, and a record.
+size_t cache_fwd_workspace_bytes(int H, int Hkv, int Nq, int d, int sms) {
   size_t rows, ctas;
   unit_shape(1ll * H / Hkv * Nq, d, sms, &rows, &ctas);
-  return 2 * ctas * rows * (d * sizeof(float) + sizeof(float2));
+  return 2 * ctas * rows * (d * sizeof(float) + sizeof(float2)) + ctas * sizeof(int4);
 }
 
 cudaError_t launch_cache_fwd(const Cache& cache, const CacheFwdCall& c, int sms,
@@ -753,6 +753,7 @@ cudaError_t launch_cache_fwd(const Cache& cache, const CacheFwdCall& c, int sms,
   p.row_tiles = (p.rows + unit_rows - 1) / unit_rows;
   p.part_o = static_cast<float*>(c.workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + 2 * ctas * unit_rows * cache.d);
+  p.joins = reinterpret_cast<int4*>(p.part_ml + 2 * ctas * unit_rows);
   if (many_rows(p.rows, cache.d)) return launch_cache_prefill(cache, p, sms, stream);
   const int nt = static_cast<int>(unit_rows / 8);
   switch (cache.d * 16 + nt) {

@@ -243,14 +243,16 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
     fence_barrier_init();
   }
   bool bad = false;
-  long long lo = 0, hi = 0;
+  long long lo = 0, hi = 0, share = 0;
   find_place<L::kRows, 128, L::kOver, kThreads>(p, red, found, &bad, [&](long long count) {
-    const long long total = count * p.Hkv, share = (total + p.ctas - 1) / p.ctas;
+    const long long total = count * p.Hkv;
+    share = (total + p.ctas - 1) / p.ctas;
     lo = blockIdx.x * share;
     hi = min(total, lo + share);
     return lo < hi ? lo / p.Hkv : -1ll;
   });
   if (bad && blockIdx.x == 0) atomicOr(p.seq.err, kErrCache);
+  if (threadIdx.x == 0) p.joins[blockIdx.x] = make_int4(0, 0, -1, 0);
   if (lo >= hi) return;
   if (warp == 12) {
     tmem_alloc(smem_u32(tmem_holder), L::kTmemCols);
@@ -299,6 +301,11 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
             w->len = at.seq.len;
             w->n = at.seq.n;
             w->whole = at.s0 == 0 && s1 == at.steps;
+            // the unit begins here and goes on behind this share, which ends
+            // where the piece does: its last place, and whose that is
+            if (at.s0 == 0 && s1 < at.steps)
+              p.joins[blockIdx.x] =
+                  make_int4(at.e, at.h, static_cast<int>((hi - 1 + at.steps - s1) / share), at.seq.n);
           }
         }
         __syncwarp();
@@ -596,11 +603,28 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
       // ---- q, once the last scores of the piece before are done.  A row is
       // scaled by a power of two to [2^7, 2^8) and becomes e4m3 parts, each
       // what the ones before have left.
-      // A thread does kSeg columns of a row, 16 at a time, in a loop small
-      // enough to stay in the instruction cache; the row is read twice (for its
-      // largest element, then from L1 or L2 for its parts).
-      constexpr int kSeg = L::kKCols, kSegs = D / kSeg, kThreadsQ = 32 * L::kConvWarps;
-      const int live = piece(np)->n;
+      // Four lanes to a row, each 16 of a part's 64 columns, so that eight
+      // lanes' load touches two lines (with a thread a row it touched eight, and
+      // the look-ups of those were most of a piece's start).  A warp does eight
+      // rows at a time, the next eight's loads in flight, and converts them in a
+      // loop small enough to stay in the instruction cache (the registers move
+      // on instead of an index).
+      // Odd rows take the parts of a pair the other way round: the codes of two
+      // rows then lie in banks of their own.
+      const int live = piece(np)->n, row0 = piece(np)->row0;
+      const int flip = L::kChunks > 1 ? r8 & 1 : 0;
+      uint4 ahead[2 * L::kChunks];        // [64-column part][half]
+      auto load_q = [&](int n) {
+        const int r = row0 + n + r8, i = r / p.seq.G;
+        const bool on = r < p.rows && i < live;
+        const uint16_t* src = p.q + b * p.qs.b + (h * p.seq.G + r - i * p.seq.G) * p.qs.h + i * p.qs.n + 16 * c16;
+        #pragma unroll
+        for (int c = 0; c < L::kChunks; ++c)
+          #pragma unroll
+          for (int k = 0; k < 2; ++k)
+            load_16_if(ahead[2 * c + k], src + 64 * (c ^ flip) + 8 * k, on);
+      };
+      load_q(8 * cw);
       if (np > 0 && !wait_uniform(bar(L::kQEmpty), (np - 1) & 1, abort)) break;
       // The next piece's flag: no converting warp is there before this one has
       // announced this piece's q.  A softmax group whose row tile has no keys in
@@ -608,53 +632,39 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
       // np - 3: eight flags.
       if (cw == 0 && lane == 0) nan_seen[(np + 1) & 7] = 0;
       #pragma unroll 1
-      for (int n = 32 * cw + lane; n < L::kRows * kSegs; n += kThreadsQ) {
-        const int rr = n / kSegs, seg = n % kSegs, r = piece(np)->row0 + rr, i = r / p.seq.G;
-        const bool on = r < p.rows && i < live;
-        const uint16_t* src = p.q + b * p.qs.b + (h * p.seq.G + r - i * p.seq.G) * p.qs.h + i * p.qs.n + kSeg * seg;
-        uint32_t top = 0;      // of the magnitudes, two lanes of 16 bits
+      for (int n = 8 * cw; n < L::kRows; n += 8 * L::kConvWarps) {
+        uint4 x[2 * L::kChunks];
         #pragma unroll
-        for (int c = 0; c < kSeg; c += 64) {
-          uint4 x[8];
-          #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            x[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (on) x[k] = *reinterpret_cast<const uint4*>(src + c + 8 * k);
-          }
-          #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            top = max_16x2(top, max_16x2(max_16x2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu),
-                                         max_16x2(x[k].z & 0x7fff7fffu, x[k].w & 0x7fff7fffu)));
-        }
-        if constexpr (kSegs == 2) top = max_16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        for (int k = 0; k < 2 * L::kChunks; ++k) x[k] = ahead[k];
+        if (n + 8 * L::kConvWarps < L::kRows) load_q(n + 8 * L::kConvWarps);
+        uint32_t top = 0;    // of the magnitudes, two lanes of 16 bits
+        #pragma unroll
+        for (int k = 0; k < 2 * L::kChunks; ++k)
+          top = max_16x2(top, max_16x2(max_16x2(x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu),
+                                       max_16x2(x[k].z & 0x7fff7fffu, x[k].w & 0x7fff7fffu)));
+        top = max_16x2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max_16x2(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const uint32_t top1 = max(top & 0xffffu, top >> 16);
         float up, down;
         const float amax = p.bf16 ? __uint_as_float(top1 << 16) : unpack2<false>(top1).x;
         row_power(amax, &up, &down);
         // (infinities have no code: their row is NaN, as its scores are)
         down = amax < __uint_as_float(0x7f800000u) ? down * 128.f : __uint_as_float(0x7fffffffu);
-        if (seg == 0) q_pow[(np & 1) * L::kRows + rr] = up * 0.0078125f;
-        const uint32_t to = sbase + L::kQOff + (rr >> 7) * L::kQTile + seg * (128 * kSeg);
-        uint4 ahead[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-        if (on) {
-          ahead[0] = *reinterpret_cast<const uint4*>(src);
-          ahead[1] = *reinterpret_cast<const uint4*>(src + 8);
-        }
+        const int rr = n + r8;
+        if (c16 == 0) q_pow[(np & 1) * L::kRows + rr] = up * 0.0078125f;
         #pragma unroll 1
-        for (int c = 0; c < kSeg / 16; ++c) {
-          const uint32_t y[8] = {ahead[0].x, ahead[0].y, ahead[0].z, ahead[0].w,
-                                 ahead[1].x, ahead[1].y, ahead[1].z, ahead[1].w};
-          if (on && c + 1 < kSeg / 16) {
-            ahead[0] = *reinterpret_cast<const uint4*>(src + 16 * c + 16);
-            ahead[1] = *reinterpret_cast<const uint4*>(src + 16 * c + 24);
-          }
+        for (int t = 0; t < L::kChunks; ++t) {
+          const uint32_t y[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
           uint32_t f[8];      // (below 256 every f16 and bf16 is an f16 to 2^-25)
           #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const float2 t = p.bf16 ? unpack2<true>(y[k]) : unpack2<false>(y[k]);
-            f[k] = pack2<false>(t.x * down, t.y * down);
+            const float2 v = p.bf16 ? unpack2<true>(y[k]) : unpack2<false>(y[k]);
+            f[k] = pack2<false>(v.x * down, v.y * down);
           }
-          const uint32_t at = to + row_chunk<kSeg>(rr & 127, c);
+          const int chunk = 4 * (t ^ flip) + c16;     // 16 columns of the row
+          constexpr int kRowChunks = L::kKCols / 16;
+          const uint32_t at = sbase + L::kQOff + (rr >> 7) * L::kQTile + chunk / kRowChunks * (128 * L::kKCols) +
+                              row_chunk<L::kKCols>(rr & 127, chunk % kRowChunks);
           #pragma unroll
           for (int q = 0; q < 3; ++q) {
             if (q == 2 && p.bf16) break;
@@ -664,6 +674,8 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
               w[k] = __byte_perm(take_e4m3(f[2 * k]), take_e4m3(f[2 * k + 1]), 0x5410);
             st_shared_v4(at + q * L::kQPart, w[0], w[1], w[2], w[3]);
           }
+          #pragma unroll
+          for (int k = 0; k + 2 < 2 * L::kChunks; ++k) x[k] = x[k + 2];
         }
       }
       fence_proxy_async_smem();
@@ -830,15 +842,15 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
         // the same rows, and its completion tells of that as well
         if (any && j > s0) {
           tc_fence_after();
-          #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tO + 32 * c, o);
+          #pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t o[16];
+            tmem_ld16(tO + 16 * c, o);
             tmem_ld_wait();
             reg_fence(o);
             #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st32(tO + 32 * c, o);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st16(tO + 16 * c, o);
           }
           tmem_st_wait();
         }
@@ -965,7 +977,7 @@ cudaError_t launch_seg(const Cache& cache, FwdCacheParams& p, int sms, cudaStrea
   p.ctas = sms;
   kern<<<p.ctas, kThreads, Pre<D>::kAlloc, stream>>>(tk, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_cache_merge<D, Pre<D>::kRows, 128, Pre<D>::kOver>(p, stream);
+  return launch_cache_merge<D, Pre<D>::kRows, 128, Pre<D>::kOver, true>(p, stream);
 }
 
 template <int D>

@@ -162,7 +162,7 @@ struct CacheFwdCall {
   void* workspace;
   unsigned int* err;
 };
-size_t cache_fwd_workspace_bytes(int B, int H, int Hkv, int Nq, int d, int sms);
+size_t cache_fwd_workspace_bytes(int H, int Hkv, int Nq, int d, int sms);
 cudaError_t launch_cache_fwd(const Cache& cache, const CacheFwdCall& c, int sms,
                              cudaStream_t stream);
 

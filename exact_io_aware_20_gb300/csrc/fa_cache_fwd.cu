@@ -27,6 +27,11 @@
 // With S^T = K Q^T and O^T = V^T P^T the cache is the A operand (16 keys or 16
 // columns a fragment), so 8 query rows fill an MMA: a step of mma.sync
 // m16n8k16 costs nothing that shows beside the loads.
+//
+// Measured (32 heads on 8, d = 128, one token a sequence): four sequences of up
+// to 131072 tokens 122 us, 5.9 TB/s (89% of what a copy reaches); eight of 8192
+// 33.5 us, 4.0 TB/s: a call's ends (the lengths, the first copies, the join) are
+// a third of that, 10 us with one sequence of 1000.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -39,7 +44,9 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;
-constexpr int kOver = 3;            // a unit's cost besides its steps, in steps
+// A unit's cost besides its steps, in steps (0 / 1 / 2 / 3: a step of 32
+// sequences with 4096 tokens takes 64 / 52.5 / 49 / 46 us).
+constexpr int kOver = 3;
 
 template <int D>
 struct Tile {

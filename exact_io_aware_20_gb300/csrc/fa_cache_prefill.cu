@@ -2,30 +2,49 @@
 // and whole ones): the same formulas as fa_cache_fwd.cu on the tensor cores of
 // tcgen05, tiles of 128 query rows x 128 keys.
 //
-// What bounds it: the tensor pipe and, next to it, the exponentials, as in the
-// 16-bit forward kernel; on top of those every 8-bit key and value has to
-// become f16 in the layout the products read.  A warpgroup of its own does
-// that: it reads the codes from memory (pages may lie anywhere, so each thread
-// follows the table for its rows; the next piece's loads are in flight while a
-// piece is converted), widens them (64 conversions a clock an SM, a quarter of
-// a tile's time) and writes them to swizzled shared memory.  A piece converted
-// once serves two tiles of query rows at d <= 128 (256 rows; every head of a
-// key/value head's group is among them), so the conversion is half of what one
-// tile would cost; at d = 256 TMEM holds one tile's O.
+// Scores.  The keys' codes are the products' operand as they are: TMA copies
+// them from the pages into the swizzled layout, and q becomes e4m3 parts
+// q 2^e = q1 + q2 (+ q3), each what the ones before have left: a part takes
+// four significant bits, so two hold a bf16 (8 bits) and three an f16 (11), and
+// S is their sum in fp32.  8-bit products run at twice the rate of 16-bit
+// ones, so two parts cost what one f16 product of widened keys would, and no
+// key passes through a register (the change from keys widened to f16 as
+// well took a chunk from 325 to 282 us).
+//
+// Values are widened to f16 (exact) by warps of their own, which follow the
+// page table row by row and write swizzled shared memory, the next tile's loads
+// in flight: 64 conversions a clock an SM, an eighth of a tile's time at
+// d <= 128, where one conversion serves two tiles of query rows (256 rows,
+// every head of a key/value head's group among them).  At d = 256 TMEM holds
+// one tile's O.
 //
 // The keys' scale multiplies the scores and the values' scale goes into the
-// exponent, both by 16-key groups (a page has at least 16): the group's
-// largest raw score is scaled, not each score, so that the scales cost eight
-// multiplications a row and tile, and the exponent's multiply-add takes them
-// for the rest.
+// exponent, both by groups of keys that a page holds for certain (64, 32 or 16
+// by the page size): the group's largest raw score is scaled, not each score,
+// and the exponent's multiply-add takes the scales for the rest (the chunk
+// below with pages of 64 takes 176 us, with pages of 16 211).
 //
 // Roles: warps 0-3 softmax of tile A, 4-7 of tile B (d = 256: conversion),
 // 8-11 conversion and q, 12 issues the products, 13 walks the share and
 // describes its pieces to the others, 14 finds the pages and scales of the
-// tiles to come.  512 threads start with 128 registers
-// each, which the groups then share out by their need.  With 192 KB of tiles
+// tiles to come, 15 copies the keys.  512 threads start with 128 registers
+// each, which the groups then share out by their need.  With 210 KB of tiles
 // next to none of the SM's storage is left as L1, so a register that spills
-// costs a trip to L2: the walk lives in one warp for that reason.
+// costs a trip to L2, and what is in nobody's loop is fetched anew each time:
+// the walk lives in one warp, and a piece's start and end are small loops (O
+// rescaled by 16 columns in a loop instead of by 32 unrolled: pages of 16, 240
+// -> 222 us; eight lanes' results brought together by shuffles so that they
+// fill lines, in more code: d = 256 308 -> 315 us, not kept).
+//
+// Measured (2 chunks of 512 tokens against up to 16384, 32 heads on 8, d = 128,
+// bf16): 176 us, 1240 TFLOP/s; d = 256, f16, four causal prompts of 4096
+// tokens, 8 heads: 297 us, 925 TFLOP/s.  What bounds it: at d <= 128 a tile pair
+// takes about 3000 clocks for 2048 of products, the softmax of each row tile
+// (400 for the maximum, 950 for the weights) and the products of the other by
+// turns; at d = 256 about 3800 for 2560, where one softmax group has nothing to
+// take turns with, and a piece's start and end, when O is read out and the
+// next q is taken apart (copies for timing without q, without the
+// results and without the join: 19, 18 and 17 us less of then 302).
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -41,7 +60,10 @@ template <int D>
 struct Pre {
   static constexpr int kTiles = D == 256 ? 1 : 2;
   static constexpr int kRows = 128 * kTiles;        // of a unit
-  static constexpr int kOver = kTiles == 1 ? 5 : 8;    // a unit's cost besides its steps, in steps
+  // A unit's cost besides its steps, in steps.  d = 256, causal prompts of 4096:
+  // 3 / 4 / 5 / 7 take 317 / 305 / 297 / 316 us; prompts of 2048 at d = 128,
+  // 4 / 6 / 8 / 11: 120.5 / 116.8 / 116.4 / 117.6, at d = 64 94.1 / 94.0 / 96.7 / 96.6.
+  static constexpr int kOver = kTiles == 1 ? 5 : 6;
   static constexpr int kSoftWarps = 4 * kTiles;
   static constexpr int kConvWarps = 12 - kSoftWarps;
   static constexpr int kConvRows = 128 / kConvWarps;   // keys of a tile that a warp converts

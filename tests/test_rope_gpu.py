@@ -52,7 +52,7 @@ def test_matches_the_rotation(dtype, B, H, Hkv, N, d, interleaved, part, axes):
 
 def test_far_positions_keep_their_angle():
     """At 2^31 - 1 an fp32 product of position and frequency is off by whole turns."""
-    freq = freqs(32) + [0.0] * 0
+    freq = freqs(32)
     table = binding.Rope(freq)
     q = torch.randn(1, 2, 4, 64, generator=torch.Generator().manual_seed(1)).half()
     pos = torch.tensor([[2 ** 31 - 1, -2 ** 31, 2 ** 30 + 1, 0]], dtype=torch.int32)

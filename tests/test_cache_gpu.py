@@ -270,6 +270,16 @@ def test_many_units_for_every_cta(d, page, B, Hkv, Nq, L):
             assert float((lse[b].double() - want_l)[some].abs().max()) < 1e-3
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d,page,H,Nq,lens,news", [
+    (64, 16, 3, 67, [20011], [67]), (128, 64, 3, 67, [20011, 150], [67, 60]),
+    (256, 32, 3, 67, [9001], [66]), (128, 16, 7, 19, [1290, 1100], [19, 2])])
+def test_a_unit_in_many_shares(d, page, H, Nq, lens, news, causal):
+    """Many rows of few units: a unit's pieces are those of up to all CTAs, and
+    its rows, odd in number, are joined four at a time."""
+    run_attention("bf16", d, page, H, 1, Nq, lens, news, causal=causal)
+
+
 @pytest.mark.parametrize("d,B,Nq", [(64, 700, 1), (128, 300, 2), (256, 1100, 1), (64, 600, 70),
                                     (128, 1100, 40)])
 def test_more_sequences_than_a_block_has_threads(d, B, Nq):

@@ -166,15 +166,54 @@ struct __align__(16) Where {
   int page, row;
 };
 
-// D[tmem] (+)= A[smem] * B[smem], both e4m3 (32 columns a product).
-__device__ __forceinline__ void mma_ss_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+// D[tmem] (+)= A[smem] * B[smem], both e4m3: kSteps products of 32 columns, one
+// after another along a row of both.  One election and one predicate for all of
+// them: the warp that issues is what the tensor pipe waits for.
+template <int kSteps>
+__device__ __forceinline__ void mma_rows_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  static_assert(kSteps == 2 || kSteps == 4, "columns of a row");
+  if constexpr (kSteps == 2)
+    asm volatile(
+        "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a, b;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+        "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a, b;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+        "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t"
+        "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, t;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem], f16: four products of 16 keys (8 columns of A,
+// 2048 bytes of B each).
+__device__ __forceinline__ void mma_64_keys(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                             uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
+      "{\n\t.reg .pred p, e, t;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.s32 a, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.s32 a, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // Instruction descriptor of kind::f8f6f4: fp32 sums, both operands e4m3 (type
@@ -209,6 +248,23 @@ __device__ __forceinline__ uint32_t take_e4m3(uint32_t& x) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(two));
   asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(back));
   return two;
+}
+
+// This thread's row of O in TMEM times alpha.
+template <int D>
+__device__ __forceinline__ void scale_o(uint32_t tO, float alpha) {
+  tc_fence_after();
+  #pragma unroll 1
+  for (int c = 0; c < D / 16; ++c) {
+    uint32_t o[16];
+    tmem_ld16(tO + 16 * c, o);
+    tmem_ld_wait();
+    reg_fence(o);
+    #pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+    tmem_st16(tO + 16 * c, o);
+  }
+  tmem_st_wait();
 }
 
 // SEG: keys that share their scales for certain (a page's, 64 at most).
@@ -436,18 +492,13 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
       // K piece in place s
       auto scores = [&](int u, int buf, int c, int s) {
         uint64_t qs = desc_add(q_desc, u * L::kQTile + c * (128 * L::kKCols));
+        const uint64_t ks = desc_add(k_desc, s * L::kKPiece);
         uint32_t more = c > 0;
         #pragma unroll 1
         for (int q = 0; q < q_parts; ++q) {
-          uint64_t ks = desc_add(k_desc, s * L::kKPiece);
-          #pragma unroll 4
-          for (int w = 0; w < L::kKCols / 32; ++w) {
-            mma_ss_e4m3(tmem + L::kTS + 128 * buf, qs, ks, kIdS, more);
-            qs = desc_add(qs, 32);
-            ks = desc_add(ks, 32);
-            more = 1;
-          }
-          qs = desc_add(qs, L::kQPart - L::kKCols);
+          mma_rows_e4m3<L::kKCols / 32>(tmem + L::kTS + 128 * buf, qs, ks, kIdS, more);
+          qs = desc_add(qs, L::kQPart);
+          more = 1;
         }
       };
       // O (+)= part h of P V of row tile u, P from score buffer `buf`, from the
@@ -456,11 +507,11 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
         uint64_t vs = desc_add(v_desc, s * L::kVPiece);
         uint32_t from = tmem + L::kTS + 128 * buf + h * (L::kVKeys / 2);
         uint32_t more = !fresh || h > 0;
-        #pragma unroll 4
-        for (int w = 0; w < L::kVKeys / 16; ++w) {
-          mma_ts(tmem + L::kTO + D * u, from, vs, kIdO, more);
-          vs = desc_add(vs, 2048);
-          from += 8;
+        #pragma unroll
+        for (int w = 0; w < L::kVKeys / 64; ++w) {
+          mma_64_keys(tmem + L::kTO + D * u, from, vs, kIdO, more);
+          vs = desc_add(vs, 64 * 128);
+          from += 32;
           more = 1;
         }
       };
@@ -827,7 +878,14 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
           m = now;
           l *= alpha;
         }
-        // the weights over S as f16, 32 columns at a time
+        // O follows the maximum.  d <= 128: S of this tile was issued after P V of
+        // the tile before on the same rows, and its completion tells of that as
+        // well.  With scales by 16 keys ahead of the weights, which leaves more
+        // registers to them (d = 128, pages of 16: 209.5 -> 197 us), otherwise
+        // behind them (pages of 64: 176.5, ahead 178.7).
+        constexpr bool kScaleFirst = L::kTiles == 2 && SEG == 16;
+        if (kScaleFirst && any && j > s0) scale_o<D>(tO, alpha);
+        // the weights over S as f16
         #pragma unroll
         for (int seg = 0; seg < 128 / SEG; ++seg) {
           const float4 sc = ld_shared_f4(mt + 16 * (SEG / 16) * seg);
@@ -860,22 +918,7 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
             tc_fence_after();
           }
         }
-        // d <= 128: S of this tile was issued after P V of the tile before on
-        // the same rows, and its completion tells of that as well
-        if (any && j > s0) {
-          tc_fence_after();
-          #pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t o[16];
-            tmem_ld16(tO + 16 * c, o);
-            tmem_ld_wait();
-            reg_fence(o);
-            #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st16(tO + 16 * c, o);
-          }
-          tmem_st_wait();
-        }
+        if (!kScaleFirst && any && j > s0) scale_o<D>(tO, alpha);
         tc_fence_before();
         mbar_arrive_warp(bar(L::kPFull + buf));
       }

@@ -22,7 +22,7 @@
 // exponent, both by groups of keys that a page holds for certain (64, 32 or 16
 // by the page size): the group's largest raw score is scaled, not each score,
 // and the exponent's multiply-add takes the scales for the rest (the chunk
-// below with pages of 64 takes 176 us, with pages of 16 211).
+// below with pages of 64 takes 172 us, with pages of 16 193).
 //
 // Roles: warps 0-3 softmax of tile A, 4-7 of tile B (d = 256: conversion),
 // 8-11 conversion and q, 12 issues the products, 13 walks the share and
@@ -37,9 +37,9 @@
 // fill lines, in more code: d = 256 308 -> 315 us, not kept).
 //
 // Measured (2 chunks of 512 tokens against up to 16384, 32 heads on 8, d = 128,
-// bf16): 176 us, 1240 TFLOP/s; d = 256, f16, four causal prompts of 4096
-// tokens, 8 heads: 297 us, 925 TFLOP/s.  What bounds it: at d <= 128 a tile pair
-// takes about 3000 clocks for 2048 of products, the softmax of each row tile
+// bf16): 172 us, 1270 TFLOP/s; d = 256, f16, four causal prompts of 4096
+// tokens, 8 heads: 296 us, 930 TFLOP/s.  What bounds it: at d <= 128 a tile pair
+// takes about 2900 clocks for 2048 of products, the softmax of each row tile
 // (400 for the maximum, 950 for the weights) and the products of the other by
 // turns; at d = 256 about 3800 for 2560, where one softmax group has nothing to
 // take turns with, and a piece's start and end, when O is read out and the

@@ -889,7 +889,8 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
         #pragma unroll
         for (int seg = 0; seg < 128 / SEG; ++seg) {
           const float4 sc = ld_shared_f4(mt + 16 * (SEG / 16) * seg);
-          const float ksr = row_scale * sc.x, sub = sc.y - m;
+          // (a product that underflows to 0 would make a masked score, -inf, NaN)
+          const float ksr = fmaxf(row_scale * sc.x, 1.17549435e-38f), sub = sc.y - m;
           const f2 k2 = {ksr, ksr}, m2 = {sub, sub};
           f2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
           #pragma unroll

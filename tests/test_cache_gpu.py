@@ -362,6 +362,22 @@ def test_queries_far_from_one(size):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("d,Nq", [(64, 1), (64, 90), (128, 3), (128, 90), (256, 1), (256, 90)])
+def test_scales_whose_product_underflows(d, Nq):
+    """Queries of 2^-100 on pages of 2^-60: every score is zero to fp32, and
+    what is masked weighs nothing all the same."""
+    g = torch.Generator().manual_seed(d + Nq)
+    lens = [300, 131]
+    codes, scales, table = ref.make_cache(30, 1, 32, d, 2, 12, g, lens)
+    scales[0] = torch.full_like(scales[0], 2.0 ** -60)
+    cache = device_cache(codes, scales, table)
+    q = (torch.randn(2, 2, Nq, d, generator=g) * 2.0 ** -100).bfloat16()
+    o, lse = binding.forward_cache(dev(q), cache, ints(lens), True, 0.1)
+    binding.device_status()
+    check_attention(o, lse, q, ref.Paged(codes[0], scales[0]), ref.Paged(codes[1], scales[1]), table,
+                    lens, [Nq, Nq], True, 0.1)
+
+
 def test_a_long_cache_and_byte_offsets_past_32_bits():
     """300,000 tokens of one sequence, at the far end of a pool of more than
     2^32 bytes; sampled against equal codes: the softmax of equal scores."""

@@ -466,6 +466,37 @@ def test_ranges_out_of_bounds_are_reported():
     binding.device_status()
 
 
+@pytest.mark.parametrize("d,page", [(64, 32), (128, 16), (256, 64)])
+def test_ranges_out_of_bounds_with_many_rows(d, page):
+    """The same for chunks of prompts: the bad sequence is reported, the others
+    are served as they are without it."""
+    g = torch.Generator().manual_seed(d)
+    lens = [200, 333, 150]
+    width = -(-333 // page)
+    codes, scales, table = ref.make_cache(3 * width + 1, 2, page, d, 3, width, g, lens)
+    q = torch.randn(3, 4, 100, d, generator=g).bfloat16().to(DEV)
+    want = binding.forward_cache(q, device_cache(codes, scales, table), ints(lens), True, 0.1)
+    binding.device_status()
+    for bad_len, bad_page in ((width * page + 1, None), (-5, None), (333, 3 * width + 1), (333, -1)):
+        bad = table.clone()
+        if bad_page is not None:
+            bad[1, 2] = bad_page
+        o, lse = binding.forward_cache(q, device_cache(codes, scales, bad), ints([200, bad_len, 150]),
+                                       True, 0.1)
+        with pytest.raises(binding.FaError) as e:
+            binding.device_status()
+        assert e.value.status == binding.FA_ERR_CACHE
+        # (cut into other shares, so joined from other pieces: both results are
+        # within 2^-8, half a step of bf16, and 2^-11 of the weights' rounding of
+        # the value, times the largest of the row's)
+        for b in (0, 2):
+            assert float((o[b].float() - want[0][b].float()).abs().max()) <= 2 * (2.0 ** -8 + 2.0 ** -11) * float(want[0][b].abs().max())
+            assert float((lse[b] - want[1][b]).abs().max()) <= 1e-4
+        if bad_page is None:
+            assert (o[1] == 0).all() and torch.isneginf(lse[1]).all()
+    binding.device_status()
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("d,page,H,Hkv", [(64, 16, 4, 2), (128, 64, 8, 2), (256, 32, 2, 1)])
 def test_a_server_s_run(d, page, H, Hkv):

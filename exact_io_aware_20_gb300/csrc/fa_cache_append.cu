@@ -433,9 +433,13 @@ cudaError_t launch_cache_append(const Cache& cache, const AppendCall& c, const R
   while ((1 << p.page_log2) < cache.page) ++p.page_log2;
   p.span = (c.N - 1 + cache.page - 1) / cache.page + 1;
   p.q_items = static_cast<long long>(c.B) * c.N * p.slots;
+  // q's heads of a thread: fewer threads than the rotary kernel's, beside the
+  // units' (256 / 512 / 1024 an SM: 6 x 333 padded tokens of 16 + 2 x 16 heads on
+  // three axes 9.6 / 10.5 / 12.8 us, 512 tokens of 32 + 2 x 8 heads 8.4 / 9.3 /
+  // 10.1, long prompts the same).
   const long long groups =
-      std::max(1ll, std::min<long long>(std::max(c.H, 1), 2048ll * 152 / p.q_items));
-  p.q_heads_per = (std::max(c.H, 1) + groups - 1) / groups;
+      std::max(1ll, std::min<long long>(std::max(c.H, 1), 256ll * 152 / p.q_items));
+  p.q_heads_per = std::min<long long>(16, (std::max(c.H, 1) + groups - 1) / groups);
   p.seq_lens = c.seq_lens;
   p.new_lens = c.new_lens;
   p.err = c.err;

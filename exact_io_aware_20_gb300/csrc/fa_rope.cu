@@ -2,11 +2,12 @@
 // round the backward pass.
 //
 // What bounds it: memory, 2 bytes read and 2 written an element (2 x 8192
-// tokens of 40 heads, d = 128: 57 us, 5.9 TB/s, 89% of what a copy reaches; five
-// tokens of four sequences 2.6 us).  A thread
-// keeps the cos and sin of one slot (8 pairs) of one token and walks over
-// heads, so the angles, which every head shares, are worked out once for up
-// to H + Hkv heads; a warp covers whole 128-byte lines of consecutive tokens.
+// tokens of 40 heads, d = 128: 55 us, 6.1 TB/s, 91% of what a copy reaches; the
+// backward pass over three axes of 4099 tokens of 32 heads, d = 64, 8.2 us; five
+// tokens of four sequences 2.5 us).  A thread keeps the cos and sin of one slot
+// (8 pairs) of one token and walks over heads, so the angles, which every head
+// shares, are worked out once for up to 16 of them; a warp covers whole
+// 128-byte lines of consecutive tokens.
 #include <algorithm>
 
 #include "rope.cuh"
@@ -42,7 +43,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
                       p.k_out + b * p.kos.b + n * p.kos.n,
                       p.qs.h, p.ks.h, p.qos.h, p.kos.h, p.H};
   const int h0 = blockIdx.y * p.heads_per;
-  rope_heads<BF16, 4>(p.r, w, slot, h0, min(p.heads, h0 + p.heads_per), pos, true);
+  rope_heads<BF16, 2>(p.r, w, slot, h0, min(p.heads, h0 + p.heads_per), pos, true);
 }
 
 }  // namespace
@@ -63,13 +64,17 @@ cudaError_t launch_rope(const RopeCall& c, const RopeArgs& r, cudaStream_t strea
   p.slots = c.d / 16;
   p.items = static_cast<long long>(c.B) * c.N * p.slots;
   p.r = r;
-  // Heads of a thread: as many as leave about 2048 threads for each SM, so
-  // that a long call works its angles out once and a short one is spread over
-  // the chip.
-  const long long want = 2048ll * 152;
+  // Heads of a thread: as many as leave about 1024 threads for each SM, so that
+  // a long call works its angles out once and a short one is spread over the
+  // chip; 16 at most, so that a long call's blocks fill more than one wave of
+  // them.  Threads an SM 512 / 1024 / 1536 / 2048: the backward pass below 8.2 /
+  // 8.3 / 9.4 / 10.1 us, 512 tokens of 32 + 8 heads 5.0 / 5.8 / 7.9 / 7.9, 4096 of
+  // them 19.6 / 17.1 / 17.9 / 18.8; 2 x 8192 of them with 6 / 10 / 20 / 40 heads a
+  // thread 56.2 / 55.2 / 54.9 / 60.8.
+  const long long want = 1024ll * 152;
   const long long groups =
       std::max(1ll, std::min(std::min<long long>(p.heads, 4096), want / p.items));
-  p.heads_per = static_cast<int>((p.heads + groups - 1) / groups);
+  p.heads_per = std::min(16, static_cast<int>((p.heads + groups - 1) / groups));
   const long long blocks = (p.items + kRopeThreads - 1) / kRopeThreads;
   const dim3 grid(static_cast<unsigned>(blocks),
                   static_cast<unsigned>((p.heads + p.heads_per - 1) / p.heads_per), 1);

@@ -136,7 +136,8 @@ __device__ __forceinline__ void turn_slot(uint4& a, uint4& b, const float (&c)[8
 
 // Rotates (or, without a rotation, copies) one slot of heads [h0, h1) of one
 // token: heads below H are q's, the others k's.  Loads of kAhead heads are in
-// flight together.  `live` false: zeros are written instead.
+// flight together, the first ahead of the angles and each next one as soon as
+// its registers are stored.  `live` false: zeros are written instead.
 struct RopeRows {
   const uint16_t *q, *k;         // of this token's sequence and row (head 0, column 0)
   uint16_t *q_out, *k_out;
@@ -147,19 +148,20 @@ template <bool BF16, int kAhead>
 __device__ __forceinline__ void rope_heads(const RopeArgs& r, const RopeRows& w, int slot, int h0,
                                            int h1, const int (&pos)[4], bool live) {
   const Slot at = slot_of(r, slot);
+  uint4 a[kAhead], b[kAhead];
+  auto load = [&](int u, int h) {
+    a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (h < h1 && live) {
+      const uint16_t* src = h < w.H ? w.q + h * w.q_h : w.k + (h - w.H) * w.k_h;
+      a[u] = *reinterpret_cast<const uint4*>(src + at.col_a);
+      b[u] = *reinterpret_cast<const uint4*>(src + at.col_b);
+    }
+  };
+  #pragma unroll
+  for (int u = 0; u < kAhead; ++u) load(u, h0 + u);
   float c[8], s[8];
   if (at.turns) slot_cos_sin(r, slot, pos, c, s);
   for (int h = h0; h < h1; h += kAhead) {
-    uint4 a[kAhead], b[kAhead];
-    #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      a[u] = b[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (h + u < h1 && live) {
-        const uint16_t* src = h + u < w.H ? w.q + (h + u) * w.q_h : w.k + (h + u - w.H) * w.k_h;
-        a[u] = *reinterpret_cast<const uint4*>(src + at.col_a);
-        b[u] = *reinterpret_cast<const uint4*>(src + at.col_b);
-      }
-    }
     #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (h + u < h1) {
@@ -171,6 +173,7 @@ __device__ __forceinline__ void rope_heads(const RopeArgs& r, const RopeRows& w,
         *reinterpret_cast<uint4*>(dst + at.col_a) = a[u];
         *reinterpret_cast<uint4*>(dst + at.col_b) = b[u];
       }
+      load(u, h + u + kAhead);
     }
   }
 }

@@ -67,7 +67,7 @@ cudaError_t launch_rope(const RopeCall& c, const RopeArgs& r, cudaStream_t strea
   // Heads of a thread: as many as leave about 1024 threads for each SM, so that
   // a long call works its angles out once and a short one is spread over the
   // chip; 16 at most, so that a long call's blocks fill more than one wave of
-  // them.  Threads an SM 512 / 1024 / 1536 / 2048: the backward pass below 8.2 /
+  // them.  Threads an SM 512 / 1024 / 1536 / 2048: the backward pass above 8.2 /
   // 8.3 / 9.4 / 10.1 us, 512 tokens of 32 + 8 heads 5.0 / 5.8 / 7.9 / 7.9, 4096 of
   // them 19.6 / 17.1 / 17.9 / 18.8; 2 x 8192 of them with 6 / 10 / 20 / 40 heads a
   // thread 56.2 / 55.2 / 54.9 / 60.8.

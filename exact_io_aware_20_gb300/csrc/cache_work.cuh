@@ -105,14 +105,17 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
 }
 
-// The power of two that a bf16 row with largest magnitude amax is divided by
-// to become f16 (1 for rows of zeros, NaN or infinities): `up` it, `down` its
-// reciprocal.
+// The power of two that brings a row with largest magnitude amax to
+// [2^TOP, 2^(TOP + 1)) (1 for rows of zeros, NaN or infinities): `down` it, `up`
+// its reciprocal.  Both are kept normal numbers, so that a row of the smallest
+// magnitudes ends lower, and with TOP = 0 one of the largest an octave higher;
+// its bits stay what they are.
+template <int TOP>
 __device__ __forceinline__ void row_power(float amax, float* up, float* down) {
-  const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23), 1), 253);
+  const int e = min(max(static_cast<int>(__float_as_uint(amax) >> 23), 1 + TOP), min(253 + TOP, 254));
   const bool plain = !(amax > 0.f) || !(amax < __uint_as_float(0x7f800000u));
-  *down = plain ? 1.f : __uint_as_float(static_cast<uint32_t>(254 - e) << 23);   // 2^(127 - e)
-  *up = plain ? 1.f : __uint_as_float(static_cast<uint32_t>(e) << 23);
+  *down = plain ? 1.f : __uint_as_float(static_cast<uint32_t>(254 + TOP - e) << 23);   // 2^(127 + TOP - e)
+  *up = plain ? 1.f : __uint_as_float(static_cast<uint32_t>(e - TOP) << 23);
 }
 
 template <int STEP>

@@ -297,7 +297,7 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         float up;
-        row_power(amax, &up, &down);
+        row_power<0>(amax, &up, &down);
         if (t == 0) q_pow[nt * 8 + g] = up;
       } else if (t == 0) {
         q_pow[nt * 8 + g] = 1.f;

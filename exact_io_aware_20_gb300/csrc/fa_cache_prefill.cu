@@ -720,11 +720,11 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
         const uint32_t top1 = max(top & 0xffffu, top >> 16);
         float up, down;
         const float amax = p.bf16 ? __uint_as_float(top1 << 16) : unpack2<false>(top1).x;
-        row_power(amax, &up, &down);
+        row_power<7>(amax, &up, &down);
         // (infinities have no code: their row is NaN, as its scores are)
-        down = amax < __uint_as_float(0x7f800000u) ? down * 128.f : __uint_as_float(0x7fffffffu);
+        if (!(amax < __uint_as_float(0x7f800000u))) down = __uint_as_float(0x7fffffffu);
         const int rr = n + r8;
-        if (c16 == 0) q_pow[(np & 1) * L::kRows + rr] = up * 0.0078125f;
+        if (c16 == 0) q_pow[(np & 1) * L::kRows + rr] = up;
         #pragma unroll 1
         for (int t = 0; t < L::kChunks; ++t) {
           const uint32_t y[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};

@@ -1,0 +1,94 @@
+"""How exact fa_fwd_cache is where it is hardest: query rows of tiny elements,
+rows with one column far above the rest, and many keys far below one.
+
+Bounds are those of the kernels' own roundings; here each kernel is held to
+its own: q is exact to 2^-25 of a row's largest element with few rows, and to
+2^-21 of it with many (where keys stay in 8 bits)."""
+import math
+
+import pytest
+import torch
+
+import cache_ref as ref
+from exact_io_aware_20_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+T = {"bf16": torch.bfloat16, "f16": torch.float16}
+FEW, MANY = 1, 90      # query rows of the two kernels at every head dim (one or two heads a key/value head)
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def q_error(x, dtype, many):
+    """What the operand that stands for a row x [d] of q may be off by, an
+    element.  Few rows: f16 with the largest in [1, 2): 2^-25 of it at most (f16
+    rows: nothing).  Many rows: the largest is brought to [2^7, 2^8) and parts
+    of 8 bits are taken off one after another, the last of them with two
+    mantissa bits and steps down to 2^-16.  What the parts before it leave is
+    within half of their step 2^-9, so that it is off by half a step of 2^-13
+    at most, 2^-14 or 2^-21 of the largest; and only where it has more than
+    three bits: elements below 2^-6 (bf16: 8 bits, 4 of them in the first part)
+    or 2^-3 (f16: 11 bits, 8 in the first two) of those with the largest at
+    2^7 at least, 2^-13 and 2^-10 of it."""
+    top = x.abs().max()
+    if not many:
+        return torch.full_like(x, float(top) * 2.0 ** -25) if dtype == "bf16" else torch.zeros_like(x)
+    small = x.abs() < top * (2.0 ** -13 if dtype == "bf16" else 2.0 ** -10)
+    return small.double() * top * 2.0 ** -21
+
+
+def check(o, lse, q, codes, scales, table, lens, causal, scale, dtype, many):
+    """Against 64 bits.  Scores: products summed in fp32 (2^-23 a step, in any
+    order) and q's own error; exp2, the scaling and the running sums 2^-20
+    together.  Weights: half a step of f16, 2^-11, or for small ones 2^-25 where
+    the largest stands at 2^7 or above: 2^-32 of it."""
+    k, v = (ref.Paged(codes[i], scales[i]) for i in (0, 1))
+    B, H, N, d = q.shape
+    Hkv = codes[0].shape[1]
+    x, o, lse = q.double(), o.cpu().double(), lse.cpu().double()
+    for b in range(B):
+        for h in range(H):
+            K, V = (c.rows(table[b], lens[b], h // (H // Hkv)) for c in (k, v))
+            for i in range(N):
+                see = lens[b] - N + i + 1 if causal else lens[b]
+                S = (K[:see] @ x[b, h, i]) * scale
+                L = torch.logsumexp(S, 0)
+                P = torch.exp(S - L)
+                want = P @ V[:see]
+                size = float((K[:see].abs() @ x[b, h, i].abs()).max()) * scale
+                off = float((K[:see].abs() @ q_error(x[b, h, i], dtype, many)).max()) * scale
+                ds = size * d * 2.0 ** -23 + off + 2.0 ** -20 * (1 + float(S.abs().max()))
+                slack = (P @ V[:see].abs()) * (2.0 ** -11 + 2 * ds + see * 2.0 ** -24) \
+                    + see * 2.0 ** -32 * 448 * float(v.scales.max())
+                bound = slack * 1.001 + ref.half_step(q.dtype) * (want.abs() + slack) + 2.0 ** -25
+                err = (o[b, h, i] - want).abs()
+                assert (err <= bound).all(), (b, h, i, float((err - bound).max()))
+                l_err = abs(float(lse[b, h, i] - L))
+                assert l_err <= ds + see * 2.0 ** -24 + 2.0 ** -21 * (1 + abs(float(L))), (b, h, i, l_err)
+
+
+def cache_of(codes, scales, table):
+    return binding.Cache(*(t.to(DEV) for t in (*codes, *scales, table)))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("Nq", [FEW, MANY])
+@pytest.mark.parametrize("size", [2.0 ** -120, 2.0 ** -122, 2.0 ** -126, 2.0 ** 125])
+def test_tiny_and_huge_queries(d, Nq, size):
+    """bf16 rows at both ends of the type, with zeros among their elements, and
+    a softmax scale that makes scores of ordinary size of them."""
+    g = torch.Generator().manual_seed(d + Nq)
+    lens = [300, 131]
+    codes, scales, table = ref.make_cache(30, 1, 32, d, 2, 12, g, lens)
+    q = torch.randn(2, 1, Nq, d, generator=g).clamp_(-5, 5)
+    q[..., ::5] = 0
+    if size > 1:
+        q[..., 3] = 255 / 32      # the largest bf16
+    q = (q.double() * size).bfloat16()
+    scale = float(torch.tensor((0.1 if size < 1 else 0.8) / size, dtype=torch.float32))     # (a normal number)
+    o, lse = binding.forward_cache(q.to(DEV), cache_of(codes, scales, table), ints(lens), True, scale)
+    binding.device_status()
+    check(o, lse, q, codes, scales, table, lens, True, scale, "bf16", Nq == MANY)

@@ -3,10 +3,16 @@
 // tcgen05, tiles of 128 query rows x 128 keys.
 //
 // Scores.  The keys' codes are the products' operand as they are: TMA copies
-// them from the pages into the swizzled layout, and q becomes e4m3 parts
-// q 2^e = q1 + q2 (+ q3), each what the ones before have left: a part takes
-// four significant bits, so two hold a bf16 (8 bits) and three an f16 (11), and
-// S is their sum in fp32.  8-bit products run at twice the rate of 16-bit
+// them from the pages into the swizzled layout, and q becomes 8-bit parts
+// q 2^e = q1 + q2 (+ q3), each what the ones before have left, the largest
+// element in [2^7, 2^8); S is their sum in fp32.  An e4m3 part takes four
+// significant bits, so two hold a bf16 (8 bits) and three an f16 (11).  The last
+// part is e5m2: what is left by then has at most three bits, which is all that
+// e5m2 holds, and its steps go down to 2^-16, where those of e4m3 end at 2^-9.
+// So q is exact but for elements below 2^-13 (f16: 2^-10) of the row's largest,
+// which are off by 2^-21 of it at most, less than the fp32 sums (with e4m3
+// throughout it was 2^-17 for those below 2^-6, which showed in rows with one
+// column far above the rest).  8-bit products run at twice the rate of 16-bit
 // ones, so two parts cost what one f16 product of widened keys would, and no
 // key passes through a register (the change from keys widened to f16 as
 // well took a chunk from 325 to 282 us).
@@ -68,7 +74,7 @@ struct Pre {
   static constexpr int kConvWarps = 12 - kSoftWarps;
   static constexpr int kConvRows = 128 / kConvWarps;   // keys of a tile that a warp converts
   static constexpr int kChunks = D / 64;            // 64-column parts
-  static constexpr int kQParts = 3;                 // e4m3 parts of q at most
+  static constexpr int kQParts = 3;                 // 8-bit parts of q at most
   static constexpr int kQPart = 128 * D;            // one part of a tile of rows
   static constexpr int kQTile = kQParts * kQPart;
   static constexpr int kKCols = D < 128 ? D : 128;  // K: 128 keys x kKCols codes
@@ -166,11 +172,11 @@ struct __align__(16) Where {
   int page, row;
 };
 
-// D[tmem] (+)= A[smem] * B[smem], both e4m3: kSteps products of 32 columns, one
+// D[tmem] (+)= A[smem] * B[smem], both 8 bits: kSteps products of 32 columns, one
 // after another along a row of both.  One election and one predicate for all of
 // them: the warp that issues is what the tensor pipe waits for.
 template <int kSteps>
-__device__ __forceinline__ void mma_rows_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+__device__ __forceinline__ void mma_rows_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                               uint32_t idesc, uint32_t accumulate) {
   static_assert(kSteps == 2 || kSteps == 4, "columns of a row");
   if constexpr (kSteps == 2)
@@ -216,10 +222,11 @@ __device__ __forceinline__ void mma_64_keys(uint32_t d_tmem, uint32_t a_tmem, ui
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Instruction descriptor of kind::f8f6f4: fp32 sums, both operands e4m3 (type
-// 0) and K-major.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
-  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+// Instruction descriptor of kind::f8f6f4: fp32 sums, both operands K-major, A e4m3
+// (type 0) or e5m2 (type 1), B e4m3.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, int a_e5m2) {
+  return (1u << 4) | (static_cast<uint32_t>(a_e5m2) << 7) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
 }
 // Shared-memory descriptor of K-major rows of COLS bytes (128: 128-byte
 // swizzle, 64: 64-byte swizzle), eight rows after eight.
@@ -247,6 +254,12 @@ __device__ __forceinline__ uint32_t take_e4m3(uint32_t& x) {
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(two) : "r"(x));
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(two));
   asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(x) : "r"(back));
+  return two;
+}
+// Two f16 -> two e5m2 codes (the low 16 bits).
+__device__ __forceinline__ uint32_t to_e5m2(uint32_t x) {
+  uint16_t two;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(two) : "r"(x));
   return two;
 }
 
@@ -476,7 +489,7 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
         drain_wait(bar(L::kKFull + i % L::kKStages), (i / L::kKStages) & 1);
     } else if (warp == 12) {
       // ---------------------------------------------------------- products
-      constexpr uint32_t kIdS = idesc_e4m3(128, 128);
+      constexpr uint32_t kIdS = idesc_f8(128, 128, 0), kIdLast = idesc_f8(128, 128, 1);
       constexpr uint32_t kIdO = idesc_f16(128, D, 0, 0, 1);
       const uint64_t q_desc = rows_desc<L::kKCols>(sbase + L::kQOff);
       const uint64_t k_desc = rows_desc<L::kKCols>(sbase + L::kKOff);
@@ -496,7 +509,7 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
         uint32_t more = c > 0;
         #pragma unroll 1
         for (int q = 0; q < q_parts; ++q) {
-          mma_rows_e4m3<L::kKCols / 32>(tmem + L::kTS + 128 * buf, qs, ks, kIdS, more);
+          mma_rows_f8<L::kKCols / 32>(tmem + L::kTS + 128 * buf, qs, ks, q + 1 < q_parts ? kIdS : kIdLast, more);
           qs = desc_add(qs, L::kQPart);
           more = 1;
         }
@@ -674,8 +687,8 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
     for (int np = 0; ok && more; ++np) {
       enter(np);
       // ---- q, once the last scores of the piece before are done.  A row is
-      // scaled by a power of two to [2^7, 2^8) and becomes e4m3 parts, each
-      // what the ones before have left.
+      // scaled by a power of two to [2^7, 2^8) and becomes 8-bit parts, each
+      // what the ones before have left, the last of them e5m2.
       // Four lanes to a row, each 16 of a part's 64 columns, so that eight
       // lanes' load touches two lines (with a thread a row it touched eight, and
       // the look-ups of those were most of a piece's start).  A warp does eight
@@ -738,14 +751,21 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
           constexpr int kRowChunks = L::kKCols / 16;
           const uint32_t at = sbase + L::kQOff + (rr >> 7) * L::kQTile + chunk / kRowChunks * (128 * L::kKCols) +
                               row_chunk<L::kKCols>(rr & 127, chunk % kRowChunks);
-          #pragma unroll
-          for (int q = 0; q < 3; ++q) {
-            if (q == 2 && p.bf16) break;
+          auto part = [&](uint32_t to, auto code) {
             uint32_t w[4];
             #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = __byte_perm(take_e4m3(f[2 * k]), take_e4m3(f[2 * k + 1]), 0x5410);
-            st_shared_v4(at + q * L::kQPart, w[0], w[1], w[2], w[3]);
+            for (int k = 0; k < 4; ++k) w[k] = __byte_perm(code(f[2 * k]), code(f[2 * k + 1]), 0x5410);
+            st_shared_v4(to, w[0], w[1], w[2], w[3]);
+          };
+          // (the first part in either branch, not ahead of them: that way a
+          // register spilled at d = 256)
+          if (p.bf16) {
+            part(at, take_e4m3);
+            part(at + L::kQPart, to_e5m2);
+          } else {
+            part(at, take_e4m3);
+            part(at + L::kQPart, take_e4m3);
+            part(at + 2 * L::kQPart, to_e5m2);
           }
           #pragma unroll
           for (int k = 0; k + 2 < 2 * L::kChunks; ++k) x[k] = x[k + 2];

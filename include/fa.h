@@ -384,6 +384,10 @@ int fa_cache_append(const fa_cache *cache, const void *q, const void *k, const v
  * What lies in masked places (rows of a page past the length, later tokens)
  * does not reach a row, whatever its value, NaN included.  The lengths are
  * read on the device, so a captured graph serves growing sequences.
+ * q is taken as it is, but for elements far below the largest of their row:
+ * with few rows bf16 elements below 2^-13 of it to 2^-25 of it, with many rows
+ * (where q is split into 8-bit parts) elements below 2^-13 (f16: 2^-10) of it
+ * to 2^-21 of it.
  * Scales must be positive and finite, between 2^-100 and 2^120.
  * Weights carry the value scale in fp32: with j the key of the largest weight
  * times value scale that a row sees, a key whose page's value scale is 2^-g of

@@ -92,3 +92,22 @@ def test_tiny_and_huge_queries(d, Nq, size):
     o, lse = binding.forward_cache(q.to(DEV), cache_of(codes, scales, table), ints(lens), True, scale)
     binding.device_status()
     check(o, lse, q, codes, scales, table, lens, True, scale, "bf16", Nq == MANY)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("Nq", [FEW, MANY])
+@pytest.mark.parametrize("column", [2.0 ** 7, 2.0 ** 10, 2.0 ** 13])
+def test_queries_with_one_column_far_above_the_rest(dtype, d, Nq, column):
+    """The large column meets keys of zero, so that the scores are the small
+    columns'."""
+    g = torch.Generator().manual_seed(d + Nq)
+    lens = [140, 131]
+    codes, scales, table = ref.make_cache(30, 1, 32, d, 2, 12, g, lens)
+    codes[0].view(torch.uint8)[..., 7] = 0
+    q = torch.randn(2, 1, Nq, d, generator=g)
+    q[..., 7] = column * 1.5
+    q = q.to(T[dtype])
+    o, lse = binding.forward_cache(q.to(DEV), cache_of(codes, scales, table), ints(lens), True, 0.25)
+    binding.device_status()
+    check(o, lse, q, codes, scales, table, lens, True, 0.25, dtype, Nq == MANY)

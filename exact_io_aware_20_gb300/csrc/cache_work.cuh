@@ -42,13 +42,20 @@ struct FwdCacheParams {
   int bf16;
   float scale_log2;
   float* part_o;          // [CTA][2][RT][D]: O of a piece, not divided by its sum
-  float2* part_ml;        // [CTA][2][RT]: its running maximum (log2 units) and sum
+  float2* part_ml;        // [CTA][2][RT]: its m (see kHead) and sum
   int4* joins;            // [CTA], the many-row kernel's: its unit that goes on behind its share
   int ctas;
 };
 
 constexpr float kNoMax = -1e30f;    // running maximum before the first key
-constexpr float kGrow = 8.f;        // the maximum moves when it grows by more (log2 units)
+// Weights are 2^(their log2 - m).  m is set kHead below a row's maximum and moves
+// when that grows by more than kGrow: the largest weight is between 2^7 and
+// 2^15, inside f16 (to 2^16), and the 25 powers below 1 that f16 has left (its
+// steps end at 2^-24) go to the others.  With m at the maximum itself keys of
+// less than 2^-25 of it were lost from the products, which over 2^17 keys came
+// to 2^-8 of a result.
+constexpr float kHead = 7.f, kGrow = 8.f;   // (log2 units)
+constexpr float kHeadInv = 1.f / 128.f;     // 2^-kHead: row sums are kept without it
 constexpr float kLogE2 = 0.6931471805599453f;
 
 // Tokens of sequence b and the query rows among them; both 0 when a length is
@@ -367,7 +374,7 @@ cache_merge_kernel(const __grid_constant__ FwdCacheParams p) {
         const float total = __shfl_sync(0xffffffffu, sum, kLanes * y), m = __shfl_sync(0xffffffffu, top, kLanes * y);
         if (r >= p.rows) break;
         const int i = r / p.seq.G, head = join.y * p.seq.G + r - i * p.seq.G;
-        const float inv = total == 0.f ? 0.f : 1.f / total;
+        const float inv = total == 0.f ? 0.f : kHeadInv / total;
         uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + b * p.os.b + head * p.os.h + i * p.os.n + lane * kVec);
         #pragma unroll
         for (int v = 0; v < kVec; v += 2)
@@ -376,7 +383,7 @@ cache_merge_kernel(const __grid_constant__ FwdCacheParams p) {
                                 : pack2<false>(acc[y][v] * inv, acc[y][v + 1] * inv);
         if (lane == 0)
           p.lse[(static_cast<long long>(b) * p.H + head) * p.seq.Nq + i] =
-              total == 0.f ? -INFINITY : (m + log2f(total)) * kLogE2;
+              total == 0.f ? -INFINITY : (m + kHead + log2f(total)) * kLogE2;
       }
     }
   }

@@ -6,10 +6,10 @@
 // fp32 sums: q as f16 (a bf16 row is first divided by the power of two of its
 // largest element, which loses nothing that the product could show), and the
 // weights as f16 with the value scale taken into the exponent,
-//     p'_j = 2^(s_j log2 e + log2 vs - m),  m = max_j (s_j log2 e + log2 vs),
-// so that they lie in [0, 1] whatever the pages' scales are; the row sum adds
-// p'_j / vs in fp32.  The running maximum is moved only when it grows by more
-// than 8 (p' then stays below 2^8, well inside f16), so that most tiles need
+//     p'_j = 2^(s_j log2 e + log2 vs - m),  m = max_j (s_j log2 e + log2 vs) - 7,
+// so that they lie in [0, 2^7] whatever the pages' scales are; the row sum adds
+// 2^-7 p'_j / vs in fp32.  m is moved only when the maximum grows by more
+// than 8 (p' then stays below 2^15, inside f16), so that most tiles need
 // one vote and no reduction.
 //
 // Work.  What bounds it for few query rows is the cache's bytes: the G query
@@ -22,8 +22,8 @@
 // writes its maximum, sum and unnormalised O, at most two pieces a CTA.
 //
 // A warp has its own ring of kStages tiles (kTile keys of K and V, 8 KB) in
-// shared memory, filled by TMA through the page table, and its own running
-// maximum, sum and O; the four warps of a CTA meet only where a unit ends.
+// shared memory, filled by TMA through the page table, and its own m,
+// sum and O; the four warps of a CTA meet only where a unit ends.
 // With S^T = K Q^T and O^T = V^T P^T the cache is the A operand (16 keys or 16
 // columns a fragment), so 8 query rows fill an MMA: a step of mma.sync
 // m16n8k16 costs nothing that shows beside the loads.
@@ -99,10 +99,10 @@ struct Smem {
   static constexpr int kBufOff = kQOff + kQBytes;          // O of warps while they are joined:
   static constexpr int kBufWarps = NT * D < 256 ? 2 : 1;   // of one where two CTAs would not fit an SM
   static constexpr int kBufBytes = kBufWarps * 8 * NT * D * 4;
-  static constexpr int kStatOff = kBufOff + kBufBytes;     // (maximum, sum) [warp][row]
+  static constexpr int kStatOff = kBufOff + kBufBytes;     // (m, sum) [warp][row]
   static constexpr int kStatBytes = kWarps * 8 * NT * 8;
   static constexpr int kQsOff = kStatOff + kStatBytes;     // [row] power of two taken off q
-  static constexpr int kMetaOff = kQsOff + 8 * NT * 4;     // (ks, log2 vs, 1 / vs) [warp][stage][page]
+  static constexpr int kMetaOff = kQsOff + 8 * NT * 4;     // (ks, log2 vs, 2^-7 / vs) [warp][stage][page]
   static constexpr int kMetaBytes = kWarps * kStages * T::kSub * 16;
   static constexpr int kBarOff = kMetaOff + kMetaBytes;
   static constexpr int kMiscOff = kBarOff + kWarps * kStages * 8;
@@ -184,7 +184,7 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       const float lv = __shfl_sync(0xffffffffu, tb_lv, from + (lane & (subs - 1)));
       if (lane < subs)
         asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(meta + (stage * T::kSub + lane) * 16),
-                     "f"(ks), "f"(lv), "f"(ex2_approx(-lv)), "f"(0.f) : "memory");
+                     "f"(ks), "f"(lv), "f"(ex2_approx(-lv - kHead)), "f"(0.f) : "memory");
     }
     __syncwarp();
   };
@@ -395,7 +395,8 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
               if (key >= row_limit(p.seq, at.seq, r)) s[nt][k] = -INFINITY;
             }
           }
-          grow |= fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + kGrow || fmaxf(s[nt][1], s[nt][3]) > m[nt][1] + kGrow;
+          grow |= fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + (kHead + kGrow) ||
+                  fmaxf(s[nt][1], s[nt][3]) > m[nt][1] + (kHead + kGrow);
         }
         if (__any_sync(0xffffffffu, grow)) {
           #pragma unroll
@@ -405,7 +406,7 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
               float top = fmaxf(s[nt][c], s[nt][c + 2]);
               #pragma unroll
               for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-              const float now = fmaxf(m[nt][c], top);
+              const float now = fmaxf(m[nt][c], top - kHead);
               const float f = ex2_approx(m[nt][c] - now);
               m[nt][c] = now;
               l[nt][c] *= f;
@@ -613,7 +614,7 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             const float sum = live ? l[nt][c] : 0.f;
             if (whole) {
               // a sum that is not above 0 is a row without keys, or NaN
-              const float inv = sum == 0.f ? 0.f : 1.f / sum;
+              const float inv = sum == 0.f ? 0.f : kHeadInv / sum;
               #pragma unroll
               for (int half = 0; half < T::kHalves; ++half) {
                 uint16_t* dst = p.o + b * p.os.b + head * p.os.h + i * p.os.n + 128 * half + kVec * g;
@@ -630,7 +631,7 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
               }
               if (g == 0)
                 p.lse[(static_cast<long long>(b) * p.H + head) * p.seq.Nq + i] =
-                    sum == 0.f ? -INFINITY : (m[nt][c] + log2f(sum)) * kLogE2;
+                    sum == 0.f ? -INFINITY : (m[nt][c] + kHead + log2f(sum)) * kLogE2;
             } else {
               #pragma unroll
               for (int half = 0; half < T::kHalves; ++half) {

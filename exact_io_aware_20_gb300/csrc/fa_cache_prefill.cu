@@ -88,7 +88,7 @@ struct Pre {
   static constexpr int kQOff = 0;
   static constexpr int kKOff = kTiles * kQTile;
   static constexpr int kVOff = kKOff + kKStages * kKPiece;
-  // By 16-key group, of eight tiles: the scales (ks, log2 vs, 1 / vs); where
+  // By 16-key group, of eight tiles: the scales (ks, log2 vs, 2^-7 / vs); where
   // the group's V begins, its page and its first row there
   static constexpr int kMetaOff = kVOff + kVStages * kVPiece;
   static constexpr int kWhereOff = kMetaOff + 8 * 8 * 16;
@@ -436,7 +436,7 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
               break;
             }
             if (lane >> 3 == t) {
-              meta[(g & 7) * 8 + i] = make_float4(ks, lv, ex2_approx(-lv), 0.f);
+              meta[(g & 7) * 8 + i] = make_float4(ks, lv, ex2_approx(-lv - kHead), 0.f);
               Where* w = where + (g & 7) * 8 + i;
               w->v = p.v + page * p.vs.b + h * p.vs.h + r * p.vs.n;
               w->page = page;
@@ -889,11 +889,11 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
           const float4 sc = ld_shared_f4(mt + 16 * (SEG / 16) * c);
           top = fmaxf(top, fmaf(fmax3(part[0], part[1], fmaxf(part[2], part[3])), row_scale * sc.x, sc.y));
         }
-        const bool grow = top > m + kGrow;
+        const bool grow = top > m + (kHead + kGrow);
         const bool any = __any_sync(0xffffffffu, grow);
         float alpha = 1.f;
         if (any) {
-          const float now = fmaxf(m, top);
+          const float now = fmaxf(m, top - kHead);
           alpha = ex2_approx(m - now);
           m = now;
           l *= alpha;
@@ -957,7 +957,7 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
       const bool in = r < p.rows, whole = w->whole != 0;
       const float sum = (in && i < w->n) ? l : 0.f;
       const long long slot = 2ll * blockIdx.x + (s0 > 0 ? 0 : 1);
-      const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+      const float inv = whole ? (sum == 0.f ? 0.f : kHeadInv / sum) : 1.f;
       // (a tile without keys in this piece may be here before the flag is reset)
       const bool nans = some && nan_seen[np & 7] != 0;
       const int nan_from = max(s0, w->all / 128) * 128, nan_to = min(s1 * 128, sees);
@@ -1020,7 +1020,7 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (in) {
         if (whole)
           p.lse[(static_cast<long long>(b) * p.H + head) * p.seq.Nq + i] =
-              sum == 0.f ? -INFINITY : (m + log2f(sum)) * kLogE2;
+              sum == 0.f ? -INFINITY : (m + kHead + log2f(sum)) * kLogE2;
         else
           p.part_ml[slot * L::kRows + 128 * u + r_tile] = make_float2(m, sum);
       }

@@ -385,13 +385,13 @@ int fa_cache_append(const fa_cache *cache, const void *q, const void *k, const v
  * does not reach a row, whatever its value, NaN included.  The lengths are
  * read on the device, so a captured graph serves growing sequences.
  * q is taken as it is, but for elements far below the largest of their row:
- * with few rows bf16 elements below 2^-13 of it to 2^-25 of it, with many rows
+ * with few rows bf16 elements below 2^-16 of it to 2^-25 of it, with many rows
  * (where q is split into 8-bit parts) elements below 2^-13 (f16: 2^-10) of it
  * to 2^-21 of it.
  * Scales must be positive and finite, between 2^-100 and 2^120.
  * Weights carry the value scale in fp32: with j the key of the largest weight
  * times value scale that a row sees, a key whose page's value scale is 2^-g of
- * j's is left out of the sum when its weight is below 2^(g - 126) of j's.  A
+ * j's is left out of the sum when its weight is below 2^(g - 133) of j's.  A
  * sequence's value scales should lie within 2^100 of one another (a page of
  * zeros has 2^-100).
  * strides[2]: of q, o; NULL: contiguous.  workspace: device memory of at

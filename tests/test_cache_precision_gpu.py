@@ -111,3 +111,38 @@ def test_queries_with_one_column_far_above_the_rest(dtype, d, Nq, column):
     o, lse = binding.forward_cache(q.to(DEV), cache_of(codes, scales, table), ints(lens), True, 0.25)
     binding.device_status()
     check(o, lse, q, codes, scales, table, lens, True, 0.25, dtype, Nq == MANY)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("Nq", [FEW, MANY])
+def test_many_keys_far_below_one(dtype, d, Nq):
+    """One key stands 17.4 above 2^17 others, of which each weighs 2^-25.1 of it
+    and all together 2^-8: one sequence a CTA, so that no cut of the keys gives
+    the small ones a maximum of their own.  (The sequences share their pages.)"""
+    n, page = 1 << 17, 256
+    B = torch.cuda.get_device_properties(0).multi_processor_count * (2 if Nq == FEW else 1)
+    k = torch.zeros(n // page, 1, page, d, dtype=torch.uint8)
+    v = torch.full((n // page, 1, page, d), 0x38, dtype=torch.uint8)      # 1.0
+    k[0, 0, 0, 0] = 0x38
+    v[0, 0, 0] = 0
+    one = torch.ones(n // page, 1)
+    table = torch.arange(n // page, dtype=torch.int32).expand(B, -1).contiguous()
+    cache = cache_of((k, v), (one, one), table)
+    q = torch.zeros(B, 1, Nq, d, dtype=T[dtype], device=DEV)
+    q[..., 0] = 1
+    scale = 17.4
+    o, lse = binding.forward_cache(q, cache, ints([n] * B), False, scale)
+    binding.device_status()
+    w = math.exp(-scale)
+    want = (n - 1) * w / (1 + (n - 1) * w)
+    # weights: 2^-32 of the largest, each; score and exp2 2^-19.  The row sum is in
+    # fp32, and what holds the largest weight takes n / 64 additions (few rows: a
+    # lane has one key in 32 and adds two at a time; many: a row adds 64 keys'
+    # sum), each rounding to 2^-24 of it: n 2^-30 = 2^-13.  (Two weights of
+    # 2^-25.1 are just below half a step of 1, so that a lane loses all of its
+    # 4096, 1.1e-4, as few rows do.)
+    sums = n * 2.0 ** -30
+    bound = n * 2.0 ** -32 + want * (2.0 ** -19 + sums + ref.half_step(T[dtype])) + 2.0 ** -25
+    assert float((o.double() - want).abs().max()) <= bound
+    assert float((lse.double() - scale - math.log1p((n - 1) * w)).abs().max()) <= 2.0 ** -18 * scale + sums

@@ -23,6 +23,25 @@ int check_sizes(int B, int heads, int N, int d, int dtype) {
   return FA_OK;
 }
 
+// x turns, |x| <= 1/2, in whole 2^-64 turns modulo one turn.
+unsigned long long turns_64(double x) {
+  const double u = std::rint(std::ldexp(std::fabs(x), 64));     // <= 2^63
+  return x < 0.0 ? 0ull - static_cast<unsigned long long>(u) : static_cast<unsigned long long>(u);
+}
+
+// The fraction of a turn that one position adds at `freq` radians (whole turns
+// add nothing), in 2^-64 turns.  freq / 2 pi is formed as two doubles, the
+// product with 1 / 2 pi and what its rounding and that of 1 / 2 pi left, and
+// each gives its own whole turns up exactly: good to 2^-64 turns for |freq| <=
+// 2^40, |freq| 2^-105 beyond.  (A product in one double is off by 2^-54 of
+// freq, which a position of 2^31 makes 2^-15 radians of at freq = 100.)
+unsigned long long turn_of(double freq) {
+  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;   // 1 / 2 pi
+  const double turns = freq * kHi;
+  const double rest = std::fma(freq, kHi, -turns) + freq * kLo;
+  return turns_64(turns - std::rint(turns)) + turns_64(rest - std::rint(rest));
+}
+
 int rope_args(const fa_rope_spec* spec, const int* positions, int pos_batch, int B, int d,
               RopeArgs* r) {
   *r = RopeArgs{};
@@ -39,10 +58,7 @@ int rope_args(const fa_rope_spec* spec, const int* positions, int pos_batch, int
   r->pos_batch = pos_batch;
   for (int i = 0; i < spec->pairs; ++i) {
     if (!std::isfinite(spec->freq[i]) || spec->axis[i] >= spec->axes) return FA_ERR_INVALID_ARG;
-    // the fraction of a turn that one position adds; whole turns add nothing
-    double turn = spec->freq[i] * 0.15915494309189533577;   // 1 / 2 pi
-    turn -= std::floor(turn);
-    r->turn[i] = turn >= 1.0 ? 0ull : static_cast<unsigned long long>(std::ldexp(turn, 64));
+    r->turn[i] = turn_of(spec->freq[i]);
     r->axis[i] = spec->axis[i];
   }
   return FA_OK;

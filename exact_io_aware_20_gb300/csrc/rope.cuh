@@ -2,14 +2,15 @@
 // (the device side shared by fa_rope.cu and fa_cache_append.cu).
 //
 // The angle t * freq of a pair is kept as a 64-bit fraction of a turn: with
-// F = freq / 2 pi * 2^64 (rounded once, on the host), t * F in 64-bit integers
-// is the angle modulo one turn with nothing lost however far t is, where a
-// product in fp32 loses t * 2^-24 radians.  The quadrant is taken off in
-// integers as well, and sin and cos of what is left, |a| <= pi / 4, are their
-// Taylor polynomials (the first terms left out are a^11 / 11! < 1.8e-9 and
-// a^12 / 12! < 1.2e-10, below half an fp32 step): about 32 instructions a
-// pair, no tables, no double precision, errors below 7e-8 (1.2e-8 and 1.9e-8
-// in the mean; the rounding of an exact value to fp32 is 1.1e-8 and 1.7e-8).
+// F = freq / 2 pi * 2^64 modulo 2^64 (a whole number, off by less than one; the
+// host forms it in more than a double), t * F in 64-bit integers is the angle
+// modulo one turn to t * 2^-64 turns, where a product in fp32 loses t * 2^-24
+// radians.  The quadrant is taken off in integers as well, and sin and cos of
+// what is left, |a| <= pi / 4, are their Taylor polynomials (the first terms
+// left out are a^11 / 11! < 1.8e-9 and a^12 / 12! < 1.2e-10, below half an fp32
+// step): about 32 instructions a pair, no tables, no double precision, errors
+// below 7e-8 (1.2e-8 and 1.9e-8 in the mean; the rounding of an exact value to
+// fp32 is 1.1e-8 and 1.7e-8).
 #pragma once
 
 #include <cstdint>

@@ -289,7 +289,7 @@ int fa_bwd_blocksparse(const void *q, const void *k, const void *v, const void *
  * for video) and pair p takes the position of axis[p].  freq is in radians
  * per position; the angle is kept as a 64-bit fraction of a turn, so far
  * positions lose nothing (angles are good to about 2^-23 radians at every
- * position).
+ * position, for frequencies up to 2^40).
  */
 #define FA_ROPE_MAX_PAIRS 128
 #define FA_ROPE_MAX_AXES 4

@@ -693,11 +693,14 @@ extern "C" int fa_get_device_status(fa_stream_t stream) {
   e = cudaMemcpyFromSymbol(&word, fa::g_device_error, sizeof(word));
   if (e != cudaSuccess) return fa::cuda_fail(e, "read device error word");
   if (word != 0) {
-    const unsigned int zero = 0;
-    e = cudaMemcpyToSymbol(fa::g_device_error, &zero, sizeof(zero));
+    // one kind a call: the others stay in the word for the next
+    const unsigned int kind = word & fa::kErrTimeout ? fa::kErrTimeout
+                              : word & fa::kErrCache ? fa::kErrCache : word;
+    const unsigned int rest = word & ~kind;
+    e = cudaMemcpyToSymbol(fa::g_device_error, &rest, sizeof(rest));
     if (e != cudaSuccess) return fa::cuda_fail(e, "clear device error word");
-    if (word & fa::kErrTimeout) return FA_ERR_TIMEOUT;
-    if (word & fa::kErrCache) return FA_ERR_CACHE;
+    if (kind == fa::kErrTimeout) return FA_ERR_TIMEOUT;
+    if (kind == fa::kErrCache) return FA_ERR_CACHE;
     std::snprintf(fa::g_cuda_msg, sizeof(fa::g_cuda_msg),
                   "a kernel found its dynamic shared memory base misaligned (error word %#x)",
                   word);

@@ -413,10 +413,11 @@ int fa_fwd_cache(const void *q, const fa_cache *cache, void *o, float *lse, int 
 size_t fa_fwd_cache_workspace_size(int B, int H, int Hkv, int Nq, int d);
 
 /*
- * Synchronises `stream`, then reports (and clears) the device-side error
- * word: FA_ERR_TIMEOUT if a kernel gave up on a bounded wait since the last
- * call, FA_ERR_CACHE if a kernel met a page table entry or a sequence length
- * out of range, FA_ERR_CUDA if the stream itself failed, FA_OK otherwise.
+ * Synchronises `stream`, then reports (and clears) what the device-side error
+ * word holds: FA_ERR_TIMEOUT if a kernel gave up on a bounded wait,
+ * FA_ERR_CACHE if a kernel met a page table entry or a sequence length out of
+ * range, FA_ERR_CUDA if the stream itself failed, FA_OK otherwise.  One kind a
+ * call, in this order: where both are there the next call reports the other.
  */
 int fa_get_device_status(fa_stream_t stream);
 

@@ -682,8 +682,8 @@ def _forward_cache(q, cache, seq_lens, causal, scale, new_lens, out, lse, worksp
     if workspace is None:
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=cache.device)
     else:
-        if workspace.get_device() != device:
-            raise ValueError("the workspace must be on the inputs' device")
+        if workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError("the workspace must be contiguous and on the inputs' device")
         ws_bytes = workspace.numel() * workspace.element_size()
     _check(load().fa_fwd_cache(
         q.data_ptr(), cache._ref, out.data_ptr(), lse.data_ptr(), B, H, Nq, int(causal), float(scale), code,

@@ -1,5 +1,6 @@
 // C-ABI layer of the rotary positions and the paged 8-bit cache: argument
 // validation and dispatch.  See include/fa.h for the contract.
+#include <algorithm>
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -158,7 +159,7 @@ extern "C" int fa_rope(const void* q, const void* k, void* q_out, void* k_out, i
   c.bf16 = dtype == FA_BF16;
   unsigned int* err = nullptr;
   if ((st = fa::check_device(&err)) != FA_OK) return st;
-  cudaError_t e = fa::launch_rope(c, r, reinterpret_cast<cudaStream_t>(stream));
+  cudaError_t e = fa::launch_rope(c, r, std::max(1, fa::device_sms()), reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA_OK : fa::cuda_fail(e, "fa_rope launch");
 }
 
@@ -200,7 +201,8 @@ extern "C" int fa_cache_append(const fa_cache* cache, const void* q, const void*
   c.seq_lens = seq_lens;
   c.new_lens = new_lens;
   if ((st = fa::check_device(&c.err)) != FA_OK) return st;
-  cudaError_t e = fa::launch_cache_append(ca, c, r, reinterpret_cast<cudaStream_t>(stream));
+  cudaError_t e = fa::launch_cache_append(ca, c, r, std::max(1, fa::device_sms()),
+                                          reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA_OK : fa::cuda_fail(e, "fa_cache_append launch");
 }
 

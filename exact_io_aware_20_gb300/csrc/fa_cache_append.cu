@@ -27,7 +27,7 @@ namespace {
 // themselves; with it few and long ones leave the memory to q's blocks (prompts
 // of 4 x 4099 tokens, 2 / 4 / 8 an SM: 72 / 77 / 81 us with q, 57 / 48 / 51
 // without).
-inline int units_wanted(bool q) { return (q ? 2 : 4) * 152; }
+inline int units_wanted(bool q, int sms) { return (q ? 2 : 4) * sms; }
 
 struct AppendParams {
   const uint16_t *q, *k, *v;
@@ -379,7 +379,7 @@ append_kernel(const __grid_constant__ AppendParams p) {
 }
 
 template <int GROUP, int HOLD>
-cudaError_t launch(AppendParams& p, int bf16, cudaStream_t stream) {
+cudaError_t launch(AppendParams& p, int bf16, int sms, cudaStream_t stream) {
   constexpr int kThreads = GROUP == 32 ? 128 : GROUP;
   // Heads of a unit: all of them when there are pages enough to fill the chip
   // without (angles are then worked out once a page), one when there are few.
@@ -387,7 +387,7 @@ cudaError_t launch(AppendParams& p, int bf16, cudaStream_t stream) {
   p.unit_heads = GROUP == 32 || HOLD == 0
                      ? 1
                      : static_cast<int>(std::max(1ll, std::min<long long>(
-                           p.cache.Hkv, pages * p.cache.Hkv / units_wanted(p.q != nullptr))));
+                           p.cache.Hkv, pages * p.cache.Hkv / units_wanted(p.q != nullptr, sms))));
   const int groups = (p.cache.Hkv + p.unit_heads - 1) / p.unit_heads;
   p.unit_heads = (p.cache.Hkv + groups - 1) / groups;      // evenly
   const long long units = pages * groups;
@@ -415,7 +415,7 @@ cudaError_t launch(AppendParams& p, int bf16, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_cache_append(const Cache& cache, const AppendCall& c, const RopeArgs& r,
-                                cudaStream_t stream) {
+                                int sms, cudaStream_t stream) {
   AppendParams p = {};
   p.q = static_cast<const uint16_t*>(c.q);
   p.k = static_cast<const uint16_t*>(c.k);
@@ -438,7 +438,7 @@ cudaError_t launch_cache_append(const Cache& cache, const AppendCall& c, const R
   // three axes 9.6 / 10.5 / 12.8 us, 512 tokens of 32 + 2 x 8 heads 8.4 / 9.3 /
   // 10.1, long prompts the same).
   const long long groups =
-      std::max(1ll, std::min<long long>(std::max(c.H, 1), 256ll * 152 / p.q_items));
+      std::max(1ll, std::min<long long>(std::max(c.H, 1), 256ll * sms / p.q_items));
   p.q_heads_per = std::min<long long>(16, (std::max(c.H, 1) + groups - 1) / groups);
   p.seq_lens = c.seq_lens;
   p.new_lens = c.new_lens;
@@ -447,10 +447,10 @@ cudaError_t launch_cache_append(const Cache& cache, const AppendCall& c, const R
   // The slots of the new rows of a page: a warp holds up to 64 of them, 256
   // threads 512, 512 threads 1024; larger pages are read twice.
   const int count = std::min(c.N, cache.page) * p.slots;
-  if (count <= 64) return launch<32, 2>(p, c.bf16, stream);
-  if (count <= 512) return launch<256, 2>(p, c.bf16, stream);
-  if (count <= 1024) return launch<512, 2>(p, c.bf16, stream);
-  return launch<512, 0>(p, c.bf16, stream);
+  if (count <= 64) return launch<32, 2>(p, c.bf16, sms, stream);
+  if (count <= 512) return launch<256, 2>(p, c.bf16, sms, stream);
+  if (count <= 1024) return launch<512, 2>(p, c.bf16, sms, stream);
+  return launch<512, 0>(p, c.bf16, sms, stream);
 }
 
 }  // namespace fa

@@ -128,7 +128,7 @@ struct RopeCall {
   Strides qs, ks, qos, kos;
   int B, H, Hkv, N, d, bf16;
 };
-cudaError_t launch_rope(const RopeCall& c, const RopeArgs& r, cudaStream_t stream);
+cudaError_t launch_rope(const RopeCall& c, const RopeArgs& r, int sms, cudaStream_t stream);
 
 // A paged 8-bit cache (see fa_cache), strides in bytes.
 struct Cache {
@@ -149,7 +149,7 @@ struct AppendCall {
   unsigned int* err;
 };
 cudaError_t launch_cache_append(const Cache& cache, const AppendCall& c, const RopeArgs& r,
-                                cudaStream_t stream);
+                                int sms, cudaStream_t stream);
 
 struct CacheFwdCall {
   const void* q;

@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeCall& c, const RopeArgs& r, cudaStream_t stream) {
+cudaError_t launch_rope(const RopeCall& c, const RopeArgs& r, int sms, cudaStream_t stream) {
   RopeParams p = {};
   p.q = static_cast<const uint16_t*>(c.q);
   p.k = static_cast<const uint16_t*>(c.k);
@@ -71,7 +71,7 @@ cudaError_t launch_rope(const RopeCall& c, const RopeArgs& r, cudaStream_t strea
   // 8.3 / 9.4 / 10.1 us, 512 tokens of 32 + 8 heads 5.0 / 5.8 / 7.9 / 7.9, 4096 of
   // them 19.6 / 17.1 / 17.9 / 18.8; 2 x 8192 of them with 6 / 10 / 20 / 40 heads a
   // thread 56.2 / 55.2 / 54.9 / 60.8.
-  const long long want = 1024ll * 152;
+  const long long want = 1024ll * sms;
   const long long groups =
       std::max(1ll, std::min(std::min<long long>(p.heads, 4096), want / p.items));
   p.heads_per = std::min(16, static_cast<int>((p.heads + groups - 1) / groups));

@@ -55,7 +55,10 @@ constexpr float kNoMax = -1e30f;    // running maximum before the first key
 // less than 2^-25 of it were lost from the products, which over 2^17 keys came
 // to 2^-8 of a result.
 constexpr float kHead = 7.f, kGrow = 8.f;   // (log2 units)
-constexpr float kHeadInv = 1.f / 128.f;     // 2^-kHead: row sums are kept without it
+// 2^-kHead: row sums are kept without it, their terms' factor 2^-kHead / vs as a
+// product (2^-7 over the largest scale, 2^120, is no normal number, and the
+// exponential would give 0)
+constexpr float kHeadInv = 1.f / 128.f;
 constexpr float kLogE2 = 0.6931471805599453f;
 
 // Tokens of sequence b and the query rows among them; both 0 when a length is

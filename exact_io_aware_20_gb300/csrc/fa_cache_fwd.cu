@@ -184,7 +184,7 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
       const float lv = __shfl_sync(0xffffffffu, tb_lv, from + (lane & (subs - 1)));
       if (lane < subs)
         asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(meta + (stage * T::kSub + lane) * 16),
-                     "f"(ks), "f"(lv), "f"(ex2_approx(-lv - kHead)), "f"(0.f) : "memory");
+                     "f"(ks), "f"(lv), "f"(ex2_approx(-lv) * kHeadInv), "f"(0.f) : "memory");
     }
     __syncwarp();
   };

@@ -436,7 +436,7 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
               break;
             }
             if (lane >> 3 == t) {
-              meta[(g & 7) * 8 + i] = make_float4(ks, lv, ex2_approx(-lv - kHead), 0.f);
+              meta[(g & 7) * 8 + i] = make_float4(ks, lv, ex2_approx(-lv) * kHeadInv, 0.f);
               Where* w = where + (g & 7) * 8 + i;
               w->v = p.v + page * p.vs.b + h * p.vs.h + r * p.vs.n;
               w->page = page;

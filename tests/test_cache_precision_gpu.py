@@ -146,3 +146,29 @@ def test_many_keys_far_below_one(dtype, d, Nq):
     bound = n * 2.0 ** -32 + want * (2.0 ** -19 + sums + ref.half_step(T[dtype])) + 2.0 ** -25
     assert float((o.double() - want).abs().max()) <= bound
     assert float((lse.double() - scale - math.log1p((n - 1) * w)).abs().max()) <= 2.0 ** -18 * scale + sums
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("Nq", [FEW, MANY])
+@pytest.mark.parametrize("power", [-100, -99, 118, 119, 120])
+def test_value_scales_at_both_ends(d, Nq, power):
+    """The smallest and largest value scales: results are those of scales of one
+    times the power, and L does not know of them."""
+    g = torch.Generator().manual_seed(d + Nq)
+    lens = [300, 131]
+    codes, scales, table = ref.make_cache(30, 1, 32, d, 2, 12, g, lens)
+    codes[1] = codes[1].float().div_(256).to(torch.float8_e4m3fn)       # below 2, so that 2^120 stays in bf16's range
+    q = torch.randn(2, 2, Nq, d, generator=g).bfloat16().to(DEV)
+    outs = []
+    for p in (0, power):
+        vs = torch.full_like(scales[1], 2.0 ** p)
+        outs.append(binding.forward_cache(q, cache_of(codes, (scales[0], vs), table), ints(lens), True, 0.1))
+    binding.device_status()
+    (o, lse), (o_p, lse_p) = outs
+    # sums of exponents of up to 2^7 round to 2^-18 (weights and L by as much, a
+    # few times over: 2^-15), weights to half a step of f16 and o to one of bf16
+    # on either side
+    want = o.double()
+    size = float(codes[1].float().abs().max())
+    assert float((lse_p - lse).abs().max()) <= 2.0 ** -15
+    assert ((o_p.double() / 2.0 ** power - want).abs() <= 2 * (2.0 ** -8 * want.abs() + 2.0 ** -11 * size)).all()

@@ -44,8 +44,10 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 3;
-// A unit's cost besides its steps, in steps (0 / 1 / 2 / 3: a step of 32
-// sequences with 4096 tokens takes 64 / 52.5 / 49 / 46 us).
+// A unit's cost besides its steps, in steps (1 / 2 / 3 / 4 / 5 / 6: 32 sequences of
+// up to 4096 tokens take 41 / 36 / 34 / 34 / 34 / 35 us, 128 of up to 700 41 / 35 /
+// 35 / 35 / 35 / 36, 64 of up to 2000 at d = 64 52 / 44 / 44 / 42 / 43 / 46, 16 of up
+// to 4000 at d = 256 26 / 24 / 23 / 23 / 22 / 23, 8 of 8192 35 / 34 / 34 / 33 / 33 / 33).
 constexpr int kOver = 3;
 
 template <int D>

@@ -28,7 +28,7 @@
 // exponent, both by groups of keys that a page holds for certain (64, 32 or 16
 // by the page size): the group's largest raw score is scaled, not each score,
 // and the exponent's multiply-add takes the scales for the rest (the chunk
-// below with pages of 64 takes 172 us, with pages of 16 193).
+// below with pages of 64 takes 173 us, with pages of 16 195).
 //
 // Roles: warps 0-3 softmax of tile A, 4-7 of tile B (d = 256: conversion),
 // 8-11 conversion and q, 12 issues the products, 13 walks the share and
@@ -43,8 +43,8 @@
 // fill lines, in more code: d = 256 308 -> 315 us, not kept).
 //
 // Measured (2 chunks of 512 tokens against up to 16384, 32 heads on 8, d = 128,
-// bf16): 172 us, 1270 TFLOP/s; d = 256, f16, four causal prompts of 4096
-// tokens, 8 heads: 296 us, 930 TFLOP/s.  What bounds it: at d <= 128 a tile pair
+// bf16): 173 us, 1260 TFLOP/s; d = 256, f16, four causal prompts of 4096
+// tokens, 8 heads: 300 us, 915 TFLOP/s.  What bounds it: at d <= 128 a tile pair
 // takes about 2900 clocks for 2048 of products, the softmax of each row tile
 // (400 for the maximum, 950 for the weights) and the products of the other by
 // turns; at d = 256 about 3800 for 2560, where one softmax group has nothing to
@@ -66,9 +66,14 @@ template <int D>
 struct Pre {
   static constexpr int kTiles = D == 256 ? 1 : 2;
   static constexpr int kRows = 128 * kTiles;        // of a unit
-  // A unit's cost besides its steps, in steps.  d = 256, causal prompts of 4096:
-  // 3 / 4 / 5 / 7 take 317 / 305 / 297 / 316 us; prompts of 2048 at d = 128,
-  // 4 / 6 / 8 / 11: 120.5 / 116.8 / 116.4 / 117.6, at d = 64 94.1 / 94.0 / 96.7 / 96.6.
+  // A unit's cost besides its steps, in steps.  d = 256, 3 / 4 / 5 / 6 / 7 / 8:
+  // causal prompts of 4 x 4096 take 322 / 311 / 301 / 305 / 321 / 326 us, of
+  // 8 x 1024 135 / 135 / 132 / 136 / 138 / 144, of 8192 249 / 238 / 236 / 237 /
+  // 240 / 243, ragged chunks of 1500 82 / 82 / 77 / 78 / 80 / 80.  d = 128, 4 / 5 /
+  // 6 / 8 / 10 / 12: 4 x 2048 121 / 124 / 117 / 117 / 115 / 119, 8 x 1000 158 / 156 /
+  // 154 / 154 / 162 / 155, 8192 265 / 246 / 240 / 244 / 244 / 248; d = 64,
+  // 4 x 2048: 90 / 97 / 89 / 96 / 90 / 98.  (How shares fall on a shape moves a
+  // time by up to 8% either way; 5 and 6 are within 2% of the best on each.)
   static constexpr int kOver = kTiles == 1 ? 5 : 6;
   static constexpr int kSoftWarps = 4 * kTiles;
   static constexpr int kConvWarps = 12 - kSoftWarps;

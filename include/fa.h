@@ -389,6 +389,8 @@ int fa_cache_append(const fa_cache *cache, const void *q, const void *k, const v
  * (where q is split into 8-bit parts) elements below 2^-13 (f16: 2^-10) of it
  * to 2^-21 of it.
  * Scales must be positive and finite, between 2^-100 and 2^120.
+ * The product with V takes the weights as f16, each to half a step (2^-11 of it)
+ * down to 2^-21 of a row's largest, and to 2^-32 of that below.
  * Weights carry the value scale in fp32: with j the key of the largest weight
  * times value scale that a row sees, a key whose page's value scale is 2^-g of
  * j's is left out of the sum when its weight is below 2^(g - 133) of j's.  A

@@ -50,6 +50,16 @@ SIGNATURES = {
     "fa_fwd_cache": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp, _vp, _vp, _vp, _sz,
                           _vp]),
     "fa_fwd_cache_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "fa_fwd_cache_tree": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _f, _i, _vp, _vp, _vp, _i, _vp, _vp, _sz,
+                               _vp]),
+    "fa_qk_norm_rope": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _f, _f, _i, _i, _i, _i, _i, _i, _vp, _vp,
+                             _i, _vp, _vp]),
+    "fa_qk_norm_rope_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _f, _f, _vp, _vp, _i, _i, _i,
+                                 _i, _i, _i, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
+    "fa_qk_norm_rope_bwd_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "fa_cache_keep": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "fa_cache_fork": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "fa_cache_fork_workspace_size": (_sz, [_i, _i, _i]),
     "fa_get_device_status": (_i, [_vp]),
     "fa_strerror": (ctypes.c_char_p, [_i]),
     "fa_selftest_expired_wait": (_i, [_i, _vp]),
@@ -669,22 +679,32 @@ def _forward_plan(cache, q, out):
             fwd_cache_workspace_size(B, H, cache[1], Nq, d))
 
 
+def _lse(lse, B, H, Nq, cache):
+    """The lse given, checked, or a new one."""
+    if lse is None:
+        return torch.empty((B, H, Nq), dtype=torch.float32, device=cache.device)
+    if (lse.dtype != torch.float32 or lse.shape != (B, H, Nq) or lse.get_device() != cache.device_index
+            or not lse.is_contiguous()):
+        raise ValueError(f"lse must be contiguous fp32 [{B}, {H}, {Nq}] on the inputs' device")
+    return lse
+
+
+def _scratch(workspace, ws_bytes, of):
+    """(workspace, its bytes): the one given, checked, or a new one of ws_bytes, on the device of `of`."""
+    if workspace is None:
+        return torch.empty(ws_bytes, dtype=torch.uint8, device=of.device), ws_bytes
+    if workspace.device != of.device or not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous and on the inputs' device")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
 def _forward_cache(q, cache, seq_lens, causal, scale, new_lens, out, lse, workspace, stream):
     if out is None:
         out = torch.empty_like(q)
     B, H, Nq, code, st, ws_bytes = _plan(_forward_plan, cache.key, _geometry(q), _geometry(out))
     device = cache.device_index
-    if lse is None:
-        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=cache.device)
-    elif (lse.dtype != torch.float32 or lse.shape != (B, H, Nq) or lse.get_device() != device
-          or not lse.is_contiguous()):
-        raise ValueError(f"lse must be contiguous fp32 [{B}, {H}, {Nq}] on the inputs' device")
-    if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=cache.device)
-    else:
-        if workspace.get_device() != device or not workspace.is_contiguous():
-            raise ValueError("the workspace must be contiguous and on the inputs' device")
-        ws_bytes = workspace.numel() * workspace.element_size()
+    lse = _lse(lse, B, H, Nq, cache)
+    workspace, ws_bytes = _scratch(workspace, ws_bytes, cache)
     _check(load().fa_fwd_cache(
         q.data_ptr(), cache._ref, out.data_ptr(), lse.data_ptr(), B, H, Nq, int(causal), float(scale), code,
         _ints(seq_lens, (B,), device, "seq_lens"), _ints(new_lens, (B,), device, "new_lens"), st,
@@ -693,5 +713,224 @@ def _forward_cache(q, cache, seq_lens, causal, scale, new_lens, out, lse, worksp
 
 
 def fwd_cache_workspace_size(B, H, Hkv, Nq, d) -> int:
-    """Bytes of workspace forward_cache needs on the current device."""
+    """Bytes of workspace forward_cache and forward_cache_tree need on the current device."""
     return int(load().fa_fwd_cache_workspace_size(B, H, Hkv, Nq, d))
+
+
+# ---------------------------------------------------------------- branching decode
+def tree_mask(parents):
+    """The mask that forward_cache_tree takes, int32 [B, Nq, ceil(Nq / 32)] on the
+    CPU, of B trees given as sequences of parents: drafted token i sees itself
+    and what token parents[b][i] < i sees (-1: none but itself, besides the
+    tokens before the drafts).  Rows behind a shorter tree's tokens are 0."""
+    N = max((len(t) for t in parents), default=0)
+    if N == 0:
+        raise ValueError("expected a drafted token at least")
+    words = -(-N // 32)
+    mask = torch.zeros((len(parents), N, words), dtype=torch.int64)
+    for b, tree in enumerate(parents):
+        for i, parent in enumerate(tree):
+            if not -1 <= parent < i:
+                raise ValueError("a drafted token's parent is one before it, or -1")
+            if parent >= 0:
+                mask[b, i] = mask[b, parent]
+            mask[b, i, i // 32] |= 1 << (i % 32)
+    return torch.where(mask >= 1 << 31, mask - (1 << 32), mask).to(torch.int32)
+
+
+def forward_cache_tree(q, cache: Cache, seq_lens, mask, scale: float, new_lens=None, out=None, lse=None,
+                       workspace=None, stream=None):
+    """(o, lse) of q [B, H, Nq, d], the last new_lens[b] tokens of each sequence
+    (None: all Nq), against the tokens before them and those of one another
+    that the mask has (fa_fwd_cache_tree).  mask: int32 [B or 1, Nq,
+    ceil(Nq / 32)], bit j % 32 of word j / 32 of row i: i sees j (`tree_mask`)."""
+    return _on_stream(q.get_device(), stream, _forward_cache_tree, q, cache, seq_lens, mask, scale,
+                      new_lens, out, lse, workspace)
+
+
+def _forward_cache_tree(q, cache, seq_lens, mask, scale, new_lens, out, lse, workspace, stream):
+    if out is None:
+        out = torch.empty_like(q)
+    B, H, Nq, code, st, ws_bytes = _plan(_forward_plan, cache.key, _geometry(q), _geometry(out))
+    device = cache.device_index
+    if (mask.dtype != torch.int32 or mask.dim() != 3 or mask.shape[0] not in (1, B) or mask.shape[1] != Nq
+            or mask.shape[2] != -(-Nq // 32) or mask.get_device() != device or not mask.is_contiguous()):
+        raise ValueError(f"the mask must be contiguous int32 [{B} or 1, {Nq}, {-(-Nq // 32)}] on the inputs' "
+                         "device")
+    lse = _lse(lse, B, H, Nq, cache)
+    workspace, ws_bytes = _scratch(workspace, ws_bytes, cache)
+    _check(load().fa_fwd_cache_tree(
+        q.data_ptr(), cache._ref, out.data_ptr(), lse.data_ptr(), B, H, Nq, float(scale), code,
+        _ints(seq_lens, (B,), device, "seq_lens"), _ints(new_lens, (B,), device, "new_lens"), mask.data_ptr(),
+        mask.shape[0], st, workspace.data_ptr(), ws_bytes, stream), "fa_fwd_cache_tree")
+    return out, lse
+
+
+def cache_keep(cache: Cache, seq_lens, window: int, keep, keep_lens=None, new_lens=None, out_lens=None,
+               stream=None):
+    """Of the last new_lens[b] tokens of each sequence (None: `window`, which is
+    the most there may be) those numbered keep[b] [:keep_lens[b]] (None: all of
+    keep's row), in increasing order, move to the front of them, in place; the
+    new lengths are returned (fa_cache_keep).  keep: int32 [B, K]; out_lens is
+    allocated unless given, and must not be seq_lens."""
+    return _on_stream(cache.device_index, stream, _cache_keep, cache, seq_lens, window, keep, keep_lens,
+                      new_lens, out_lens)
+
+
+def _cache_keep(cache, seq_lens, window, keep, keep_lens, new_lens, out_lens, stream):
+    B, device = cache.B, cache.device_index
+    if keep.dim() != 2:
+        raise ValueError("expected keep [B, K]")
+    if out_lens is None:
+        out_lens = torch.empty((B,), dtype=torch.int32, device=cache.device)
+    _check(load().fa_cache_keep(
+        cache._ref, B, int(window), keep.shape[1], _ints(seq_lens, (B,), device, "seq_lens"),
+        _ints(new_lens, (B,), device, "new_lens"), _ints(keep, (B, keep.shape[1]), device, "keep"),
+        _ints(keep_lens, (B,), device, "keep_lens"), _ints(out_lens, (B,), device, "out_lens"), stream),
+        "fa_cache_keep")
+    return out_lens
+
+
+def cache_fork(cache: Cache, refs, parents, seq_lens, reserve_lens=None, out_lens=None, block_table=None,
+               workspace=None, stream=None):
+    """Sequence b goes on from sequence parents[b] (-1: it begins empty), with
+    pages for reserve_lens[b] tokens at least (None: for those it has); whole
+    pages are shared, the others kept, copied or taken from the free ones, and
+    refs int32 [pages], how many hold each page, is brought up to date
+    (fa_cache_fork).  The cache's block_table is changed in place, or the new
+    one written to `block_table`.  The new lengths are returned (out_lens may be
+    seq_lens)."""
+    return _on_stream(cache.device_index, stream, _cache_fork, cache, refs, parents, seq_lens, reserve_lens,
+                      out_lens, block_table, workspace)
+
+
+def cache_fork_workspace_size(B, pages, table_width) -> int:
+    """Bytes of workspace cache_fork needs."""
+    return int(load().fa_cache_fork_workspace_size(B, pages, table_width))
+
+
+def _cache_fork(cache, refs, parents, seq_lens, reserve_lens, out_lens, block_table, workspace, stream):
+    B, device = cache.B, cache.device_index
+    if out_lens is None:
+        out_lens = torch.empty((B,), dtype=torch.int32, device=cache.device)
+    table = _ints(cache.tensors[4] if block_table is None else block_table, (B, cache.table_width), device,
+                  "block_table")
+    ws_bytes = _plan(cache_fork_workspace_size, B, cache.pages, cache.table_width)
+    workspace, ws_bytes = _scratch(workspace, ws_bytes, cache)
+    _check(load().fa_cache_fork(
+        cache._ref, table, _ints(refs, (cache.pages,), device, "refs"), B, _ints(parents, (B,), device, "parents"),
+        _ints(seq_lens, (B,), device, "seq_lens"), _ints(reserve_lens, (B,), device, "reserve_lens"),
+        _ints(out_lens, (B,), device, "out_lens"), workspace.data_ptr(), ws_bytes, stream), "fa_cache_fork")
+    return out_lens
+
+
+# ---------------------------------------------------------------- norms of q and k
+def _norm_plan(q_weight, k_weight, heads, *views):
+    """(B, H, Hkv, N, d, dtype code, weights_f32, fa_strides) of q and k views by turns, the first two q's
+    and k's; heads: whether there is a k."""
+    B, H, N, d = views[0][0] if len(views[0][0]) == 4 else (0, 0, 0, 0)
+    if B == 0 or any((v is None) == heads for v in views[1::2]):
+        raise ValueError("expected q [B, H, N, d], and k [B, Hkv, N, d] in every place or none")
+    if heads and len(views[1][0]) != 4:
+        raise ValueError("expected k [B, Hkv, N, d]")
+    dtype, device = views[0][2], views[0][3]
+    Hkv = views[1][0][1] if heads else 0
+    st = (FaStrides * len(views))()
+    for i, v in enumerate(views):
+        if v is not None:
+            st[i] = FaStrides(*_view(v, (B, Hkv if i % 2 else H, N, d), dtype, device, "k" if i % 2 else "q"))
+    if not heads and k_weight is not None:
+        raise ValueError("a k_weight without k")
+    types = set()
+    for w in (q_weight, k_weight):
+        if w is not None:
+            of, stride, its_dtype, its_device = w
+            if of != (d,) or (d > 1 and stride != (1,)) or its_device != device:
+                raise ValueError(f"weights must be contiguous [{d}] on the inputs' device")
+            types.add(its_dtype)
+    if len(types) > 1 or not types <= {dtype, torch.float32}:
+        raise TypeError("weights are both of the inputs' dtype, or both fp32")
+    return B, H, Hkv, N, d, _code(dtype), int(types == {torch.float32}), st
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, eps: float, positions=None, table: Rope | None = None,
+                 offset: float = 0.0, q_out=None, k_out=None, stream=None):
+    """(q_out, k_out): every row x of q [B, H, N, d] and k [B, Hkv, N, d] (or
+    None) becomes x / sqrt(mean(x^2) + eps) * (offset + weight), rotated by
+    `table` (None: not rotated) at `positions` as in `rope` (fa_qk_norm_rope).
+    Weights [d] of the inputs' dtype or fp32, None: ones.  Any views with d
+    contiguous; outputs are allocated like the inputs unless given, and may be
+    the inputs."""
+    return _on_stream(q.get_device(), stream, _qk_norm_rope, q, k, q_weight, k_weight, eps, positions, table,
+                      offset, q_out, k_out)
+
+
+def _qk_norm_rope(q, k, q_weight, k_weight, eps, positions, table, offset, q_out, k_out, stream):
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    if k is not None and k_out is None:
+        k_out = torch.empty_like(k)
+    B, H, Hkv, N, d, code, f32, st = _plan(_norm_plan, _geometry(q_weight), _geometry(k_weight), k is not None,
+                                           _geometry(q), _geometry(k), _geometry(q_out), _geometry(k_out))
+    pos, pos_batch = (None, 1) if table is None else _positions(positions, table.axes, B, N, q.get_device())
+    _check(load().fa_qk_norm_rope(
+        q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), _ptr(q_weight), _ptr(k_weight), f32, float(eps),
+        float(offset), B, H, Hkv, N, d, code, None if table is None else table._ref, pos, pos_batch, st, stream),
+        "fa_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, eps: float, positions=None,
+                          table: Rope | None = None, offset: float = 0.0, dq=None, dk=None, dq_weight=None,
+                          dk_weight=None, workspace=None, stream=None):
+    """(dq, dk, dq_weight, dk_weight) of `qk_norm_rope` from the gradients of its
+    outputs and its inputs (fa_qk_norm_rope_bwd); the weights' gradients are
+    fp32 [d], None where there is no weight.  dq may be dq_out or q."""
+    return _on_stream(q.get_device(), stream, _qk_norm_rope_backward, dq_out, dk_out, q, k, q_weight, k_weight,
+                      eps, positions, table, offset, dq, dk, dq_weight, dk_weight, workspace)
+
+
+def qk_norm_rope_bwd_workspace_size(B, H, Hkv, N, d) -> int:
+    """Bytes of workspace qk_norm_rope_backward needs on the current device."""
+    return int(load().fa_qk_norm_rope_bwd_workspace_size(B, H, Hkv, N, d))
+
+
+def _norm_bwd_workspace(device, *sizes):
+    return qk_norm_rope_bwd_workspace_size(*sizes)
+
+
+def _qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, eps, positions, table, offset, dq, dk,
+                           dq_weight, dk_weight, workspace, stream):
+    if dq is None:
+        dq = torch.empty_like(q)
+    if k is not None and dk is None:
+        dk = torch.empty_like(k)
+    B, H, Hkv, N, d, code, f32, st = _plan(
+        _norm_plan, _geometry(q_weight), _geometry(k_weight), k is not None, _geometry(dq_out), _geometry(dk_out),
+        _geometry(q), _geometry(k), _geometry(dq), _geometry(dk))
+    device = q.get_device()
+
+    def sums(weight, given, what):
+        if weight is None:
+            if given is not None:
+                raise ValueError(f"{what} without its weight")
+            return None
+        if given is None:
+            return torch.empty((d,), dtype=torch.float32, device=q.device)
+        if (given.dtype != torch.float32 or given.shape != (d,) or given.get_device() != device
+                or not given.is_contiguous()):
+            raise ValueError(f"{what} must be contiguous fp32 [{d}] on the inputs' device")
+        return given
+
+    dq_weight, dk_weight = sums(q_weight, dq_weight, "dq_weight"), sums(k_weight, dk_weight, "dk_weight")
+    ws_bytes = 0
+    if dq_weight is not None or dk_weight is not None:
+        ws_bytes = _plan(_norm_bwd_workspace, device, B, H, Hkv, N, d)
+        workspace, ws_bytes = _scratch(workspace, ws_bytes, q)
+    pos, pos_batch = (None, 1) if table is None else _positions(positions, table.axes, B, N, device)
+    _check(load().fa_qk_norm_rope_bwd(
+        dq_out.data_ptr(), _ptr(dk_out), q.data_ptr(), _ptr(k), dq.data_ptr(), _ptr(dk), _ptr(q_weight),
+        _ptr(k_weight), f32, float(eps), float(offset), _ptr(dq_weight), _ptr(dk_weight), B, H, Hkv, N, d, code,
+        None if table is None else table._ref, pos, pos_batch, st, _ptr(workspace), ws_bytes, stream),
+        "fa_qk_norm_rope_bwd")
+    return dq, dk, dq_weight, dk_weight

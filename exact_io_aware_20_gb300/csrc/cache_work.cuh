@@ -19,9 +19,12 @@
 
 namespace fa {
 
+// What the query rows of a sequence see of its tokens.
+enum : int { kSeeAll = 0, kSeeCausal = 1, kSeeTree = 2 };
+
 struct SeqParams {
   const int *seq_lens, *new_lens;
-  int B, G, Nq, causal;
+  int B, G, Nq, causal;   // (causal: kSee...)
   long long capacity;   // tokens that a table row can map
   unsigned int* err;
 };
@@ -45,6 +48,9 @@ struct FwdCacheParams {
   float2* part_ml;        // [CTA][2][RT]: its m (see kHead) and sum
   int4* joins;            // [CTA], the many-row kernel's: its unit that goes on behind its share
   int ctas;
+  const uint32_t* tree;   // kSeeTree: [1 or B][Nq][tree_words], bit j of row i: it sees drafted token j
+  long long tree_batch;   // words from a sequence's to the next's
+  int tree_words;
 };
 
 constexpr float kNoMax = -1e30f;    // running maximum before the first key
@@ -70,7 +76,7 @@ __device__ __forceinline__ Sequence sequence_at(const SeqParams& p, int b, bool*
   Sequence s;
   s.len = p.seq_lens[b];
   s.n = p.new_lens != nullptr ? p.new_lens[b] : p.Nq;
-  if (s.len < 0 || s.len > p.capacity || s.n < 0 || s.n > p.Nq) {
+  if (s.len < 0 || s.len > p.capacity || s.n < 0 || s.n > p.Nq || (p.causal == kSeeTree && s.len < s.n)) {
     *bad = true;
     s.len = s.n = 0;
   }
@@ -90,17 +96,39 @@ __device__ __forceinline__ TileLimits tile_limits(const SeqParams& p, const Sequ
   TileLimits t;
   if (i0 > i1) {
     t.lim = t.full = 0;
-  } else if (p.causal) {
+  } else if (p.causal == kSeeCausal) {
     t.lim = max(0, s.len - s.n + i1 + 1);
     t.full = max(0, s.len - s.n + i0 + 1);
+  } else if (p.causal == kSeeTree) {
+    t.lim = s.len;
+    t.full = s.len - s.n;
   } else {
     t.lim = t.full = s.len;
   }
   return t;
 }
-// The keys that row r sees.
+// The keys that row r sees (of a tree: behind which it sees none).
 __device__ __forceinline__ int row_limit(const SeqParams& p, const Sequence& s, int r) {
-  return p.causal ? min(s.len, s.len - s.n + r / p.G + 1) : s.len;
+  return p.causal == kSeeCausal ? min(s.len, s.len - s.n + r / p.G + 1) : s.len;
+}
+
+// The mask row of token i of sequence b.
+__device__ __forceinline__ const uint32_t* tree_row(const FwdCacheParams& p, int b, int i) {
+  return p.tree + b * p.tree_batch + static_cast<long long>(i) * p.tree_words;
+}
+// Whether the row sees `key`, before the drafted tokens (from `base` on) or
+// among them; key < the sequence's length.
+__device__ __forceinline__ bool tree_sees(const uint32_t* row, int base, int key) {
+  return key < base || (row[(key - base) >> 5] >> ((key - base) & 31) & 1);
+}
+// What the row sees of the 32 keys from key0 on, a bit each; none from `end` on.
+__device__ __forceinline__ uint32_t tree_window(const uint32_t* row, int words, int base, int key0, int end) {
+  const int k = (key0 - base) >> 5;      // (rounds down: -1 and less stand before the drafted tokens)
+  const uint32_t lo = k < 0 ? ~0u : k < words ? row[k] : 0u;
+  const uint32_t hi = k + 1 < 0 ? ~0u : k + 1 < words ? row[k + 1] : 0u;
+  const uint32_t bits = __funnelshift_r(lo, hi, (key0 - base) & 31);
+  const int left = end - key0;
+  return left >= 32 ? bits : left <= 0 ? 0u : bits & ((1u << left) - 1u);
 }
 
 // Four e4m3 codes -> two f16x2.
@@ -426,5 +454,8 @@ cudaError_t launch_cache_merge(const FwdCacheParams& p, cudaStream_t stream) {
 int cache_prefill_rows(int d);
 cudaError_t launch_cache_prefill(const Cache& cache, FwdCacheParams& p, int sms,
                                  cudaStream_t stream);
+// The same with the mask of a tree (fa_cache_prefill_tree.cu).
+cudaError_t launch_cache_prefill_tree(const Cache& cache, FwdCacheParams& p, int sms,
+                                      cudaStream_t stream);
 
 }  // namespace fa

@@ -18,6 +18,7 @@
 
 #include <cuda_fp8.h>
 
+#include "cache_codes.cuh"
 #include "rope.cuh"
 
 namespace fa {
@@ -83,25 +84,6 @@ __device__ __forceinline__ uint2 to_codes(const float* x, float inv) {
     }
   }
   return make_uint2(w[0], w[1]);
-}
-
-// Sixteen codes for a scale `ratio` (<= 1) times their own.
-__device__ __forceinline__ uint4 rescaled(uint4 v, float ratio) {
-  uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t out = 0;
-    #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const __nv_fp8x2_storage_t two = static_cast<__nv_fp8x2_storage_t>(w[i] >> (16 * j));
-      const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(two, __NV_E4M3)));
-      out |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(
-                 make_float2(f.x * ratio, f.y * ratio), __NV_SATFINITE, __NV_E4M3))
-             << (16 * j);
-    }
-    w[i] = out;
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 __device__ __forceinline__ float finite_max(float m, const float (&x)[16]) {

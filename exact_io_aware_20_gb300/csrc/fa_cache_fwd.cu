@@ -38,8 +38,16 @@
 
 #include "cache_work.cuh"
 
+// 1: the kernels with the mask of a tree of drafted tokens (fa_cache_fwd_tree.cu
+// compiles this file a second time, so that the others carry none of it)
+#ifndef FA_CACHE_TREE
+#define FA_CACHE_TREE 0
+#endif
+
 namespace fa {
 namespace {
+
+constexpr bool kTree = FA_CACHE_TREE != 0;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
@@ -104,7 +112,8 @@ struct Smem {
   static constexpr int kStatOff = kBufOff + kBufBytes;     // (m, sum) [warp][row]
   static constexpr int kStatBytes = kWarps * 8 * NT * 8;
   static constexpr int kQsOff = kStatOff + kStatBytes;     // [row] power of two taken off q
-  static constexpr int kMetaOff = kQsOff + 8 * NT * 4;     // (ks, log2 vs, 2^-7 / vs) [warp][stage][page]
+  static constexpr int kTreeOff = kQsOff + 8 * NT * 4;     // [row] what it sees of the drafted tokens, a bit each
+  static constexpr int kMetaOff = kTreeOff + (kTree ? 8 * NT * 8 : 0);     // (ks, log2 vs, 2^-7 / vs) [warp][stage][page]
   static constexpr int kMetaBytes = kWarps * kStages * T::kSub * 16;
   static constexpr int kBarOff = kMetaOff + kMetaBytes;
   static constexpr int kMiscOff = kBarOff + kWarps * kStages * 8;
@@ -134,6 +143,7 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   uint2* q_frag = reinterpret_cast<uint2*>(smem + S::kQOff);
   float2* stat = reinterpret_cast<float2*>(smem + S::kStatOff);
   float* q_pow = reinterpret_cast<float*>(smem + S::kQsOff);
+  unsigned long long* tree = reinterpret_cast<unsigned long long*>(smem + S::kTreeOff);
   const uint32_t meta = base + S::kMetaOff + warp * kStages * T::kSub * 16;
   const uint32_t ring = base + warp * kStages * 2 * T::kBytes;
   const uint32_t bars = base + S::kBarOff + warp * kStages * 8;
@@ -283,6 +293,17 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
           w[c][1] = *reinterpret_cast<const uint4*>(src + 64 * c + 8);
         }
       }
+      if constexpr (kTree) {
+        // (this kernel's rows are those of 64 tokens at most: two words of each)
+        if (t == 0) {
+          unsigned long long bits = 0;
+          if (r < p.rows && r / p.seq.G < at.seq.n) {
+            const uint32_t* row = tree_row(p, b, r / p.seq.G);
+            bits = row[0] | (p.tree_words > 1 ? static_cast<unsigned long long>(row[1]) << 32 : 0ull);
+          }
+          tree[nt * 8 + g] = bits;
+        }
+      }
       float down = 1.f;
       if (p.bf16) {
         #pragma unroll
@@ -394,7 +415,13 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             if constexpr (PARTIAL) {
               const int r = row0 + nt * 8 + 2 * t + (k & 1);
               const int key = k0 + mt * 16 + key_of<D>(g) + (k >> 1) * 8;
-              if (key >= row_limit(p.seq, at.seq, r)) s[nt][k] = -INFINITY;
+              if constexpr (kTree) {
+                const int j = key - (at.seq.len - at.seq.n);
+                if (key >= at.seq.len || (j >= 0 && !(tree[nt * 8 + 2 * t + (k & 1)] >> j & 1)))
+                  s[nt][k] = -INFINITY;
+              } else {
+                if (key >= row_limit(p.seq, at.seq, r)) s[nt][k] = -INFINITY;
+              }
             }
           }
           grow |= fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + (kHead + kGrow) ||
@@ -726,15 +753,21 @@ void unit_shape(long long rows, int d, int sms, size_t* unit_rows, size_t* ctas)
 
 }  // namespace
 
+#if !FA_CACHE_TREE
 // Two pieces of a unit's rows for each CTA, and a record.
 size_t cache_fwd_workspace_bytes(int H, int Hkv, int Nq, int d, int sms) {
   size_t rows, ctas;
   unit_shape(1ll * H / Hkv * Nq, d, sms, &rows, &ctas);
   return 2 * ctas * rows * (d * sizeof(float) + sizeof(float2)) + ctas * sizeof(int4);
 }
+#endif
 
+#if FA_CACHE_TREE
+cudaError_t launch_cache_fwd_tree(const Cache& cache, const CacheFwdCall& c, int sms, cudaStream_t stream) {
+#else
 cudaError_t launch_cache_fwd(const Cache& cache, const CacheFwdCall& c, int sms,
                              cudaStream_t stream) {
+#endif
   FwdCacheParams p = {};
   p.seq = {c.seq_lens, c.new_lens, c.B, c.H / cache.Hkv, c.Nq, c.causal,
            static_cast<long long>(cache.width) * cache.page, c.err};
@@ -764,7 +797,15 @@ cudaError_t launch_cache_fwd(const Cache& cache, const CacheFwdCall& c, int sms,
   p.part_o = static_cast<float*>(c.workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + 2 * ctas * unit_rows * cache.d);
   p.joins = reinterpret_cast<int4*>(p.part_ml + 2 * ctas * unit_rows);
+#if FA_CACHE_TREE
+  p.seq.causal = kSeeTree;
+  p.tree = c.tree;
+  p.tree_words = (c.Nq + 31) / 32;
+  p.tree_batch = c.tree_batch > 1 ? 1ll * c.Nq * p.tree_words : 0;
+  if (many_rows(p.rows, cache.d)) return launch_cache_prefill_tree(cache, p, sms, stream);
+#else
   if (many_rows(p.rows, cache.d)) return launch_cache_prefill(cache, p, sms, stream);
+#endif
   const int nt = static_cast<int>(unit_rows / 8);
   switch (cache.d * 16 + nt) {
     case 64 * 16 + 1: return launch<64, 1>(cache, p, sms, stream);

@@ -57,8 +57,17 @@
 
 #include "cache_work.cuh"
 
+// 1: the kernels with the mask of a tree of drafted tokens
+// (fa_cache_prefill_tree.cu compiles this file a second time, so that the others
+// carry none of it)
+#ifndef FA_CACHE_TREE
+#define FA_CACHE_TREE 0
+#endif
+
 namespace fa {
 namespace {
+
+constexpr bool kTree = FA_CACHE_TREE != 0;
 
 constexpr int kThreads = 512;
 
@@ -850,15 +859,31 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (piece(np)->s1 < 0) break;
       const int end = piece(np)->end[u], full = piece(np)->full[u];
       int sees;       // the keys that this thread's row sees
+      const uint32_t* drafts = nullptr;      // (of a tree: its mask, and the first drafted token)
+      int base = 0;
       {
         const int r = piece(np)->row0 + 128 * u + r_tile;
         const Sequence seq = {piece(np)->len, piece(np)->n};
         sees = r < p.rows ? max(0, row_limit(p.seq, seq, r)) : 0;
+        if constexpr (kTree) {
+          // a row without a token of its own sees none
+          const int i = r / p.seq.G;
+          if (r >= p.rows || i >= seq.n) sees = 0;
+          drafts = tree_row(p, piece(np)->b, sees > 0 ? i : 0);
+          base = seq.len - seq.n;
+        }
       }
       float m = kNoMax, l = 0.f, row_scale = 0.f;
       for (int j = s0; j < end; ++j) {
         const int buf = L::kTiles == 2 ? u : cs & 1;
         const uint32_t tS = tmem + L::kTS + 128 * buf + lane_off;
+        uint32_t window[4] = {~0u, ~0u, ~0u, ~0u};
+        if constexpr (kTree) {
+          // (ahead of the scores, whose wait hides the loads)
+          if (j * 128 + 128 > full)
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) window[k] = tree_window(drafts, p.tree_words, base, j * 128 + 32 * k, sees);
+        }
         if (!wait_uniform(bar(L::kSFull + buf), (L::kTiles == 2 ? cs : cs >> 1) & 1, abort)) {
           ok = false;
           break;
@@ -877,7 +902,7 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
           const int lim = sees - j * 128;
           #pragma unroll
           for (int i = 0; i < 128; ++i)
-            if (i >= lim) s[i] = -INFINITY;
+            if (kTree ? !(window[i / 32] >> (i % 32) & 1) : i >= lim) s[i] = -INFINITY;
         }
         const uint32_t mt = sbase + L::kMetaOff + ((g + j - s0) & 7) * 128;
         float top = kNoMax;
@@ -980,6 +1005,9 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
           // NaN codes among the values that this row sees in tiles where the
           // conversion left them out (rare: a loop over those keys)
           for (int key = nan_from; in && key < nan_to; ++key) {
+            if constexpr (kTree) {
+              if (!tree_sees(drafts, base, key)) continue;
+            }
             int page = p.table[static_cast<long long>(b) * p.width + (key >> p.page_log2)];
             if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.pages)) page = 0;
             const uint32_t* row = reinterpret_cast<const uint32_t*>(
@@ -1080,10 +1108,14 @@ cudaError_t launch(const Cache& cache, FwdCacheParams& p, int sms, cudaStream_t 
 
 }  // namespace
 
+#if FA_CACHE_TREE
+cudaError_t launch_cache_prefill_tree(const Cache& cache, FwdCacheParams& p, int sms, cudaStream_t stream) {
+#else
 int cache_prefill_rows(int d) { return d == 256 ? Pre<256>::kRows : Pre<128>::kRows; }
 
 cudaError_t launch_cache_prefill(const Cache& cache, FwdCacheParams& p, int sms,
                                  cudaStream_t stream) {
+#endif
   switch (cache.d) {
     case 64: return launch<64>(cache, p, sms, stream);
     case 128: return launch<128>(cache, p, sms, stream);

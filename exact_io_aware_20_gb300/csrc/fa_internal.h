@@ -161,10 +161,49 @@ struct CacheFwdCall {
   const int *seq_lens, *new_lens;
   void* workspace;
   unsigned int* err;
+  const unsigned int* tree;   // the mask of a tree of drafted tokens, [tree_batch][Nq][words]
+  int tree_batch;
 };
 size_t cache_fwd_workspace_bytes(int H, int Hkv, int Nq, int d, int sms);
 cudaError_t launch_cache_fwd(const Cache& cache, const CacheFwdCall& c, int sms,
                              cudaStream_t stream);
+cudaError_t launch_cache_fwd_tree(const Cache& cache, const CacheFwdCall& c, int sms,
+                                  cudaStream_t stream);
+
+struct NormCall {
+  const void *q, *k;          // k nullptr: q only
+  const void *dq_out, *dk_out;   // backward
+  void *q_out, *k_out;        // backward: dq, dk
+  const void *q_weight, *k_weight;   // nullptr: ones
+  int weights_f32;
+  float eps, offset;
+  float *dq_weight, *dk_weight;
+  float* partial;             // backward's workspace
+  Strides qs, ks, dqs, dks, qos, kos;
+  int B, H, Hkv, N, d, bf16;
+};
+cudaError_t launch_qk_norm(const NormCall& c, const RopeArgs& r, int sms, cudaStream_t stream);
+cudaError_t launch_qk_norm_bwd(const NormCall& c, const RopeArgs& r, int sms, cudaStream_t stream);
+size_t qk_norm_bwd_workspace_bytes(int B, int heads, int N, int d, int sms);
+
+struct KeepCall {
+  int B, N, K;
+  const int *seq_lens, *new_lens, *keep, *keep_lens;
+  int* out_lens;
+  unsigned int* err;
+};
+cudaError_t launch_cache_keep(const Cache& cache, const KeepCall& c, int sms, cudaStream_t stream);
+
+struct ForkCall {
+  int B;
+  int *block_table, *refs;
+  const int *parents, *seq_lens, *reserve_lens;
+  int* out_lens;
+  void* workspace;
+  unsigned int* err;
+};
+size_t cache_fork_workspace_bytes(int B, int pages, int width);
+cudaError_t launch_cache_fork(const Cache& cache, const ForkCall& c, int sms, cudaStream_t stream);
 
 // C-ABI helpers: record a CUDA error's text (returns FA_ERR_CUDA); check that
 // the current device is an sm_103 part and get its error word; a caller's

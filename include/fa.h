@@ -415,6 +415,143 @@ int fa_fwd_cache(const void *q, const fa_cache *cache, void *o, float *lse, int 
 size_t fa_fwd_cache_workspace_size(int B, int H, int Hkv, int Nq, int d);
 
 /*
+ * Attention of a tree of drafted tokens over the cache: fa_fwd_cache for query
+ * rows that are the last new_lens[b] tokens of their sequence (NULL: all Nq),
+ * with a mask of their own among one another.  Row i of sequence b sees every
+ * token before those, and drafted token j (token seq_lens[b] - new_lens[b] + j)
+ * where bit j % 32 of word j / 32 of tree_mask[b][i] is set; rows and bits from
+ * new_lens[b] on are not looked at.  Nothing is implied: a row sees itself only
+ * where its own bit is set, and any set of bits is allowed (a row that sees no
+ * token gets O = 0 and L = -inf, as do rows from new_lens[b] on).  Sequences
+ * with fewer tokens than new_lens[b] count as empty and are reported as
+ * FA_ERR_CACHE, like other lengths out of range.
+ * tree_mask: device memory, [mask_batch][Nq][ceil(Nq / 32)] words, mask_batch 1
+ * (one tree for every sequence) or B.  Everything else (masked places, scales,
+ * strides, workspace of fa_fwd_cache_workspace_size bytes) as in fa_fwd_cache.
+ */
+int fa_fwd_cache_tree(const void *q, const fa_cache *cache, void *o, float *lse, int B, int H,
+                      int Nq, float scale, int dtype, const int *seq_lens, const int *new_lens,
+                      const unsigned int *tree_mask, int mask_batch, const fa_strides *strides,
+                      void *workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * Norms of queries and keys for each head, with the rotation in the same pass
+ * (no counterpart on the pages: what attention models apply to q and k ahead
+ * of the products).  A row x of d elements (one token of one head) becomes
+ *     turn(x * r * (offset + weight)),   r = 1 / sqrt(mean(x^2) + eps),
+ * where turn is the rotation of fa_rope; statistics, product and rotation in
+ * fp32, each result rounded once.  q_weight and k_weight: [d], one for every
+ * head of q and one for every head of k, of `dtype`, or fp32 where weights_f32
+ * is 1 (of both), 16-byte aligned; NULL: ones (and no offset).  eps: finite,
+ * at least 2^-100; offset: finite (0, or 1 for weights kept around zero).
+ * spec NULL: no rotation (positions and pos_batch are then not looked at).
+ * k may be NULL (k_out and k_weight then too).  strides[4]: of q, k, q_out,
+ * k_out.  Everything else as in fa_rope; an output may be its own input.
+ */
+int fa_qk_norm_rope(const void *q, const void *k, void *q_out, void *k_out, const void *q_weight,
+                    const void *k_weight, int weights_f32, float eps, float offset, int B, int H,
+                    int Hkv, int N, int d, int dtype, const fa_rope_spec *spec,
+                    const int *positions, int pos_batch, const fa_strides *strides,
+                    fa_stream_t stream);
+
+/*
+ * Its backward pass, from the gradients dq_out, dk_out of the results and the
+ * inputs q, k: with g the gradient turned back, h = x r and
+ * u = g (offset + weight),
+ *     dx = r (u - h mean(u h)),     dweight = sum over all rows of g h.
+ * dq, dk: 16-bit, `dtype`, rounded once; dq_weight, dk_weight: fp32 [d], either
+ * may be NULL (not wanted), and has to be where its weight is.  The statistics
+ * are formed again.  Sums over rows run in an order that depends on the sizes
+ * and the device's SM count alone: the same bits on every run.  strides[6]: of
+ * dq_out, dk_out, q, k, dq, dk (a NULL k: dk_out, dk and dk_weight too).  dq may
+ * be dq_out or q (same pointer and strides), dk likewise.  workspace: at least
+ * fa_qk_norm_rope_bwd_workspace_size(...) bytes for the current device, 256-byte
+ * aligned, contents on entry do not matter; not looked at where both weights'
+ * gradients are NULL.
+ */
+int fa_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *q, const void *k,
+                        void *dq, void *dk, const void *q_weight, const void *k_weight,
+                        int weights_f32, float eps, float offset, float *dq_weight,
+                        float *dk_weight, int B, int H, int Hkv, int N, int d, int dtype,
+                        const fa_rope_spec *spec, const int *positions, int pos_batch,
+                        const fa_strides *strides, void *workspace, size_t workspace_bytes,
+                        fa_stream_t stream);
+
+/* Bytes of workspace fa_qk_norm_rope_bwd needs on the current device (Hkv 0
+ * where k is NULL); 0 for invalid sizes. */
+size_t fa_qk_norm_rope_bwd_workspace_size(int B, int H, int Hkv, int N, int d);
+
+/*
+ * Keeps some of the last tokens of each sequence and drops the others (the
+ * accepted branch of a drafted tree; a prompt thinned to the tokens that
+ * matter).  Of the last new_lens[b] tokens of sequence b (NULL: N; at most N)
+ * those numbered keep[b][0] < keep[b][1] < ... < keep[b][keep_lens[b] - 1] move
+ * up to the front of them, for K and V and every head; out_lens[b] =
+ * seq_lens[b] - new_lens[b] + keep_lens[b].  keep: int32 [B][K], 1 <= K <= N;
+ * keep_lens: int32 [B], 0 <= keep_lens[b] <= K, NULL: all K.  out_lens must not
+ * be one of the inputs (every head reads those).  The block table does not
+ * change.
+ *
+ * A page that takes tokens has one scale for them: the largest of the scales
+ * that its tokens come with (its own among them when a token of the sequence
+ * that was in it is still there).  Codes that come with a smaller scale are
+ * rounded again for it (exact but for e4m3 subnormals where scales are powers
+ * of two).  Rows of a page behind the sequence's last token are left as they
+ * are.  Pages that hold the tokens in question must not be shared between
+ * sequences.
+ *
+ * A sequence with a length out of range (as in fa_cache_append, new_lens[b]
+ * above seq_lens[b] included), with keep_lens[b] out of range or with numbers
+ * that are not increasing or not below new_lens[b] keeps everything
+ * (out_lens[b] = seq_lens[b]); pages outside 0 .. pages - 1 are neither read nor
+ * written.  Either is reported by the next fa_get_device_status as FA_ERR_CACHE.
+ */
+int fa_cache_keep(const fa_cache *cache, int B, int N, int K, const int *seq_lens,
+                  const int *new_lens, const int *keep, const int *keep_lens, int *out_lens,
+                  fa_stream_t stream);
+
+/*
+ * Forks, reorders, ends and begins sequences over shared pages, and hands
+ * pages out: sequence b goes on from what was sequence parents[b] (-1: it
+ * begins empty; a sequence that is nobody's parent ends, and lets its pages
+ * go).  The cache's block_table is the table before the call; the table after
+ * it is written to block_table, which may be the same array or one of the same
+ * shape elsewhere.  Here a table row holds its sequence's pages and -1 (or
+ * another number out of range) behind them.  refs: int32 [pages], how many hold
+ * each page: table rows, and whoever else the caller counts (a page that
+ * prompts share, say); 0: the page is free.  Brought up to date.
+ *
+ * With L = seq_lens[parents[b]] (0 for -1) sequence b holds pages for
+ * max(L, reserve_lens[b]) tokens after the call (reserve_lens NULL: for L), and
+ * out_lens[b] = L (out_lens may be seq_lens):
+ *   - the L / page_size full pages of its parent, shared;
+ *   - from there on the parent's own places, where it is the first of the
+ *     parent's children (the lowest b) and nobody else held that page
+ *     (refs[page] == 1);
+ *   - at every other place a page whose count was 0 before the call, the
+ *     lowest numbers first, in the order of (b, place).  (Pages that this call
+ *     sets free can be had from the next one on.)
+ * Where the page in which token L will stand is not the parent's own, and
+ * L % page_size tokens are in it, those tokens' codes and the page's scales are
+ * copied; other rows of the new page are left as they are.
+ *
+ * Numbers out of range (parents[b] outside -1 .. B - 1: taken as -1; a length
+ * outside 0 .. table_width * page_size: taken as 0; a reserve above that: cut; a
+ * parent's page outside 0 .. pages - 1: the place gets -1, or a page without
+ * the copy) and a lack of free pages (places get -1) are reported by the next
+ * fa_get_device_status as FA_ERR_CACHE.  workspace: at least
+ * fa_cache_fork_workspace_size(...) bytes, 256-byte aligned, contents on entry
+ * do not matter.  Work on the same cache, table or counts has to be ordered by
+ * the caller.
+ */
+int fa_cache_fork(const fa_cache *cache, int *block_table, int *refs, int B, const int *parents,
+                  const int *seq_lens, const int *reserve_lens, int *out_lens, void *workspace,
+                  size_t workspace_bytes, fa_stream_t stream);
+
+/* Bytes of workspace fa_cache_fork needs; 0 for invalid sizes. */
+size_t fa_cache_fork_workspace_size(int B, int pages, int table_width);
+
+/*
  * Synchronises `stream`, then reports (and clears) what the device-side error
  * word holds: FA_ERR_TIMEOUT if a kernel gave up on a bounded wait,
  * FA_ERR_CACHE if a kernel met a page table entry or a sequence length out of

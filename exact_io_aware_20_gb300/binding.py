@@ -52,6 +52,7 @@ SIGNATURES = {
     "fa_fwd_cache_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "fa_fwd_cache_tree": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _f, _i, _vp, _vp, _vp, _i, _vp, _vp, _sz,
                                _vp]),
+    "fa_fwd_cache_tree_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "fa_qk_norm_rope": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _f, _f, _i, _i, _i, _i, _i, _i, _vp, _vp,
                              _i, _vp, _vp]),
     "fa_qk_norm_rope_bwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _f, _f, _vp, _vp, _i, _i, _i,
@@ -668,7 +669,7 @@ def forward_cache(q, cache: Cache, seq_lens, causal: bool, scale: float, new_len
                       new_lens, out, lse, workspace)
 
 
-def _forward_plan(cache, q, out):
+def _forward_plan(cache, q, out, size):
     if len(q[0]) != 4:
         raise ValueError("expected q [B, H, Nq, d]")
     B, H, Nq, d = q[0]
@@ -676,7 +677,7 @@ def _forward_plan(cache, q, out):
         raise ValueError(f"q{tuple(q[0])} does not fit a cache of {cache[0]} sequences, {cache[1]} heads, "
                          f"d {cache[2]} on device {cache[3]}")
     return (B, H, Nq, _code(q[2]), _L6(*_view(q, q[0], q[2], q[3], "q"), *_view(out, q[0], q[2], q[3], "out")),
-            fwd_cache_workspace_size(B, H, cache[1], Nq, d))
+            size(B, H, cache[1], Nq, d))
 
 
 def _lse(lse, B, H, Nq, cache):
@@ -701,7 +702,8 @@ def _scratch(workspace, ws_bytes, of):
 def _forward_cache(q, cache, seq_lens, causal, scale, new_lens, out, lse, workspace, stream):
     if out is None:
         out = torch.empty_like(q)
-    B, H, Nq, code, st, ws_bytes = _plan(_forward_plan, cache.key, _geometry(q), _geometry(out))
+    B, H, Nq, code, st, ws_bytes = _plan(_forward_plan, cache.key, _geometry(q), _geometry(out),
+                                         fwd_cache_workspace_size)
     device = cache.device_index
     lse = _lse(lse, B, H, Nq, cache)
     workspace, ws_bytes = _scratch(workspace, ws_bytes, cache)
@@ -713,7 +715,7 @@ def _forward_cache(q, cache, seq_lens, causal, scale, new_lens, out, lse, worksp
 
 
 def fwd_cache_workspace_size(B, H, Hkv, Nq, d) -> int:
-    """Bytes of workspace forward_cache and forward_cache_tree need on the current device."""
+    """Bytes of workspace forward_cache needs on the current device."""
     return int(load().fa_fwd_cache_workspace_size(B, H, Hkv, Nq, d))
 
 
@@ -738,6 +740,11 @@ def tree_mask(parents):
     return torch.where(mask >= 1 << 31, mask - (1 << 32), mask).to(torch.int32)
 
 
+def fwd_cache_tree_workspace_size(B, H, Hkv, Nq, d) -> int:
+    """Bytes of workspace forward_cache_tree needs on the current device."""
+    return int(load().fa_fwd_cache_tree_workspace_size(B, H, Hkv, Nq, d))
+
+
 def forward_cache_tree(q, cache: Cache, seq_lens, mask, scale: float, new_lens=None, out=None, lse=None,
                        workspace=None, stream=None):
     """(o, lse) of q [B, H, Nq, d], the last new_lens[b] tokens of each sequence
@@ -751,7 +758,8 @@ def forward_cache_tree(q, cache: Cache, seq_lens, mask, scale: float, new_lens=N
 def _forward_cache_tree(q, cache, seq_lens, mask, scale, new_lens, out, lse, workspace, stream):
     if out is None:
         out = torch.empty_like(q)
-    B, H, Nq, code, st, ws_bytes = _plan(_forward_plan, cache.key, _geometry(q), _geometry(out))
+    B, H, Nq, code, st, ws_bytes = _plan(_forward_plan, cache.key, _geometry(q), _geometry(out),
+                                         fwd_cache_tree_workspace_size)
     device = cache.device_index
     if (mask.dtype != torch.int32 or mask.dim() != 3 or mask.shape[0] not in (1, B) or mask.shape[1] != Nq
             or mask.shape[2] != -(-Nq // 32) or mask.get_device() != device or not mask.is_contiguous()):

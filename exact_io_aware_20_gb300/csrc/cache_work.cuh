@@ -303,13 +303,13 @@ struct Walk {
 // is over before the attention kernel's end, and a record would be one more
 // read behind it.
 constexpr int kMergeThreads = 128, kMergeRows = 4;
-template <int D, int RT, int STEP, int OVER, bool RECORDS>
+template <int D, int RT, int STEP, int OVER, bool RECORDS, int ROWS>
 __global__ void __launch_bounds__(kMergeThreads)
 cache_merge_kernel(const __grid_constant__ FwdCacheParams p) {
   constexpr int kVec = D / 32, kWarps = kMergeThreads / 32;
-  constexpr int kRows = RECORDS ? kMergeRows : 1;      // of a warp at a time
+  constexpr int kRows = ROWS;                          // of a warp at a time
   constexpr int kLanes = 32 / kRows;                   // that share out a row's pieces
-  constexpr int kPieces = RECORDS ? 1 : 4;             // whose O is in flight at once
+  constexpr int kPieces = ROWS > 1 ? 1 : 4;            // whose O is in flight at once
   __shared__ long long red[2 * kWarps];
   __shared__ longlong2 found;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -434,11 +434,20 @@ cache_merge_kernel(const __grid_constant__ FwdCacheParams p) {
 }
 
 // Launches the join behind the attention kernel, as its programmatic
-// dependent.
+// dependent.  With records, units of few rows (`rows` of them at most, not 0)
+// and many pieces have a row a warp.
 template <int D, int RT, int STEP, int OVER, bool RECORDS>
-cudaError_t launch_cache_merge(const FwdCacheParams& p, cudaStream_t stream) {
+cudaError_t launch_cache_merge(const FwdCacheParams& p, cudaStream_t stream, int rows = 0) {
+  constexpr int kWarps = kMergeThreads / 32;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.ctas), RECORDS ? RT / (kMergeThreads / 32 * kMergeRows) : RT > 8 ? RT / 8 : 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.ctas), RECORDS ? RT / (kWarps * kMergeRows) : RT > 8 ? RT / 8 : 1, 1);
+  auto kern = cache_merge_kernel<D, RT, STEP, OVER, RECORDS, RECORDS ? kMergeRows : 1>;
+  if constexpr (RECORDS) {
+    if (rows > 0) {
+      kern = cache_merge_kernel<D, RT, STEP, OVER, true, 1>;
+      cfg.gridDim.y = static_cast<unsigned>((rows + kWarps - 1) / kWarps);
+    }
+  }
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -446,7 +455,7 @@ cudaError_t launch_cache_merge(const FwdCacheParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_merge_kernel<D, RT, STEP, OVER, RECORDS>, p);
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 // The tcgen05 kernel, for many query rows (fa_cache_prefill.cu): rows of a

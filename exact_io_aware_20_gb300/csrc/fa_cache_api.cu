@@ -211,6 +211,11 @@ extern "C" size_t fa_fwd_cache_workspace_size(int B, int H, int Hkv, int Nq, int
   return fa::cache_fwd_workspace_bytes(H, Hkv, Nq, d, fa::device_sms());
 }
 
+extern "C" size_t fa_fwd_cache_tree_workspace_size(int B, int H, int Hkv, int Nq, int d) {
+  if (Hkv < 1 || fa::check_sizes(B, H, Nq, d, FA_BF16) != FA_OK || H % Hkv != 0) return 0;
+  return fa::cache_tree_workspace_bytes(H, Hkv, Nq, d, fa::device_sms());
+}
+
 namespace fa {
 namespace {
 
@@ -241,7 +246,8 @@ int attend(const void* q, const fa_cache* cache, void* o, float* lse, int B, int
   if (!workspace || !aligned(workspace, 256)) return FA_ERR_WORKSPACE;
   if ((st = check_device(&c.err)) != FA_OK) return st;
   const int sms = device_sms();
-  if (workspace_bytes < cache_fwd_workspace_bytes(H, ca.Hkv, Nq, ca.d, sms))
+  if (workspace_bytes < (tree != nullptr ? cache_tree_workspace_bytes(H, ca.Hkv, Nq, ca.d, sms)
+                                         : cache_fwd_workspace_bytes(H, ca.Hkv, Nq, ca.d, sms)))
     return FA_ERR_WORKSPACE;
   c.B = B;
   c.H = H;

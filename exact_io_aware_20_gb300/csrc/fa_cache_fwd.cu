@@ -740,8 +740,13 @@ namespace {
 // units of this file's kernel hold, at d = 256 than one.  Measured (B = 8,
 // 8 key/value heads, 8192 tokens), this kernel / the other: d = 64 at 64 rows
 // 57 / 63 us, at 128 rows 91 / 66; d = 128 at 32 rows 64 / 74, at 64 rows
-// 107 / 76; d = 256 at 8 rows 64 / 70, at 16 rows 103 / 71.
-bool many_rows(long long rows, int d) { return rows > (d == 256 ? 1 : 2) * most_rows(d); }
+// 107 / 76; d = 256 at 8 rows 64 / 70, at 16 rows 103 / 71.  A tree's rows, whose
+// many-row kernel shares one tile's keys out among its softmax groups: from more
+// rows than one unit holds (2 sequences of 60000 tokens, this kernel / the other:
+// d = 128 at 8 rows 63 / 66, 16 70 / 66, 32 91 / 67; d = 64 at 32 rows 63 / 58, 64
+// 106 / 59; 8 of 8192, d = 128 at 8 rows 39 / 45, 16 46 / 46; one of 1000, d = 128
+// at 8 rows 13 / 15, 28 15.5 / 15.4).
+bool many_rows(long long rows, int d) { return rows > (kTree || d == 256 ? 1 : 2) * most_rows(d); }
 
 // Rows of a unit, and CTAs at most.
 void unit_shape(long long rows, int d, int sms, size_t* unit_rows, size_t* ctas) {
@@ -753,14 +758,16 @@ void unit_shape(long long rows, int d, int sms, size_t* unit_rows, size_t* ctas)
 
 }  // namespace
 
-#if !FA_CACHE_TREE
 // Two pieces of a unit's rows for each CTA, and a record.
+#if FA_CACHE_TREE
+size_t cache_tree_workspace_bytes(int H, int Hkv, int Nq, int d, int sms) {
+#else
 size_t cache_fwd_workspace_bytes(int H, int Hkv, int Nq, int d, int sms) {
+#endif
   size_t rows, ctas;
   unit_shape(1ll * H / Hkv * Nq, d, sms, &rows, &ctas);
   return 2 * ctas * rows * (d * sizeof(float) + sizeof(float2)) + ctas * sizeof(int4);
 }
-#endif
 
 #if FA_CACHE_TREE
 cudaError_t launch_cache_fwd_tree(const Cache& cache, const CacheFwdCall& c, int sms, cudaStream_t stream) {

@@ -128,6 +128,23 @@ struct Pre {
   static_assert(256 + kTiles * D <= 512, "TMEM budget");
 };
 
+// With SPLIT a unit has 128 rows at most (few drafts of a tree), so that there is
+// no second tile of rows for the second softmax group.  The two groups take 64
+// keys of each tile instead, each with its own maximum, sum and O, the scores a
+// tile ahead in the other buffer; where a piece ends they join.  (100 rows, 8
+// sequences of 8192 tokens, 8 key/value heads, d = 128: 75 us with one group idle,
+// 55 with whole key tiles by turns, 51 so, 49 with a row a warp in the joins; the
+// values' codes by TMA through shared memory 55, not kept.)  The place of the
+// second tile of q holds what the groups exchange: both sides' (m, sum), a
+// barrier for when those are there and one for when every O has been read.
+template <int D>
+struct Split {
+  using L = Pre<D>;
+  static constexpr int kStatOff = L::kQOff + L::kQTile;     // [group][row]
+  static constexpr int kThere = kStatOff + 2 * 128 * 8, kRead = kThere + 8;
+  static_assert(L::kTiles == 1 || kRead + 8 <= L::kKOff, "the second tile's place");
+};
+
 template <int N>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -294,13 +311,18 @@ __device__ __forceinline__ void scale_o(uint32_t tO, float alpha) {
   tmem_st_wait();
 }
 
-// SEG: keys that share their scales for certain (a page's, 64 at most).
-template <int D, int SEG>
+// SEG: keys that share their scales for certain (a page's, 64 at most).  SPLIT:
+// one tile of rows, of whose keys each softmax group takes half.
+template <int D, int SEG, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ FwdCacheParams p) {
   using L = Pre<D>;
   using W = Walk<L::kRows, 128, L::kOver>;
+  static_assert(!SPLIT || L::kTiles == 2, "two softmax groups");
+  // rows of q that are converted (SPLIT: those that there are; what the others'
+  // scores come to reaches no row)
+  const int q_rows = SPLIT ? min(128, p.rows) : L::kRows;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -344,6 +366,11 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
       mbar_init(bar(L::kTileEmpty + s), 1);
     }
     mbar_init(bar(L::kDrain), 1);
+    if constexpr (SPLIT) {
+      const uint32_t there = sbase + Split<D>::kThere, read = sbase + Split<D>::kRead;
+      mbar_init(there, L::kSoftWarps);
+      mbar_init(read, L::kSoftWarps);
+    }
     *abort = 0;
     fence_barrier_init();
   }
@@ -390,7 +417,7 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
             int all = 0x7fffffff;
             #pragma unroll
             for (int u = 0; u < L::kTiles; ++u) {
-              const int r0 = row0 + 128 * u, r1 = min(p.rows, r0 + 128);
+              const int r0 = row0 + (SPLIT ? 0 : 128 * u), r1 = min(p.rows, r0 + 128);
               TileLimits t = {0, 0};
               if (r0 < r1) t = tile_limits(p.seq, at.seq, r0, r1);
               const int end = min(s1, (t.lim + 127) / 128);
@@ -518,7 +545,7 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
       // S (+)= part c of Q K^T of row tile u, into score buffer `buf`, from the
       // K piece in place s
       auto scores = [&](int u, int buf, int c, int s) {
-        uint64_t qs = desc_add(q_desc, u * L::kQTile + c * (128 * L::kKCols));
+        uint64_t qs = desc_add(q_desc, (SPLIT ? 0 : u * L::kQTile) + c * (128 * L::kKCols));
         const uint64_t ks = desc_add(k_desc, s * L::kKPiece);
         uint32_t more = c > 0;
         #pragma unroll 1
@@ -591,6 +618,41 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
               mma_commit(bar(L::kVEmpty + s));
             }
             if (!ok) break;
+            mma_commit(bar(L::kODone));
+            mma_commit(bar(L::kTileEmpty + (g & 7)));
+          }
+        } else if constexpr (SPLIT) {
+          // one row tile, its scores a tile ahead in the other buffer; P V of
+          // either half of the keys into an O of its own
+          auto next_scores = [&](int buf) -> bool {
+            if (!k_wait(kp)) return false;
+            tc_fence_after();
+            const int s = lane0(kp % L::kKStages);
+            scores(0, buf, 0, s);
+            mma_commit(bar(L::kKEmpty + s));
+            mma_commit(bar(L::kSFull + buf));
+            ++kp;
+            return true;
+          };
+          ok = next_scores(lane0(g & 1));
+          for (int j = w.s0; ok && j < w.s1; ++j, ++g, ++vp) {
+            if (j + 1 < w.s1) {
+              if (!next_scores(lane0((g + 1) & 1))) { ok = false; break; }
+            } else {
+              mma_commit(bar(L::kQEmpty));
+            }
+            ok = v_wait(vp);
+            if (!ok) break;
+            const int buf = lane0(g & 1), sv = lane0(vp % L::kVStages);
+            #pragma unroll 1
+            for (int u = 0; u < 2; ++u) {
+              if (!wait_uniform(bar(L::kPFull + u), g & 1, abort)) { ok = false; break; }
+              tc_fence_after();
+              mma_64_keys(tmem + L::kTO + D * u, tmem + L::kTS + 128 * buf + 64 * u,
+                          desc_add(v_desc, sv * L::kVPiece + u * (64 * 128)), kIdO, j > w.s0);
+            }
+            if (!ok) break;
+            mma_commit(bar(L::kVEmpty + sv));
             mma_commit(bar(L::kODone));
             mma_commit(bar(L::kTileEmpty + (g & 7)));
           }
@@ -732,11 +794,11 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
       // np - 3: eight flags.
       if (cw == 0 && lane == 0) nan_seen[(np + 1) & 7] = 0;
       #pragma unroll 1
-      for (int n = 8 * cw; n < L::kRows; n += 8 * L::kConvWarps) {
+      for (int n = 8 * cw; n < q_rows; n += 8 * L::kConvWarps) {
         uint4 x[2 * L::kChunks];
         #pragma unroll
         for (int k = 0; k < 2 * L::kChunks; ++k) x[k] = ahead[k];
-        if (n + 8 * L::kConvWarps < L::kRows) load_q(n + 8 * L::kConvWarps);
+        if (n + 8 * L::kConvWarps < q_rows) load_q(n + 8 * L::kConvWarps);
         uint32_t top = 0;    // of the magnitudes, two lanes of 16 bits
         #pragma unroll
         for (int k = 0; k < 2 * L::kChunks; ++k)
@@ -846,11 +908,14 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
   } else {
     // ------------------------------------------------------------ softmax
     more_registers<L::kRegSoft>();
-    const int u = warp >> 2;                      // row tile of this warpgroup
+    const int u = warp >> 2;                      // row tile of this warpgroup (SPLIT: half of the keys)
+    constexpr bool kOneTile = SPLIT || L::kTiles == 1;
+    constexpr int kHalf = SPLIT ? 64 : 0, kCols = SPLIT ? 64 : 128;
     const int r_tile = (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tO = tmem + L::kTO + (L::kTiles == 2 ? D * u : 0) + lane_off;
-    int cs = 0, od = 0;     // S_FULL phases (d = 256: tiles), O_DONE phases consumed
+    int cs = 0, od = 0;     // S_FULL phases (one tile of rows: tiles), O_DONE phases consumed
+    const uint32_t stat = sbase + Split<D>::kStatOff + 8 * r_tile;      // SPLIT: [group] of this row
     int g = 0;              // tiles of the CTA so far
     bool ok = true;
     for (int np = 0; ok; ++np) {
@@ -858,56 +923,65 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
       const int s0 = piece(np)->s0;
       if (piece(np)->s1 < 0) break;
       const int end = piece(np)->end[u], full = piece(np)->full[u];
-      int sees;       // the keys that this thread's row sees
-      const uint32_t* drafts = nullptr;      // (of a tree: its mask, and the first drafted token)
-      int base = 0;
-      {
+      int sees = 0;   // the keys that this thread's row sees
+      if constexpr (!kTree) {
         const int r = piece(np)->row0 + 128 * u + r_tile;
         const Sequence seq = {piece(np)->len, piece(np)->n};
         sees = r < p.rows ? max(0, row_limit(p.seq, seq, r)) : 0;
-        if constexpr (kTree) {
-          // a row without a token of its own sees none
-          const int i = r / p.seq.G;
-          if (r >= p.rows || i >= seq.n) sees = 0;
-          drafts = tree_row(p, piece(np)->b, sees > 0 ? i : 0);
-          base = seq.len - seq.n;
-        }
       }
+      // Of a tree: its mask row, the first drafted token and where the row's
+      // keys end, from the record each time (registers are short).
+      struct Drafts {
+        const uint32_t* row;
+        int base, end;
+      };
+      auto drafts_of = [&]() -> Drafts {
+        const volatile Piece* w = piece(np);
+        const int i = (w->row0 + (SPLIT ? 0 : 128 * u) + r_tile) / p.seq.G, n = w->n, len = w->len;
+        return {tree_row(p, w->b, i < n ? i : 0), len - n, i < n ? len : 0};
+      };
       float m = kNoMax, l = 0.f, row_scale = 0.f;
       for (int j = s0; j < end; ++j) {
-        const int buf = L::kTiles == 2 ? u : cs & 1;
-        const uint32_t tS = tmem + L::kTS + 128 * buf + lane_off;
-        uint32_t window[4] = {~0u, ~0u, ~0u, ~0u};
-        if constexpr (kTree) {
-          // (ahead of the scores, whose wait hides the loads)
-          if (j * 128 + 128 > full)
-            #pragma unroll
-            for (int k = 0; k < 4; ++k) window[k] = tree_window(drafts, p.tree_words, base, j * 128 + 32 * k, sees);
-        }
-        if (!wait_uniform(bar(L::kSFull + buf), (L::kTiles == 2 ? cs : cs >> 1) & 1, abort)) {
+        const int buf = kOneTile ? cs & 1 : u;
+        const uint32_t tS = tmem + L::kTS + 128 * buf + kHalf * u + lane_off;
+        if (!wait_uniform(bar(L::kSFull + buf), (kOneTile ? cs >> 1 : cs) & 1, abort)) {
           ok = false;
           break;
         }
         ++cs;
         tc_fence_after();
-        if (j == s0) row_scale = q_pow[(np & 1) * L::kRows + 128 * u + r_tile] * p.scale_log2;
-        uint32_t sr[128];
+        if (j == s0) {
+          const int r = (SPLIT ? 0 : 128 * u) + r_tile;
+          row_scale = !SPLIT || r < q_rows ? q_pow[(np & 1) * L::kRows + r] * p.scale_log2 : 0.f;
+        }
+        uint32_t sr[kCols];
         #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < kCols / 32; ++c)
           tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * c]));
         tmem_ld_wait();
         reg_fence(sr);
         float* s = reinterpret_cast<float*>(sr);
         if (j * 128 + 128 > full) {
-          const int lim = sees - j * 128;
-          #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (kTree ? !(window[i / 32] >> (i % 32) & 1) : i >= lim) s[i] = -INFINITY;
+          if constexpr (kTree) {
+            const Drafts d = drafts_of();
+            #pragma unroll
+            for (int k = 0; k < kCols / 32; ++k) {
+              const uint32_t w = tree_window(d.row, p.tree_words, d.base, j * 128 + kHalf * u + 32 * k, d.end);
+              #pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(w >> i & 1)) s[32 * k + i] = -INFINITY;
+            }
+          } else {
+            const int lim = sees - j * 128;
+            #pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (i >= lim) s[i] = -INFINITY;
+          }
         }
-        const uint32_t mt = sbase + L::kMetaOff + ((g + j - s0) & 7) * 128;
+        const uint32_t mt = sbase + L::kMetaOff + ((g + j - s0) & 7) * 128 + kHalf * u;
         float top = kNoMax;
         #pragma unroll
-        for (int c = 0; c < 128 / SEG; ++c) {
+        for (int c = 0; c < kCols / SEG; ++c) {
           float part[4];
           #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -933,11 +1007,11 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
         // well.  With scales by 16 keys ahead of the weights, which leaves more
         // registers to them (d = 128, pages of 16: 209.5 -> 197 us), otherwise
         // behind them (pages of 64: 176.5, ahead 178.7).
-        constexpr bool kScaleFirst = L::kTiles == 2 && SEG == 16;
+        constexpr bool kScaleFirst = !kOneTile && SEG == 16;
         if (kScaleFirst && any && j > s0) scale_o<D>(tO, alpha);
         // the weights over S as f16
         #pragma unroll
-        for (int seg = 0; seg < 128 / SEG; ++seg) {
+        for (int seg = 0; seg < kCols / SEG; ++seg) {
           const float4 sc = ld_shared_f4(mt + 16 * (SEG / 16) * seg);
           // (a product that underflows to 0 would make a masked score, -inf, NaN)
           const float ksr = fmaxf(row_scale * sc.x, 1.17549435e-38f), sub = sc.y - m;
@@ -960,7 +1034,7 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
           l = fmaf(all.x + all.y, sc.z, l);
         }
         tmem_st_wait();
-        if constexpr (L::kTiles == 1) {
+        if constexpr (kOneTile) {
           // P V of the tile before has to be done before O may be rescaled
           // (the scores waited for above were issued ahead of it)
           if (j > s0) {
@@ -970,19 +1044,46 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
           }
         }
         if (!kScaleFirst && any && j > s0) scale_o<D>(tO, alpha);
+        if constexpr (SPLIT) {
+          // P V over both groups' O of the piece before, which both have to have read
+          if (np > 0 && j == s0) {
+            if (!wait_uniform(sbase + Split<D>::kRead, (np - 1) & 1, abort)) { ok = false; break; }
+            tc_fence_after();
+          }
+        }
         tc_fence_before();
-        mbar_arrive_warp(bar(L::kPFull + buf));
+        mbar_arrive_warp(bar(L::kPFull + (SPLIT ? u : buf)));
       }
       if (!ok) break;
       // ---------------------------------------------------------- results
       const bool some = end > s0;     // the tile has keys in this piece
-      if (some) {
+      float of0 = 1.f, of1 = 0.f;     // SPLIT: the groups' O count so much
+      if constexpr (SPLIT) {
+        // (m, sum) to the other group
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(stat + 1024 * u), "f"(m), "f"(l) : "memory");
+        mbar_arrive_warp(sbase + Split<D>::kThere);
+        if (!wait_uniform(bar(L::kODone), od & 1, abort) ||
+            !wait_uniform(sbase + Split<D>::kThere, np & 1, abort)) {
+          ok = false;
+          break;
+        }
+        ++od;
+        tc_fence_after();
+        float m2, l2;
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(m2), "=f"(l2) : "r"(stat + 1024 * (u ^ 1)) : "memory");
+        const float top = fmaxf(m, m2), f = ex2_approx(m - top), f2 = ex2_approx(m2 - top);
+        // (a group that has no key for the row has nothing to add)
+        l = (l == 0.f ? 0.f : l * f) + (l2 == 0.f ? 0.f : l2 * f2);
+        m = top;
+        of0 = u == 0 ? f : f2;
+        of1 = u == 0 ? f2 : f;
+      } else if (some) {
         if (!wait_uniform(bar(L::kODone + (L::kTiles == 2 ? u : 0)), od & 1, abort)) { ok = false; break; }
         ++od;
         tc_fence_after();
       }
       const volatile Piece* w = piece(np);
-      const int r = w->row0 + 128 * u + r_tile, b = w->b, kh = w->h, s1 = w->s1;
+      const int r = w->row0 + (SPLIT ? 0 : 128 * u) + r_tile, b = w->b, kh = w->h, s1 = w->s1;
       const int i = r / p.seq.G, head = kh * p.seq.G + r % p.seq.G;
       const bool in = r < p.rows, whole = w->whole != 0;
       const float sum = (in && i < w->n) ? l : 0.f;
@@ -990,13 +1091,30 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
       const float inv = whole ? (sum == 0.f ? 0.f : kHeadInv / sum) : 1.f;
       // (a tile without keys in this piece may be here before the flag is reset)
       const bool nans = some && nan_seen[np & 7] != 0;
-      const int nan_from = max(s0, w->all / 128) * 128, nan_to = min(s1 * 128, sees);
+      Drafts drafts = {nullptr, 0, 0};
+      if constexpr (kTree) drafts = drafts_of();
+      const int nan_from = max(s0, w->all / 128) * 128, nan_to = min(s1 * 128, kTree ? drafts.end : sees);
       piece_done(np);
       auto write = [&](auto with_nans, int c) {
         uint32_t o[32];
         #pragma unroll
         for (int k = 0; k < 32; ++k) o[k] = 0u;
-        if (some) {
+        if constexpr (SPLIT) {
+          uint32_t o2[32];
+          const uint32_t t0 = tmem + L::kTO + lane_off + 32 * c;
+          tmem_ld32(t0, o);
+          tmem_ld32(t0 + D, o2);
+          tmem_ld_wait();
+          reg_fence(o);
+          reg_fence(o2);
+          #pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            // (an O that counts for nothing may be anything)
+            const float x = of0 == 0.f ? 0.f : __uint_as_float(o[k]) * of0;
+            const float y = of1 == 0.f ? 0.f : __uint_as_float(o2[k]) * of1;
+            o[k] = __float_as_uint(x + y);
+          }
+        } else if (some) {
           tmem_ld32(tO + 32 * c, o);
           tmem_ld_wait();
           reg_fence(o);
@@ -1006,7 +1124,7 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
           // conversion left them out (rare: a loop over those keys)
           for (int key = nan_from; in && key < nan_to; ++key) {
             if constexpr (kTree) {
-              if (!tree_sees(drafts, base, key)) continue;
+              if (!tree_sees(drafts.row, drafts.base, key)) continue;
             }
             int page = p.table[static_cast<long long>(b) * p.width + (key >> p.page_log2)];
             if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.pages)) page = 0;
@@ -1036,26 +1154,33 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
               dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           } else if (sum != 0.f) {
-            uint4* dst = reinterpret_cast<uint4*>(p.part_o + (slot * L::kRows + 128 * u + r_tile) * D + 32 * c);
+            uint4* dst = reinterpret_cast<uint4*>(
+                p.part_o + (slot * L::kRows + (SPLIT ? 0 : 128 * u) + r_tile) * D + 32 * c);
             #pragma unroll
             for (int k = 0; k < 8; ++k)
               dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
         }
       };
+      // (SPLIT: half of the columns each)
+      const int c0 = SPLIT ? D / 64 * u : 0, c1 = SPLIT ? D / 64 * (u + 1) : D / 32;
       if (nans) {     // (the same for the whole warp)
         #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) write(std::true_type{}, c);
+        for (int c = c0; c < c1; ++c) write(std::true_type{}, c);
       } else {
         #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) write(std::false_type{}, c);
+        for (int c = c0; c < c1; ++c) write(std::false_type{}, c);
       }
-      if (in) {
+      if (in && !(SPLIT && u == 1)) {
         if (whole)
           p.lse[(static_cast<long long>(b) * p.H + head) * p.seq.Nq + i] =
               sum == 0.f ? -INFINITY : (m + kHead + log2f(sum)) * kLogE2;
         else
-          p.part_ml[slot * L::kRows + 128 * u + r_tile] = make_float2(m, sum);
+          p.part_ml[slot * L::kRows + (SPLIT ? 0 : 128 * u) + r_tile] = make_float2(m, sum);
+      }
+      if constexpr (SPLIT) {
+        tc_fence_before();
+        mbar_arrive_warp(sbase + Split<D>::kRead);
       }
       tc_fence_before();   // O has been read out before the next P_FULL allows P V over it
       g += s1 - s0;
@@ -1072,13 +1197,13 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
   }
 }
 
-template <int D, int SEG>
+template <int D, int SEG, bool SPLIT>
 cudaError_t launch_seg(const Cache& cache, FwdCacheParams& p, int sms, cudaStream_t stream) {
   static std::atomic<bool> set[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  auto kern = cache_prefill_kernel<D, SEG>;
+  auto kern = cache_prefill_kernel<D, SEG, SPLIT>;
   if (!set[dev & 63]) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Pre<D>::kAlloc);
     if (e != cudaSuccess) return e;
@@ -1096,14 +1221,20 @@ cudaError_t launch_seg(const Cache& cache, FwdCacheParams& p, int sms, cudaStrea
   p.ctas = sms;
   kern<<<p.ctas, kThreads, Pre<D>::kAlloc, stream>>>(tk, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_cache_merge<D, Pre<D>::kRows, 128, Pre<D>::kOver, true>(p, stream);
+  return launch_cache_merge<D, Pre<D>::kRows, 128, Pre<D>::kOver, true>(p, stream, SPLIT ? p.rows : 0);
 }
 
 template <int D>
 cudaError_t launch(const Cache& cache, FwdCacheParams& p, int sms, cudaStream_t stream) {
-  return cache.page >= 64   ? launch_seg<D, 64>(cache, p, sms, stream)
-         : cache.page == 32 ? launch_seg<D, 32>(cache, p, sms, stream)
-                            : launch_seg<D, 16>(cache, p, sms, stream);
+  if constexpr (kTree && Pre<D>::kTiles == 2) {
+    if (p.rows <= 128)
+      return cache.page >= 64   ? launch_seg<D, 64, true>(cache, p, sms, stream)
+             : cache.page == 32 ? launch_seg<D, 32, true>(cache, p, sms, stream)
+                                : launch_seg<D, 16, true>(cache, p, sms, stream);
+  }
+  return cache.page >= 64   ? launch_seg<D, 64, false>(cache, p, sms, stream)
+         : cache.page == 32 ? launch_seg<D, 32, false>(cache, p, sms, stream)
+                            : launch_seg<D, 16, false>(cache, p, sms, stream);
 }
 
 }  // namespace

@@ -165,6 +165,7 @@ struct CacheFwdCall {
   int tree_batch;
 };
 size_t cache_fwd_workspace_bytes(int H, int Hkv, int Nq, int d, int sms);
+size_t cache_tree_workspace_bytes(int H, int Hkv, int Nq, int d, int sms);
 cudaError_t launch_cache_fwd(const Cache& cache, const CacheFwdCall& c, int sms,
                              cudaStream_t stream);
 cudaError_t launch_cache_fwd_tree(const Cache& cache, const CacheFwdCall& c, int sms,

@@ -427,12 +427,17 @@ size_t fa_fwd_cache_workspace_size(int B, int H, int Hkv, int Nq, int d);
  * FA_ERR_CACHE, like other lengths out of range.
  * tree_mask: device memory, [mask_batch][Nq][ceil(Nq / 32)] words, mask_batch 1
  * (one tree for every sequence) or B.  Everything else (masked places, scales,
- * strides, workspace of fa_fwd_cache_workspace_size bytes) as in fa_fwd_cache.
+ * strides) as in fa_fwd_cache, the workspace of at least
+ * fa_fwd_cache_tree_workspace_size(...) bytes.
  */
 int fa_fwd_cache_tree(const void *q, const fa_cache *cache, void *o, float *lse, int B, int H,
                       int Nq, float scale, int dtype, const int *seq_lens, const int *new_lens,
                       const unsigned int *tree_mask, int mask_batch, const fa_strides *strides,
                       void *workspace, size_t workspace_bytes, fa_stream_t stream);
+
+/* Bytes of workspace fa_fwd_cache_tree needs on the current device; 0 for
+ * invalid sizes. */
+size_t fa_fwd_cache_tree_workspace_size(int B, int H, int Hkv, int Nq, int d);
 
 /*
  * Norms of queries and keys for each head, with the rotation in the same pass

@@ -122,6 +122,8 @@ def test_workspace_sizes_of_invalid_sizes(lib):  # noqa: F811
     for args in ((0, 9, 4), (2, 0, 4), (2, 9, 0), (65536, 9, 4), (65535, 9, 40000)):
         assert lib.fa_cache_fork_workspace_size(*args) == 0
     assert lib.fa_cache_fork_workspace_size(2, 9, 4) > 0
+    for args in ((0, 4, 2, 1, 128), (1, 4, 3, 1, 128), (1, 4, 0, 1, 128), (1, 4, 2, 0, 128), (1, 4, 2, 1, 96)):
+        assert lib.fa_fwd_cache_tree_workspace_size(*args) == 0
     for args in ((0, 4, 2, 8, 64), (1, 0, 2, 8, 64), (1, 4, -1, 8, 64), (1, 4, 2, 0, 64), (1, 4, 2, 8, 80)):
         assert lib.fa_qk_norm_rope_bwd_workspace_size(*args) == 0
     assert lib.fa_qk_norm_rope_bwd_workspace_size(1, 4, 0, 8, 64) > 0

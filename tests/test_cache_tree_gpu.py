@@ -181,7 +181,7 @@ def test_graphs_that_run_together_and_the_same_bits(N):
         q = torch.randn(2, 8, N + i, 128, generator=g).bfloat16().to(DEV)
         mask = torch.stack([branch.pack(random_mask(N + i, g, "tree"), N + i) for _ in range(2)]).to(DEV)
         want = binding.forward_cache_tree(q, cache, n, mask, 0.1)
-        ws = torch.full((binding.fwd_cache_workspace_size(2, 8, 2, N + i, 128),), 0xFF, dtype=torch.uint8, device=DEV)
+        ws = torch.full((binding.fwd_cache_tree_workspace_size(2, 8, 2, N + i, 128),), 0xFF, dtype=torch.uint8, device=DEV)
         for x, y in zip(binding.forward_cache_tree(q, cache, n, mask, 0.1, workspace=ws), want):
             assert torch.equal(x, y)
         s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()

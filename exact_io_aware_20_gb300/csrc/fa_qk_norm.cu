@@ -6,6 +6,14 @@
 //     dw = sum over rows of turn_back(dy) h.
 // A row is D / 16 threads next to one another, a slot (8 pairs, as in rope.cuh)
 // each: its sums are shuffles among them, and every element is read once.
+//
+// What bounds it: memory (2 x 8192 tokens of 32 + 8 heads, d = 128, bf16:
+// forward, 2 bytes read and 2 written an element, 57 us, 5.9 TB/s, 87% of what a
+// copy reaches; backward, 4 read and 2 written, 85 us, as much), with the
+// arithmetic close behind: two lanes of fp32 an instruction (without 62 and 107
+// us).  Short calls: five tokens of four sequences forward 3.4 us; 4099 tokens of
+// 32 heads, d = 64, three axes, backward 20 us, of which the blocks' sums and the
+// kernel that adds them up are a quarter.
 #include <algorithm>
 
 #include "rope.cuh"
@@ -13,7 +21,7 @@
 namespace fa {
 namespace {
 
-constexpr int kNormThreads = 256;
+constexpr int kFwdThreads = 128, kNormThreads = 256;
 
 struct NormParams {
   // of q and of k
@@ -33,280 +41,349 @@ struct NormParams {
   RopeArgs r;
 };
 
-// A slot's 16 values x1[8], x2[8] as pairs (PAIRS: neighbours, also where the
-// slot does not turn) and back.
+// A slot's 16 values: x1 and x2 of its 8 pairs, two pairs at a time for the packed
+// arithmetic.  PAIRS: neighbours in memory (also where the slot does not turn),
+// otherwise x1 is the first chunk and x2 the second.
+struct Vals {
+  f2 a[4], b[4];
+};
 template <bool BF16, bool PAIRS>
-__device__ __forceinline__ void pack_slot(const float (&x1)[8], const float (&x2)[8], uint4& a, uint4& b) {
+__device__ __forceinline__ Vals unpack_vals(const uint4& u, const uint4& v) {
+  const uint32_t w[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+  Vals r;
+  #pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 lo = unpack2<BF16>(w[PAIRS ? 2 * k : k]), hi = unpack2<BF16>(w[PAIRS ? 2 * k + 1 : 4 + k]);
+    r.a[k] = PAIRS ? f2{lo.x, hi.x} : f2{lo.x, lo.y};
+    r.b[k] = PAIRS ? f2{lo.y, hi.y} : f2{hi.x, hi.y};
+  }
+  return r;
+}
+template <bool BF16, bool PAIRS>
+__device__ __forceinline__ void pack_vals(const Vals& r, uint4& u, uint4& v) {
   uint32_t w[8];
   #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[i] = PAIRS ? pack2<BF16>(x1[i], x2[i]) : pack2<BF16>(x1[2 * i], x1[2 * i + 1]);
-    w[4 + i] = PAIRS ? pack2<BF16>(x1[4 + i], x2[4 + i]) : pack2<BF16>(x2[2 * i], x2[2 * i + 1]);
+  for (int k = 0; k < 4; ++k) {
+    w[PAIRS ? 2 * k : k] = PAIRS ? pack2<BF16>(r.a[k].x, r.b[k].x) : pack2<BF16>(r.a[k].x, r.a[k].y);
+    w[PAIRS ? 2 * k + 1 : 4 + k] = PAIRS ? pack2<BF16>(r.a[k].y, r.b[k].y) : pack2<BF16>(r.b[k].x, r.b[k].y);
   }
-  a = make_uint4(w[0], w[1], w[2], w[3]);
-  b = make_uint4(w[4], w[5], w[6], w[7]);
+  u = make_uint4(w[0], w[1], w[2], w[3]);
+  v = make_uint4(w[4], w[5], w[6], w[7]);
+}
+__device__ __forceinline__ void scale_vals(Vals& r, float x) {
+  const f2 f = {x, x};
+  #pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    r.a[k] = fmul2(r.a[k], f);
+    r.b[k] = fmul2(r.b[k], f);
+  }
 }
 
-// The slot's weights with their offset, as x1 and x2 above.
+// The slot's weights with their offset.
 template <bool BF16, bool PAIRS>
-__device__ __forceinline__ void load_weights(const NormParams& p, const void* w, const Slot& at,
-                                             float (&w1)[8], float (&w2)[8]) {
+__device__ __forceinline__ Vals load_weights(const NormParams& p, const void* w, const Slot& at) {
+  Vals r;
   if (w == nullptr) {
     #pragma unroll
-    for (int j = 0; j < 8; ++j) w1[j] = w2[j] = 1.f;
-    return;
+    for (int k = 0; k < 4; ++k) r.a[k] = r.b[k] = f2{1.f, 1.f};
+    return r;
   }
   if (p.weights_f32) {
     const float* f = static_cast<const float*>(w);
     #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      w1[j] = PAIRS ? (j < 4 ? f[at.col_a + 2 * j] : f[at.col_b + 2 * j - 8]) : f[at.col_a + j];
-      w2[j] = PAIRS ? (j < 4 ? f[at.col_a + 2 * j + 1] : f[at.col_b + 2 * j - 7]) : f[at.col_b + j];
+    for (int k = 0; k < 4; ++k) {
+      const float* x = f + (PAIRS && k >= 2 ? at.col_b + 4 * k - 8 : at.col_a + (PAIRS ? 4 : 2) * k);
+      const float* y = f + at.col_b + 2 * k;
+      r.a[k] = PAIRS ? f2{x[0], x[2]} : f2{x[0], x[1]};
+      r.b[k] = PAIRS ? f2{x[1], x[3]} : f2{y[0], y[1]};
     }
   } else {
     const uint16_t* h = static_cast<const uint16_t*>(w);
-    unpack_slot<BF16>(*reinterpret_cast<const uint4*>(h + at.col_a),
-                      *reinterpret_cast<const uint4*>(h + at.col_b), PAIRS, w1, w2);
+    r = unpack_vals<BF16, PAIRS>(*reinterpret_cast<const uint4*>(h + at.col_a),
+                                 *reinterpret_cast<const uint4*>(h + at.col_b));
   }
+  const f2 off = {p.offset, p.offset};
   #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    w1[j] += p.offset;
-    w2[j] += p.offset;
+  for (int k = 0; k < 4; ++k) {
+    r.a[k] = fadd2(r.a[k], off);
+    r.b[k] = fadd2(r.b[k], off);
+  }
+  return r;
+}
+
+// cos and sin of the slot's pairs.
+__device__ __forceinline__ void load_angles(const RopeArgs& r, int slot, int b, int n, int N, f2 (&c)[4],
+                                            f2 (&s)[4]) {
+  int pos[4];
+  float x[8], y[8];
+  load_positions(r, b, n, N, n, pos);
+  slot_cos_sin(r, slot, pos, x, y);
+  #pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    c[k] = {x[2 * k], x[2 * k + 1]};
+    s[k] = {y[2 * k], y[2 * k + 1]};
   }
 }
 
 template <int SLOTS>
-__device__ __forceinline__ float row_sum(float x) {
+__device__ __forceinline__ float row_sum(f2 x) {
+  float y = x.x + x.y;
   #pragma unroll
-  for (int m = SLOTS / 2; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-  return x;
+  for (int m = SLOTS / 2; m > 0; m >>= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
+  return y;
+}
+template <int SLOTS>
+__device__ __forceinline__ float row_squares(const Vals& x) {
+  f2 s = {0.f, 0.f};
+  #pragma unroll
+  for (int k = 0; k < 4; ++k) s = ffma2(x.a[k], x.a[k], ffma2(x.b[k], x.b[k], s));
+  return row_sum<SLOTS>(s);
 }
 
 // bf16 rows whose squares leave fp32 are taken times this (eps is nothing to
 // them).
 constexpr float kDown = 8.470329472543003e-22f;   // 2^-70
 
-template <int SLOTS>
-__device__ __forceinline__ float row_squares(const float (&x1)[8], const float (&x2)[8]) {
-  float s[2] = {0.f, 0.f};
-  #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    s[0] = fmaf(x1[j], x1[j], s[0]);
-    s[1] = fmaf(x2[j], x2[j], s[1]);
-  }
-  return row_sum<SLOTS>(s[0] + s[1]);
-}
-
 // r of a row; where its squares leave fp32, the row and r are of x 2^-70 (*down
 // is that factor, 1 otherwise).
 template <int SLOTS>
-__device__ __forceinline__ float row_norm(float eps, float (&x1)[8], float (&x2)[8], float* down) {
-  float ss = row_squares<SLOTS>(x1, x2);
+__device__ __forceinline__ float row_norm(float eps, Vals& x, float* down) {
+  constexpr float kInf = 3.402823466e38f;
+  float ss = row_squares<SLOTS>(x);
   *down = 1.f;
-  if (__any_sync(0xffffffffu, !(ss < __uint_as_float(0x7f800000u)))) {   // (whole rows: no lane of one alone)
-    if (!(ss < __uint_as_float(0x7f800000u))) {
+  if (__any_sync(0xffffffffu, !(ss <= kInf))) {   // (whole rows: no lane of one alone)
+    if (!(ss <= kInf)) {
       *down = kDown;
-      #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x1[j] *= kDown;
-        x2[j] *= kDown;
-      }
+      scale_vals(x, kDown);
     }
-    ss = row_squares<SLOTS>(x1, x2);
+    ss = row_squares<SLOTS>(x);
   }
   return rsqrtf(fmaf(ss, 1.f / (16 * SLOTS), *down == 1.f ? eps : 0.f));
 }
 
-// A thread has one slot of one token, and up to heads_per heads of q or of k.
+// A thread has one slot of one token, and up to heads_per heads of q or of k, two
+// of them on their way.  (Blocks of 128 threads, six an SM: 57.3 us for the long
+// call above; 256 threads, three an SM 59.4, with four heads on their way 59.2,
+// two an SM 66.7.)
 template <bool BF16, int SLOTS, bool PAIRS>
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kFwdThreads, 6) norm_kernel(const __grid_constant__ NormParams p) {
   constexpr int kAhead = 2;
-  const long long item = static_cast<long long>(blockIdx.x) * kNormThreads + threadIdx.x;
+  const long long item = static_cast<long long>(blockIdx.x) * kFwdThreads + threadIdx.x;
   const bool on = item < p.items;       // (the same for a whole row)
   const int slot = static_cast<int>(item % SLOTS);
   const long long tok = on ? item / SLOTS : 0;
   const int b = static_cast<int>(tok / p.N), n = static_cast<int>(tok % p.N);
   const int which = static_cast<int>(blockIdx.y) >= p.groups_q;
   const int h0 = (blockIdx.y - (which ? p.groups_q : 0)) * p.heads_per;
-  const int h1 = min(p.heads[which], h0 + p.heads_per);
+  const int heads = min(p.heads[which], h0 + p.heads_per) - h0;
   const Slot at = slot_of(p.r, slot);
-  const Strides xs = p.xs[which], os = p.os[which];
-  const uint16_t* src = p.x[which] + b * xs.b + n * xs.n;
-  uint16_t* dst = p.out[which] + b * os.b + n * os.n;
+  const long long in_h = p.xs[which].h, out_h = p.os[which].h;
+  const uint16_t* src = p.x[which] + b * p.xs[which].b + n * p.xs[which].n + h0 * in_h;
+  uint16_t* dst = p.out[which] + b * p.os[which].b + n * p.os[which].n + h0 * out_h;
   uint4 ra[kAhead], rb[kAhead];
-  auto load = [&](int u, int h) {
+  auto load = [&](int u, int h) {       // (the heads one after another)
     ra[u] = rb[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (on && h < h1) {
-      ra[u] = *reinterpret_cast<const uint4*>(src + h * xs.h + at.col_a);
-      rb[u] = *reinterpret_cast<const uint4*>(src + h * xs.h + at.col_b);
+    if (on && h < heads) {
+      ra[u] = *reinterpret_cast<const uint4*>(src + at.col_a);
+      rb[u] = *reinterpret_cast<const uint4*>(src + at.col_b);
     }
+    src += in_h;
   };
   #pragma unroll
-  for (int u = 0; u < kAhead; ++u) load(u, h0 + u);
+  for (int u = 0; u < kAhead; ++u) load(u, u);
   // y1 = r (x1 w1 c - x2 w2 s), y2 = r (x2 w2 c + x1 w1 s)
-  float c1[8], c2[8], s1[8], s2[8];
-  load_weights<BF16, PAIRS>(p, p.weight[which], at, c1, c2);
+  Vals w = load_weights<BF16, PAIRS>(p, p.weight[which], at), ws;
   if (at.turns) {
-    int pos[4];
-    float c[8], s[8];
-    load_positions(p.r, b, n, p.N, n, pos);
-    slot_cos_sin(p.r, slot, pos, c, s);
+    f2 c[4], s[4];
+    load_angles(p.r, slot, b, n, p.N, c, s);
     #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      s1[j] = c1[j] * s[j];
-      s2[j] = c2[j] * s[j];
-      c1[j] *= c[j];
-      c2[j] *= c[j];
+    for (int k = 0; k < 4; ++k) {
+      ws.a[k] = fmul2(w.a[k], s[k]);
+      ws.b[k] = fmul2(w.b[k], f2{-s[k].x, -s[k].y});
+      w.a[k] = fmul2(w.a[k], c[k]);
+      w.b[k] = fmul2(w.b[k], c[k]);
     }
   }
-  for (int h = h0; h < h1; h += kAhead) {
+  for (int h = 0; h < heads; h += kAhead) {
     #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-      float x1[8], x2[8], down;
-      unpack_slot<BF16>(ra[u], rb[u], PAIRS, x1, x2);
+      Vals x = unpack_vals<BF16, PAIRS>(ra[u], rb[u]);
       load(u, h + u + kAhead);
-      const float r = row_norm<SLOTS>(p.eps, x1, x2, &down);
-      if (at.turns) {
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float y1 = fmaf(x1[j], c1[j], -(x2[j] * s2[j])), y2 = fmaf(x2[j], c2[j], x1[j] * s1[j]);
-          x1[j] = y1 * r;
-          x2[j] = y2 * r;
+      float down;
+      const float r = row_norm<SLOTS>(p.eps, x, &down);
+      #pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        f2 y = fmul2(x.a[k], w.a[k]), z = fmul2(x.b[k], w.b[k]);
+        if (at.turns) {
+          y = ffma2(x.b[k], ws.b[k], y);
+          z = ffma2(x.a[k], ws.a[k], z);
         }
-      } else {
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          x1[j] *= c1[j] * r;
-          x2[j] *= c2[j] * r;
-        }
+        x.a[k] = y;
+        x.b[k] = z;
       }
-      if (on && h + u < h1) {
+      scale_vals(x, r);
+      if (on && h + u < heads) {
         uint4 a, v;
-        pack_slot<BF16, PAIRS>(x1, x2, a, v);
-        *reinterpret_cast<uint4*>(dst + (h + u) * os.h + at.col_a) = a;
-        *reinterpret_cast<uint4*>(dst + (h + u) * os.h + at.col_b) = v;
+        pack_vals<BF16, PAIRS>(x, a, v);
+        *reinterpret_cast<uint4*>(dst + at.col_a) = a;
+        *reinterpret_cast<uint4*>(dst + at.col_b) = v;
       }
+      dst += out_h;
     }
   }
+}
+
+// 16 bytes to shared memory (zeros where `on` is false).
+__device__ __forceinline__ void copy_async_16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void copy_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // The backward pass.  Units (a tile of 256 / SLOTS tokens, one head), q's first,
 // tile by tile, are cut into equal shares, a block each; a thread keeps its
 // slot's angles while the tile stays, and its sums of the weights' gradients
 // until the block goes from q to k or ends: one partial sum a block, which
-// norm_sum_kernel adds up in a fixed order.
+// norm_sum_kernel adds up in a fixed order.  A thread's next kRing - 1 units are
+// on their way to shared memory of its own (no barrier between them; the long
+// call above with kRing 2 / 3 / 4 / 6 94 / 85.5 / 92 / 95.5 us, through registers
+// one unit ahead 104; three blocks an SM spill, 141).
+constexpr int kRing = 3;
 template <bool BF16, int SLOTS, bool PAIRS>
 __global__ void __launch_bounds__(kNormThreads, 2) norm_bwd_kernel(const __grid_constant__ NormParams p) {
   constexpr int kTokens = kNormThreads / SLOTS, D = 16 * SLOTS, kWarps = kNormThreads / 32;
+  extern __shared__ __align__(16) uint4 ring[];      // [kRing][x, x, dy, dy][thread]
   __shared__ float red[kWarps][D];
   const int tid = threadIdx.x, slot = tid % SLOTS;
   const Slot at = slot_of(p.r, slot);
   const long long units = p.tiles * (p.heads[0] + p.heads[1]);
   const long long lo = units * blockIdx.x / gridDim.x, hi = units * (blockIdx.x + 1) / gridDim.x;
+  const uint32_t mine = smem_u32(ring) + 16 * tid;
   grid_launch_dependents();
   #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     const int H = p.heads[which];
     const long long first = which ? p.tiles * p.heads[0] : 0;
     const long long u0 = max(lo, first) - first, u1 = min(hi, first + p.tiles * H) - first;
-    float d1[8], d2[8];
+    Vals dw;
     #pragma unroll
-    for (int j = 0; j < 8; ++j) d1[j] = d2[j] = 0.f;
+    for (int k = 0; k < 4; ++k) dw.a[k] = dw.b[k] = f2{0.f, 0.f};
     if (u0 < u1) {
-      const Strides xs = p.xs[which], dys = p.dys[which], os = p.os[which];
-      float w1[8], w2[8], c[8], s[8];
-      load_weights<BF16, PAIRS>(p, p.weight[which], at, w1, w2);
-      // the unit that is loaded next: its tile and head, and this thread's token
-      long long tile = u0 / H;
-      int h = static_cast<int>(u0 % H);
-      bool on = false;
-      const uint16_t *x = nullptr, *dy = nullptr;
-      uint16_t* out = nullptr;
-      int b = 0, n = 0;
-      auto enter = [&]() {
-        const long long tok = tile * kTokens + tid / SLOTS;
-        on = tok * SLOTS < p.items;
-        b = on ? static_cast<int>(tok / p.N) : 0;
-        n = on ? static_cast<int>(tok % p.N) : 0;
-        x = p.x[which] + b * xs.b + n * xs.n;
-        dy = p.dy[which] + b * dys.b + n * dys.n;
-        out = p.out[which] + b * os.b + n * os.n;
+      const Vals w = load_weights<BF16, PAIRS>(p, p.weight[which], at);
+      f2 c[4], s[4];
+      // this thread's token of a tile; false where there is none (then the first)
+      auto token = [&](int tile, int* b, int* n) -> bool {
+        const long long tok = static_cast<long long>(tile) * kTokens + tid / SLOTS;
+        const bool on = tok * SLOTS < p.items;
+        *b = on ? static_cast<int>(tok / p.N) : 0;
+        *n = on ? static_cast<int>(tok % p.N) : 0;
+        return on;
       };
-      uint4 next[4];
-      auto load = [&]() {
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) next[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (on) {
-          next[0] = *reinterpret_cast<const uint4*>(x + h * xs.h + at.col_a);
-          next[1] = *reinterpret_cast<const uint4*>(x + h * xs.h + at.col_b);
-          next[2] = *reinterpret_cast<const uint4*>(dy + h * dys.h + at.col_a);
-          next[3] = *reinterpret_cast<const uint4*>(dy + h * dys.h + at.col_b);
+      // the unit that is fetched next, and the one that is worked on
+      int f_tile = static_cast<int>(u0 / H), f_h = static_cast<int>(u0 % H), f_left = static_cast<int>(u1 - u0);
+      int tile = f_tile, h = f_h, left = f_left;
+      bool f_on = false;
+      const uint16_t *x = nullptr, *dy = nullptr;
+      auto enter = [&]() {
+        int b, n;
+        f_on = token(f_tile, &b, &n);
+        x = p.x[which] + b * p.xs[which].b + n * p.xs[which].n + f_h * p.xs[which].h;
+        dy = p.dy[which] + b * p.dys[which].b + n * p.dys[which].n + f_h * p.dys[which].h;
+      };
+      auto fetch = [&](int stage) {
+        if (f_left > 0) {
+          const uint32_t to = mine + stage * (4 * 16 * kNormThreads);
+          copy_async_16(to, x + at.col_a, f_on);
+          copy_async_16(to + 16 * kNormThreads, x + at.col_b, f_on);
+          copy_async_16(to + 32 * kNormThreads, dy + at.col_a, f_on);
+          copy_async_16(to + 48 * kNormThreads, dy + at.col_b, f_on);
+          x += p.xs[which].h;
+          dy += p.dys[which].h;
+          if (++f_h == H) {
+            f_h = 0;
+            ++f_tile;
+            if (f_left > 1) enter();
+          }
+          --f_left;
         }
+        copy_async_commit();
       };
       enter();
-      load();
-      bool fresh = true;       // the unit's tile is another than the last one's
-      for (long long u = u0; u < u1; ++u) {
-        float x1[8], x2[8], g1[8], g2[8];
-        unpack_slot<BF16>(next[0], next[1], PAIRS, x1, x2);
-        unpack_slot<BF16>(next[2], next[3], PAIRS, g1, g2);
-        uint16_t* dst = out + h * os.h;
-        const bool live = on;
-        if (fresh && at.turns) {
-          int pos[4];
-          load_positions(p.r, b, n, p.N, n, pos);
-          slot_cos_sin(p.r, slot, pos, c, s);
+      #pragma unroll
+      for (int i = 0; i < kRing - 1; ++i) fetch(i);
+      bool fresh = true, on = false;       // the unit's tile is another than the last one's
+      uint16_t* out = nullptr;
+      for (int stage = 0; left > 0; --left, stage = (stage + 1) % kRing) {
+        if (fresh) {
+          int b, n;
+          on = token(tile, &b, &n);
+          out = p.out[which] + b * p.os[which].b + n * p.os[which].n + h * p.os[which].h;
+          if (at.turns) load_angles(p.r, slot, b, n, p.N, c, s);
         }
+        copy_async_wait<kRing - 2>();
+        const uint4* in = ring + stage * (4 * kNormThreads) + tid;
+        Vals v = unpack_vals<BF16, PAIRS>(in[0], in[kNormThreads]);
+        Vals g = unpack_vals<BF16, PAIRS>(in[2 * kNormThreads], in[3 * kNormThreads]);
+        fetch((stage + kRing - 1) % kRing);
+        if (at.turns) {          // (the angles are turned round: p.r.inverse)
+          #pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const f2 a = g.a[k], o = g.b[k];
+            g.a[k] = ffma2(a, c[k], fmul2(o, f2{-s[k].x, -s[k].y}));
+            g.b[k] = ffma2(o, c[k], fmul2(a, s[k]));
+          }
+        }
+        float down;
+        const float r = row_norm<SLOTS>(p.eps, v, &down);
+        scale_vals(v, r);                                // h
+        f2 dot = {0.f, 0.f};
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          dw.a[k] = ffma2(g.a[k], v.a[k], dw.a[k]);
+          dw.b[k] = ffma2(g.b[k], v.b[k], dw.b[k]);
+          g.a[k] = fmul2(g.a[k], w.a[k]);                // u
+          g.b[k] = fmul2(g.b[k], w.b[k]);
+          dot = ffma2(g.a[k], v.a[k], ffma2(g.b[k], v.b[k], dot));
+        }
+        const float mean = row_sum<SLOTS>(dot) * (-1.f / D), f = r * down;
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          g.a[k] = ffma2(v.a[k], f2{mean, mean}, g.a[k]);
+          g.b[k] = ffma2(v.b[k], f2{mean, mean}, g.b[k]);
+        }
+        scale_vals(g, f);
+        if (on) {
+          uint4 a, o;
+          pack_vals<BF16, PAIRS>(g, a, o);
+          *reinterpret_cast<uint4*>(out + at.col_a) = a;
+          *reinterpret_cast<uint4*>(out + at.col_b) = o;
+        }
+        out += p.os[which].h;
         fresh = ++h == H;
         if (fresh) {
           h = 0;
           ++tile;
-          if (u + 1 < u1) enter();
-        }
-        if (u + 1 < u1) load();
-        if (at.turns) turn_pairs(g1, g2, c, s);      // (the angles are turned round: p.r.inverse)
-        float down;
-        const float r = row_norm<SLOTS>(p.eps, x1, x2, &down);
-        float dot[2] = {0.f, 0.f};
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          x1[j] *= r;                                // h
-          x2[j] *= r;
-          d1[j] = fmaf(g1[j], x1[j], d1[j]);
-          d2[j] = fmaf(g2[j], x2[j], d2[j]);
-          g1[j] *= w1[j];                            // u
-          g2[j] *= w2[j];
-          dot[0] = fmaf(g1[j], x1[j], dot[0]);
-          dot[1] = fmaf(g2[j], x2[j], dot[1]);
-        }
-        const float mean = row_sum<SLOTS>(dot[0] + dot[1]) * (1.f / D), f = r * down;
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          g1[j] = fmaf(-x1[j], mean, g1[j]) * f;
-          g2[j] = fmaf(-x2[j], mean, g2[j]) * f;
-        }
-        if (live) {
-          uint4 a, v;
-          pack_slot<BF16, PAIRS>(g1, g2, a, v);
-          *reinterpret_cast<uint4*>(dst + at.col_a) = a;
-          *reinterpret_cast<uint4*>(dst + at.col_b) = v;
         }
       }
     }
     if (p.partial != nullptr) {
       #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < 8; ++j) {
+        float a = j & 1 ? dw.a[j / 2].y : dw.a[j / 2].x, o = j & 1 ? dw.b[j / 2].y : dw.b[j / 2].x;
         #pragma unroll
         for (int m = SLOTS; m < 32; m <<= 1) {
-          d1[j] += __shfl_xor_sync(0xffffffffu, d1[j], m);
-          d2[j] += __shfl_xor_sync(0xffffffffu, d2[j], m);
+          a += __shfl_xor_sync(0xffffffffu, a, m);
+          o += __shfl_xor_sync(0xffffffffu, o, m);
         }
-      if ((tid & 31) < SLOTS) {
-        #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int a = PAIRS ? (j < 4 ? at.col_a + 2 * j : at.col_b + 2 * j - 8) : at.col_a + j;
-          red[tid >> 5][a] = d1[j];
-          red[tid >> 5][PAIRS ? a + 1 : at.col_b + j] = d2[j];
+        if ((tid & 31) < SLOTS) {
+          const int col = PAIRS ? (j < 4 ? at.col_a + 2 * j : at.col_b + 2 * j - 8) : at.col_a + j;
+          red[tid >> 5][col] = a;
+          red[tid >> 5][PAIRS ? col + 1 : at.col_b + j] = o;
         }
       }
       __syncthreads();
@@ -398,15 +475,16 @@ int bwd_blocks(int B, int heads, int N, int d, int sms) {
 cudaError_t launch_qk_norm(const NormCall& c, const RopeArgs& r, int sms, cudaStream_t stream) {
   NormParams p;
   fill(c, r, &p);
+  // heads of a thread: as in launch_rope
   const int heads = c.H + c.Hkv;
   const long long want = 1024ll * sms;
   const long long groups = std::max(1ll, std::min(std::min<long long>(heads, 4096), want / p.items));
   p.heads_per = std::min(16, static_cast<int>((heads + groups - 1) / groups));
   p.groups_q = (c.H + p.heads_per - 1) / p.heads_per;
-  const dim3 grid(static_cast<unsigned>((p.items + kNormThreads - 1) / kNormThreads),
+  const dim3 grid(static_cast<unsigned>((p.items + kFwdThreads - 1) / kFwdThreads),
                   static_cast<unsigned>(p.groups_q + (c.Hkv + p.heads_per - 1) / p.heads_per), 1);
   return by_type(c, r, [&](auto bf16, auto slots, auto pairs) -> cudaError_t {
-    norm_kernel<bf16.value, slots.value, pairs.value><<<grid, kNormThreads, 0, stream>>>(p);
+    norm_kernel<bf16.value, slots.value, pairs.value><<<grid, kFwdThreads, 0, stream>>>(p);
     return cudaGetLastError();
   });
 }
@@ -421,7 +499,11 @@ cudaError_t launch_qk_norm_bwd(const NormCall& c, const RopeArgs& r, int sms, cu
   p.tiles = bwd_tiles(c.B, c.N, c.d);
   const int blocks = bwd_blocks(c.B, c.H + c.Hkv, c.N, c.d, sms);
   cudaError_t e = by_type(c, r, [&](auto bf16, auto slots, auto pairs) -> cudaError_t {
-    norm_bwd_kernel<bf16.value, slots.value, pairs.value><<<blocks, kNormThreads, 0, stream>>>(p);
+    auto kern = norm_bwd_kernel<bf16.value, slots.value, pairs.value>;
+    constexpr int smem = kRing * 4 * 16 * kNormThreads;
+    const cudaError_t e2 = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e2 != cudaSuccess) return e2;
+    kern<<<blocks, kNormThreads, smem, stream>>>(p);
     return cudaGetLastError();
   });
   if (e != cudaSuccess || c.partial == nullptr) return e;

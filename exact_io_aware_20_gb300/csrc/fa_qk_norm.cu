@@ -41,6 +41,36 @@ struct NormParams {
   RopeArgs r;
 };
 
+// The columns of a slot: two chunks of eight, so that the chunks that the threads
+// of a row read at a time lie next to one another (two chunks next to one another
+// a thread are half sectors each: 4099 tokens of 32 heads, d = 64, interleaved,
+// backward 20 us instead of REPLACE).  Half-split: chunk b is the other half of
+// chunk a's pairs, or both do not turn.  Interleaved: four pairs in each.
+struct NormSlot {
+  int col_a, col_b;
+  int pair_a, pair_b;        // the first pair of a chunk (half-split: of both)
+  bool turn_a, turn_b;
+};
+template <int D, bool PAIRS>
+__device__ __forceinline__ NormSlot norm_slot(const RopeArgs& r, int slot) {
+  NormSlot s;
+  if constexpr (PAIRS) {
+    s.col_a = 8 * slot;
+    s.col_b = D / 2 + 8 * slot;
+    s.pair_a = 4 * slot;
+    s.pair_b = D / 4 + 4 * slot;
+    s.turn_a = s.col_a < 2 * r.pairs;
+    s.turn_b = s.col_b < 2 * r.pairs;
+  } else {
+    const int turning = r.pairs >> 3, still = slot - turning;
+    s.turn_a = s.turn_b = still < 0;
+    s.col_a = still < 0 ? 8 * slot : 2 * r.pairs + 8 * still;
+    s.col_b = still < 0 ? r.pairs + 8 * slot : r.pairs + D / 2 + 8 * still;
+    s.pair_a = s.pair_b = 8 * slot;
+  }
+  return s;
+}
+
 // A slot's 16 values: x1 and x2 of its 8 pairs, two pairs at a time for the packed
 // arithmetic.  PAIRS: neighbours in memory (also where the slot does not turn),
 // otherwise x1 is the first chunk and x2 the second.
@@ -81,7 +111,7 @@ __device__ __forceinline__ void scale_vals(Vals& r, float x) {
 
 // The slot's weights with their offset.
 template <bool BF16, bool PAIRS>
-__device__ __forceinline__ Vals load_weights(const NormParams& p, const void* w, const Slot& at) {
+__device__ __forceinline__ Vals load_weights(const NormParams& p, const void* w, const NormSlot& at) {
   Vals r;
   if (w == nullptr) {
     #pragma unroll
@@ -111,13 +141,23 @@ __device__ __forceinline__ Vals load_weights(const NormParams& p, const void* w,
   return r;
 }
 
-// cos and sin of the slot's pairs.
-__device__ __forceinline__ void load_angles(const RopeArgs& r, int slot, int b, int n, int N, f2 (&c)[4],
-                                            f2 (&s)[4]) {
+// cos and sin of the slot's pairs (1 and 0 of those that do not turn).
+template <bool PAIRS>
+__device__ __forceinline__ void load_angles(const RopeArgs& r, const NormSlot& at, int b, int n, int N,
+                                            f2 (&c)[4], f2 (&s)[4]) {
   int pos[4];
-  float x[8], y[8];
   load_positions(r, b, n, N, n, pos);
-  slot_cos_sin(r, slot, pos, x, y);
+  float x[8], y[8];
+  #pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    x[j] = 1.f;
+    y[j] = 0.f;
+    if (!(PAIRS && j >= 4 ? at.turn_b : at.turn_a)) continue;
+    const int pair = PAIRS && j >= 4 ? at.pair_b + j - 4 : at.pair_a + j, ax = r.axis[pair];
+    const int t = ax == 0 ? pos[0] : ax == 1 ? pos[1] : ax == 2 ? pos[2] : pos[3];
+    turn_cos_sin(static_cast<uint64_t>(static_cast<int64_t>(t)) * r.turn[pair], x[j], y[j]);
+    y[j] = r.inverse ? -y[j] : y[j];
+  }
   #pragma unroll
   for (int k = 0; k < 4; ++k) {
     c[k] = {x[2 * k], x[2 * k + 1]};
@@ -176,7 +216,7 @@ __global__ void __launch_bounds__(kFwdThreads, 6) norm_kernel(const __grid_const
   const int which = static_cast<int>(blockIdx.y) >= p.groups_q;
   const int h0 = (blockIdx.y - (which ? p.groups_q : 0)) * p.heads_per;
   const int heads = min(p.heads[which], h0 + p.heads_per) - h0;
-  const Slot at = slot_of(p.r, slot);
+  const NormSlot at = norm_slot<16 * SLOTS, PAIRS>(p.r, slot);
   const long long in_h = p.xs[which].h, out_h = p.os[which].h;
   const uint16_t* src = p.x[which] + b * p.xs[which].b + n * p.xs[which].n + h0 * in_h;
   uint16_t* dst = p.out[which] + b * p.os[which].b + n * p.os[which].n + h0 * out_h;
@@ -193,9 +233,9 @@ __global__ void __launch_bounds__(kFwdThreads, 6) norm_kernel(const __grid_const
   for (int u = 0; u < kAhead; ++u) load(u, u);
   // y1 = r (x1 w1 c - x2 w2 s), y2 = r (x2 w2 c + x1 w1 s)
   Vals w = load_weights<BF16, PAIRS>(p, p.weight[which], at), ws;
-  if (at.turns) {
+  if (at.turn_a) {       // (where chunk b turns, a does)
     f2 c[4], s[4];
-    load_angles(p.r, slot, b, n, p.N, c, s);
+    load_angles<PAIRS>(p.r, at, b, n, p.N, c, s);
     #pragma unroll
     for (int k = 0; k < 4; ++k) {
       ws.a[k] = fmul2(w.a[k], s[k]);
@@ -214,7 +254,7 @@ __global__ void __launch_bounds__(kFwdThreads, 6) norm_kernel(const __grid_const
       #pragma unroll
       for (int k = 0; k < 4; ++k) {
         f2 y = fmul2(x.a[k], w.a[k]), z = fmul2(x.b[k], w.b[k]);
-        if (at.turns) {
+        if (PAIRS && k >= 2 ? at.turn_b : at.turn_a) {
           y = ffma2(x.b[k], ws.b[k], y);
           z = ffma2(x.a[k], ws.a[k], z);
         }
@@ -260,7 +300,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_bwd_kernel(const __grid_
   extern __shared__ __align__(16) uint4 ring[];      // [kRing][x, x, dy, dy][thread]
   __shared__ float red[kWarps][D];
   const int tid = threadIdx.x, slot = tid % SLOTS;
-  const Slot at = slot_of(p.r, slot);
+  const NormSlot at = norm_slot<D, PAIRS>(p.r, slot);
   const long long units = p.tiles * (p.heads[0] + p.heads[1]);
   const long long lo = units * blockIdx.x / gridDim.x, hi = units * (blockIdx.x + 1) / gridDim.x;
   const uint32_t mine = smem_u32(ring) + 16 * tid;
@@ -274,7 +314,6 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_bwd_kernel(const __grid_
     #pragma unroll
     for (int k = 0; k < 4; ++k) dw.a[k] = dw.b[k] = f2{0.f, 0.f};
     if (u0 < u1) {
-      const Vals w = load_weights<BF16, PAIRS>(p, p.weight[which], at);
       f2 c[4], s[4];
       // this thread's token of a tile; false where there is none (then the first)
       auto token = [&](int tile, int* b, int* n) -> bool {
@@ -316,6 +355,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_bwd_kernel(const __grid_
       enter();
       #pragma unroll
       for (int i = 0; i < kRing - 1; ++i) fetch(i);
+      const Vals w = load_weights<BF16, PAIRS>(p, p.weight[which], at);
       bool fresh = true, on = false;       // the unit's tile is another than the last one's
       uint16_t* out = nullptr;
       for (int stage = 0; left > 0; --left, stage = (stage + 1) % kRing) {
@@ -323,16 +363,16 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_bwd_kernel(const __grid_
           int b, n;
           on = token(tile, &b, &n);
           out = p.out[which] + b * p.os[which].b + n * p.os[which].n + h * p.os[which].h;
-          if (at.turns) load_angles(p.r, slot, b, n, p.N, c, s);
+          if (at.turn_a) load_angles<PAIRS>(p.r, at, b, n, p.N, c, s);
         }
         copy_async_wait<kRing - 2>();
         const uint4* in = ring + stage * (4 * kNormThreads) + tid;
         Vals v = unpack_vals<BF16, PAIRS>(in[0], in[kNormThreads]);
         Vals g = unpack_vals<BF16, PAIRS>(in[2 * kNormThreads], in[3 * kNormThreads]);
         fetch((stage + kRing - 1) % kRing);
-        if (at.turns) {          // (the angles are turned round: p.r.inverse)
-          #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) {          // (the angles are turned round: p.r.inverse)
+          if (PAIRS && k >= 2 ? at.turn_b : at.turn_a) {
             const f2 a = g.a[k], o = g.b[k];
             g.a[k] = ffma2(a, c[k], fmul2(o, f2{-s[k].x, -s[k].y}));
             g.b[k] = ffma2(o, c[k], fmul2(a, s[k]));
@@ -371,7 +411,9 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_bwd_kernel(const __grid_
         }
       }
     }
-    if (p.partial != nullptr) {
+    if (p.partial != nullptr && u0 >= u1) {
+      if (tid < D) p.partial[(2ll * blockIdx.x + which) * D + tid] = 0.f;
+    } else if (p.partial != nullptr) {
       #pragma unroll
       for (int j = 0; j < 8; ++j) {
         float a = j & 1 ? dw.a[j / 2].y : dw.a[j / 2].x, o = j & 1 ? dw.b[j / 2].y : dw.b[j / 2].x;

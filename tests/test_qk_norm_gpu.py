@@ -72,7 +72,7 @@ def check_backward(got, dw, dy, x, w, eps, offset, turn, pairs, interleaved, ter
 
 def run(dtype, wtype, B, H, Hkv, N, d, interleaved, part, axes, offset, seed=0, size=1.0, eps=1e-6, given=True):
     g = torch.Generator().manual_seed(seed + B * N + d + axes)
-    pairs = d // 2 // part if part else 0
+    pairs = 0 if part == 0 else d // 2 // part if part < 8 else part       # (8 and more: how many)
     freq = [10000.0 ** (-i / max(1, pairs)) for i in range(pairs)]
     axis = [i * axes // max(1, pairs) for i in range(pairs)]
     table = binding.Rope(freq, axis, interleaved) if pairs else None
@@ -126,6 +126,12 @@ def test_matches_the_formulas(dtype, wtype, B, H, Hkv, N, d, interleaved, part):
 @pytest.mark.parametrize("wtype,offset", [(None, 0.0), ("f16", 1.0), ("f32", 1.0)])
 def test_axes_offsets_and_no_weights(d, Hkv, wtype, offset):
     run("f16", wtype, 2, 12, Hkv, 45, d, True, 1, 3, offset)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,pairs", [(64, 8), (64, 24), (128, 40), (128, 56), (256, 16), (256, 72), (256, 120)])
+def test_part_of_each_row_turned(interleaved, d, pairs):
+    run("bf16", "bf16", 2, 6, 2, 21, d, interleaved, pairs, 1, 0.0)
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])

@@ -17,14 +17,31 @@
 #include "fa_internal.h"
 #include "sm103_ptx.cuh"
 
+// 1: for the kernels with the mask of a tree of drafted tokens.  They are
+// compiled from the same sources as the others (fa_cache_fwd_tree.cu,
+// fa_cache_prefill_tree.cu), which so carry none of it; what differs lies in a
+// namespace of its own.
+#ifndef FA_CACHE_TREE
+#define FA_CACHE_TREE 0
+#endif
+
 namespace fa {
 
-// What the query rows of a sequence see of its tokens.
-enum : int { kSeeAll = 0, kSeeCausal = 1, kSeeTree = 2 };
+// The tcgen05 kernels, for many query rows (fa_cache_prefill.cu): rows of a unit.
+int cache_prefill_rows(int d);
+
+#if FA_CACHE_TREE
+#define FA_CACHE_NAMESPACE tree
+#else
+#define FA_CACHE_NAMESPACE plain
+#endif
+inline namespace FA_CACHE_NAMESPACE {
+
+constexpr bool kTree = FA_CACHE_TREE != 0;
 
 struct SeqParams {
   const int *seq_lens, *new_lens;
-  int B, G, Nq, causal;   // (causal: kSee...)
+  int B, G, Nq, causal;
   long long capacity;   // tokens that a table row can map
   unsigned int* err;
 };
@@ -48,7 +65,7 @@ struct FwdCacheParams {
   float2* part_ml;        // [CTA][2][RT]: its m (see kHead) and sum
   int4* joins;            // [CTA], the many-row kernel's: its unit that goes on behind its share
   int ctas;
-  const uint32_t* tree;   // kSeeTree: [1 or B][Nq][tree_words], bit j of row i: it sees drafted token j
+  const uint32_t* tree;   // of a tree: [1 or B][Nq][tree_words], bit j of row i: it sees drafted token j
   long long tree_batch;   // words from a sequence's to the next's
   int tree_words;
 };
@@ -76,10 +93,16 @@ __device__ __forceinline__ Sequence sequence_at(const SeqParams& p, int b, bool*
   Sequence s;
   s.len = p.seq_lens[b];
   s.n = p.new_lens != nullptr ? p.new_lens[b] : p.Nq;
-  if (s.len < 0 || s.len > p.capacity || s.n < 0 || s.n > p.Nq || (p.causal == kSeeTree && s.len < s.n)) {
+  if (s.len < 0 || s.len > p.capacity || s.n < 0 || s.n > p.Nq) {
     *bad = true;
     s.len = s.n = 0;
   }
+#if FA_CACHE_TREE
+  if (s.len < s.n) {
+    *bad = true;
+    s.len = s.n = 0;
+  }
+#endif
   return s;
 }
 
@@ -96,20 +119,20 @@ __device__ __forceinline__ TileLimits tile_limits(const SeqParams& p, const Sequ
   TileLimits t;
   if (i0 > i1) {
     t.lim = t.full = 0;
-  } else if (p.causal == kSeeCausal) {
+  } else if (p.causal) {
     t.lim = max(0, s.len - s.n + i1 + 1);
     t.full = max(0, s.len - s.n + i0 + 1);
-  } else if (p.causal == kSeeTree) {
-    t.lim = s.len;
-    t.full = s.len - s.n;
   } else {
     t.lim = t.full = s.len;
+#if FA_CACHE_TREE
+    t.full = s.len - s.n;      // (p.causal is 0)
+#endif
   }
   return t;
 }
-// The keys that row r sees (of a tree: behind which it sees none).
+// The keys that row r sees.
 __device__ __forceinline__ int row_limit(const SeqParams& p, const Sequence& s, int r) {
-  return p.causal == kSeeCausal ? min(s.len, s.len - s.n + r / p.G + 1) : s.len;
+  return p.causal ? min(s.len, s.len - s.n + r / p.G + 1) : s.len;
 }
 
 // The mask row of token i of sequence b.
@@ -442,7 +465,7 @@ cudaError_t launch_cache_merge(const FwdCacheParams& p, cudaStream_t stream, int
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.ctas), RECORDS ? RT / (kWarps * kMergeRows) : RT > 8 ? RT / 8 : 1, 1);
   auto kern = cache_merge_kernel<D, RT, STEP, OVER, RECORDS, RECORDS ? kMergeRows : 1>;
-  if constexpr (RECORDS) {
+  if constexpr (RECORDS && kTree) {
     if (rows > 0) {
       kern = cache_merge_kernel<D, RT, STEP, OVER, true, 1>;
       cfg.gridDim.y = static_cast<unsigned>((rows + kWarps - 1) / kWarps);
@@ -458,13 +481,10 @@ cudaError_t launch_cache_merge(const FwdCacheParams& p, cudaStream_t stream, int
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-// The tcgen05 kernel, for many query rows (fa_cache_prefill.cu): rows of a
-// unit, and its launch.
-int cache_prefill_rows(int d);
+// The launch of the many-row kernels.
 cudaError_t launch_cache_prefill(const Cache& cache, FwdCacheParams& p, int sms,
                                  cudaStream_t stream);
-// The same with the mask of a tree (fa_cache_prefill_tree.cu).
-cudaError_t launch_cache_prefill_tree(const Cache& cache, FwdCacheParams& p, int sms,
-                                      cudaStream_t stream);
+
+}  // namespace tree, plain
 
 }  // namespace fa

@@ -38,16 +38,8 @@
 
 #include "cache_work.cuh"
 
-// 1: the kernels with the mask of a tree of drafted tokens (fa_cache_fwd_tree.cu
-// compiles this file a second time, so that the others carry none of it)
-#ifndef FA_CACHE_TREE
-#define FA_CACHE_TREE 0
-#endif
-
 namespace fa {
 namespace {
-
-constexpr bool kTree = FA_CACHE_TREE != 0;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
@@ -805,14 +797,11 @@ cudaError_t launch_cache_fwd(const Cache& cache, const CacheFwdCall& c, int sms,
   p.part_ml = reinterpret_cast<float2*>(p.part_o + 2 * ctas * unit_rows * cache.d);
   p.joins = reinterpret_cast<int4*>(p.part_ml + 2 * ctas * unit_rows);
 #if FA_CACHE_TREE
-  p.seq.causal = kSeeTree;
   p.tree = c.tree;
   p.tree_words = (c.Nq + 31) / 32;
   p.tree_batch = c.tree_batch > 1 ? 1ll * c.Nq * p.tree_words : 0;
-  if (many_rows(p.rows, cache.d)) return launch_cache_prefill_tree(cache, p, sms, stream);
-#else
-  if (many_rows(p.rows, cache.d)) return launch_cache_prefill(cache, p, sms, stream);
 #endif
+  if (many_rows(p.rows, cache.d)) return launch_cache_prefill(cache, p, sms, stream);
   const int nt = static_cast<int>(unit_rows / 8);
   switch (cache.d * 16 + nt) {
     case 64 * 16 + 1: return launch<64, 1>(cache, p, sms, stream);

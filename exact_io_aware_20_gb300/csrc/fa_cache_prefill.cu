@@ -57,17 +57,8 @@
 
 #include "cache_work.cuh"
 
-// 1: the kernels with the mask of a tree of drafted tokens
-// (fa_cache_prefill_tree.cu compiles this file a second time, so that the others
-// carry none of it)
-#ifndef FA_CACHE_TREE
-#define FA_CACHE_TREE 0
-#endif
-
 namespace fa {
 namespace {
-
-constexpr bool kTree = FA_CACHE_TREE != 0;
 
 constexpr int kThreads = 512;
 
@@ -134,7 +125,9 @@ struct Pre {
 // tile ahead in the other buffer; where a piece ends they join.  (100 rows, 8
 // sequences of 8192 tokens, 8 key/value heads, d = 128: 75 us with one group idle,
 // 55 with whole key tiles by turns, 51 so, 49 with a row a warp in the joins; the
-// values' codes by TMA through shared memory 55, not kept.)  The place of the
+// values' codes by TMA through shared memory 55, not kept.  With one wait a tile
+// for the issuing warp a tile takes 0.95 us instead of 0.99: 24 rows of 4 ragged
+// sequences up to 131072 161 -> 156 us.)  The place of the
 // second tile of q holds what the groups exchange: both sides' (m, sum), a
 // barrier for when those are there and one for when every O has been read.
 template <int D>
@@ -144,6 +137,12 @@ struct Split {
   static constexpr int kThere = kStatOff + 2 * 128 * 8, kRead = kThere + 8;
   static_assert(L::kTiles == 1 || kRead + 8 <= L::kKOff, "the second tile's place");
 };
+
+// A unit's cost besides its steps, in steps (SPLIT, d = 128, 2 / 4 / 6 / 9 / 13: 100
+// rows of 8 x 8192 tokens 50.9 / 50.0 / 48.9 / 49.3 / 51.1 us, 32 rows of 64 ragged
+// ones up to 4000 102 / 93 / 92 / 93 / 94).
+template <int D, bool SPLIT>
+constexpr int unit_over() { return SPLIT ? 6 : Pre<D>::kOver; }
 
 template <int N>
 __device__ __forceinline__ void more_registers() {
@@ -169,6 +168,31 @@ __device__ __forceinline__ void load_16_if(uint4& x, const void* src, bool on) {
       "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
       : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
       : "l"(src), "r"(static_cast<uint32_t>(on)));
+}
+
+// Wait of a whole warp for a barrier a lane, bounded like mbar_wait.  By tests that
+// do not suspend the warp: suspended on one lane's barrier it is not woken by
+// another's (at a piece's ends that cost 8 us).
+__device__ __forceinline__ bool wait_each(uint32_t bar, uint32_t parity, volatile int* abort) {
+  uint64_t t0 = 0;
+  for (uint64_t round = 0;; ++round) {
+    #pragma unroll 1
+    for (int i = 0; i < 64; ++i) {
+      uint32_t done;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+      if (__all_sync(0xffffffffu, done != 0)) return true;
+    }
+    if (t0 == 0) t0 = globaltimer_ns();
+    const bool over = globaltimer_ns() - t0 > FA_WAIT_LIMIT_NS || round >= FA_WAIT_LIMIT_NS / 64;
+    if (__any_sync(0xffffffffu, over || *abort != 0)) {
+      if (*abort == 0) *abort = 2;
+      return false;
+    }
+  }
 }
 
 // Reads of shared memory by its own address: through a generic pointer they
@@ -318,7 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ FwdCacheParams p) {
   using L = Pre<D>;
-  using W = Walk<L::kRows, 128, L::kOver>;
+  constexpr int kOver = unit_over<D, SPLIT>();
+  using W = Walk<L::kRows, 128, kOver>;
   static_assert(!SPLIT || L::kTiles == 2, "two softmax groups");
   // rows of q that are converted (SPLIT: those that there are; what the others'
   // scores come to reaches no row)
@@ -376,7 +401,7 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
   }
   bool bad = false;
   long long lo = 0, hi = 0, share = 0;
-  find_place<L::kRows, 128, L::kOver, kThreads>(p, red, found, &bad, [&](long long count) {
+  find_place<L::kRows, 128, kOver, kThreads>(p, red, found, &bad, [&](long long count) {
     const long long total = count * p.Hkv;
     share = (total + p.ctas - 1) / p.ctas;
     lo = blockIdx.x * share;
@@ -622,39 +647,51 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
             mma_commit(bar(L::kTileEmpty + (g & 7)));
           }
         } else if constexpr (SPLIT) {
-          // one row tile, its scores a tile ahead in the other buffer; P V of
-          // either half of the keys into an O of its own
-          auto next_scores = [&](int buf) -> bool {
-            if (!k_wait(kp)) return false;
-            tc_fence_after();
+          // one row tile, its scores up to two tiles ahead in the two buffers; P V
+          // of either half of the keys into an O of its own
+          auto next_scores = [&](int buf) {
             const int s = lane0(kp % L::kKStages);
             scores(0, buf, 0, s);
             mma_commit(bar(L::kKEmpty + s));
             mma_commit(bar(L::kSFull + buf));
             ++kp;
-            return true;
           };
-          ok = next_scores(lane0(g & 1));
+          #pragma unroll 1
+          for (int i = 0; ok && i < min(2, w.s1 - w.s0); ++i) {
+            ok = k_wait(kp);
+            tc_fence_after();
+            if (ok) next_scores(lane0((g + i) & 1));
+          }
+          if (w.s1 - w.s0 <= 2) mma_commit(bar(L::kQEmpty));
           for (int j = w.s0; ok && j < w.s1; ++j, ++g, ++vp) {
-            if (j + 1 < w.s1) {
-              if (!next_scores(lane0((g + 1) & 1))) { ok = false; break; }
-            } else {
-              mma_commit(bar(L::kQEmpty));
+            // everything that the step needs in one wait, a barrier a lane: the
+            // tile's values, both groups' weights and the keys of the next but one
+            const bool next = j + 2 < w.s1;
+            const int sv = vp % L::kVStages, sk = kp % L::kKStages;
+            uint32_t on = bar(L::kVFull + sv);
+            int turn = vp / L::kVStages;
+            if (lane == 1 || lane == 2) {
+              on = bar(L::kPFull + lane - 1);
+              turn = g;
+            } else if (lane == 3 && next) {
+              on = bar(L::kKFull + sk);
+              turn = kp / L::kKStages;
             }
-            ok = v_wait(vp);
+            ok = wait_each(on, turn & 1, abort);
             if (!ok) break;
-            const int buf = lane0(g & 1), sv = lane0(vp % L::kVStages);
+            tc_fence_after();
+            const int buf = lane0(g & 1), from = lane0(sv);
             #pragma unroll 1
-            for (int u = 0; u < 2; ++u) {
-              if (!wait_uniform(bar(L::kPFull + u), g & 1, abort)) { ok = false; break; }
-              tc_fence_after();
+            for (int u = 0; u < 2; ++u)
               mma_64_keys(tmem + L::kTO + D * u, tmem + L::kTS + 128 * buf + 64 * u,
-                          desc_add(v_desc, sv * L::kVPiece + u * (64 * 128)), kIdO, j > w.s0);
-            }
-            if (!ok) break;
-            mma_commit(bar(L::kVEmpty + sv));
+                          desc_add(v_desc, from * L::kVPiece + u * (64 * 128)), kIdO, j > w.s0);
+            mma_commit(bar(L::kVEmpty + from));
             mma_commit(bar(L::kODone));
             mma_commit(bar(L::kTileEmpty + (g & 7)));
+            if (next) {
+              next_scores(buf);
+              if (j + 3 == w.s1) mma_commit(bar(L::kQEmpty));
+            }
           }
         } else {
           // two row tiles by turns, P V of a tile and its next scores together
@@ -1221,7 +1258,7 @@ cudaError_t launch_seg(const Cache& cache, FwdCacheParams& p, int sms, cudaStrea
   p.ctas = sms;
   kern<<<p.ctas, kThreads, Pre<D>::kAlloc, stream>>>(tk, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_cache_merge<D, Pre<D>::kRows, 128, Pre<D>::kOver, true>(p, stream, SPLIT ? p.rows : 0);
+  return launch_cache_merge<D, Pre<D>::kRows, 128, unit_over<D, SPLIT>(), true>(p, stream, SPLIT ? p.rows : 0);
 }
 
 template <int D>
@@ -1239,14 +1276,13 @@ cudaError_t launch(const Cache& cache, FwdCacheParams& p, int sms, cudaStream_t 
 
 }  // namespace
 
-#if FA_CACHE_TREE
-cudaError_t launch_cache_prefill_tree(const Cache& cache, FwdCacheParams& p, int sms, cudaStream_t stream) {
-#else
+#if !FA_CACHE_TREE
 int cache_prefill_rows(int d) { return d == 256 ? Pre<256>::kRows : Pre<128>::kRows; }
+#endif
 
+inline namespace FA_CACHE_NAMESPACE {
 cudaError_t launch_cache_prefill(const Cache& cache, FwdCacheParams& p, int sms,
                                  cudaStream_t stream) {
-#endif
   switch (cache.d) {
     case 64: return launch<64>(cache, p, sms, stream);
     case 128: return launch<128>(cache, p, sms, stream);
@@ -1254,5 +1290,6 @@ cudaError_t launch_cache_prefill(const Cache& cache, FwdCacheParams& p, int sms,
   }
   return cudaErrorInvalidValue;
 }
+}  // namespace tree, plain
 
 }  // namespace fa

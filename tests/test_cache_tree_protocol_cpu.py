@@ -47,26 +47,35 @@ class SplitModel(Model):
             def ahead(buf, j):
                 nonlocal kp
                 s = kp % self.k_stages
-                yield self.k_full[s], (kp // self.k_stages) & 1
                 self.scores(0, buf, n, j, 0, s)
                 self.commit(self.k_empty[s])
                 self.commit(self.s_full[buf])
                 kp += 1
 
-            yield from ahead(g & 1, s0)
+            for i in range(min(2, s1 - s0)):
+                yield self.k_full[kp % self.k_stages], (kp // self.k_stages) & 1
+                ahead((g + i) & 1, s0 + i)
+            if s1 - s0 <= 2:
+                self.commit(self.q_empty)
             for j in range(s0, s1):
-                if j + 1 < s1:
-                    yield from ahead((g + 1) & 1, j + 1)
-                else:
-                    self.commit(self.q_empty)
-                sv = vp % self.v_stages
-                yield self.v_full[sv], (vp // self.v_stages) & 1
+                more = j + 2 < s1
+                sv, sk = vp % self.v_stages, kp % self.k_stages
+                # (one wait of several lanes: each barrier's phase, in any order)
+                waits = [(self.v_full[sv], (vp // self.v_stages) & 1), (self.p_full[0], g & 1), (self.p_full[1], g & 1)]
+                if more:
+                    waits.append((self.k_full[sk], (kp // self.k_stages) & 1))
+                self.rng.shuffle(waits)
+                for x in waits:
+                    yield x
                 for u in range(2):
-                    yield self.p_full[u], g & 1
                     self.values(u, g & 1, n, j, 0, sv, j == s0)
                 self.commit(self.v_empty[sv])
                 self.commit(self.o_done[0])
                 self.commit(self.tile_empty[g & 7])
+                if more:
+                    ahead(g & 1, j + 2)
+                    if j + 3 == s1:
+                        self.commit(self.q_empty)
                 vp += 1
                 g += 1
 
@@ -146,7 +155,8 @@ def test_the_model_is_the_kernel_s():
         assert known["kQOff"] + known["kQTile"] + 2 * 128 * 8 + 16 <= known["kKOff"]
         assert known["kSoftWarps"] == 8
     for line in ("mbar_init(there, L::kSoftWarps)", "mbar_init(read, L::kSoftWarps)",
-                 "bar(L::kPFull + u), g & 1", "sbase + Split<D>::kRead, (np - 1) & 1",
+                 "on = bar(L::kPFull + lane - 1);", "turn = g;", "turn = kp / L::kKStages;", "int turn = vp / L::kVStages;",
+                 "wait_each(on, turn & 1, abort)", "sbase + Split<D>::kRead, (np - 1) & 1",
                  "bar(L::kODone), od & 1", "sbase + Split<D>::kThere, np & 1",
                  "bar(L::kSFull + buf), (kOneTile ? cs >> 1 : cs) & 1",
                  "static constexpr int kStatOff = L::kQOff + L::kQTile;",

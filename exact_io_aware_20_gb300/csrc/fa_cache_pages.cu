@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads) fork_plan_kernel(const __grid_consta
     if (fresh) {
       p.place[row + rank] = i;
       if (i == full && (len & page_mask) != 0) {
-        tail[0] = old;
+        tail[0] = old >= 0 ? old : ca.pages - 1;      // (out of range: any page that is there, and reported)
         tail[1] = rank;
       }
     }

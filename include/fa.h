@@ -542,8 +542,8 @@ int fa_cache_keep(const fa_cache *cache, int B, int N, int K, const int *seq_len
  *
  * Numbers out of range (parents[b] outside -1 .. B - 1: taken as -1; a length
  * outside 0 .. table_width * page_size: taken as 0; a reserve above that: cut; a
- * parent's page outside 0 .. pages - 1: the place gets -1, or a page without
- * the copy) and a lack of free pages (places get -1) are reported by the next
+ * parent's page outside 0 .. pages - 1: the place gets -1, or, where its tokens
+ * are copied, those of the last page) and a lack of free pages (places get -1) are reported by the next
  * fa_get_device_status as FA_ERR_CACHE.  workspace: at least
  * fa_cache_fork_workspace_size(...) bytes, 256-byte aligned, contents on entry
  * do not matter.  Work on the same cache, table or counts has to be ordered by

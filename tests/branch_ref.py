@@ -139,8 +139,8 @@ def fork(table, refs, parents, lens, reserve, page):
                 row[i] = old
             else:
                 row[i] = free.pop(0) if free else -1
-                if i == L // page and L % page and old >= 0 and row[i] >= 0:
-                    copies.append((old, row[i], L % page))
+                if i == L // page and L % page and parent >= 0 and row[i] >= 0:
+                    copies.append((old if old >= 0 else pages - 1, row[i], L % page))
             if row[i] >= 0:
                 now[row[i]] += 1
         seen.add(parent)

@@ -63,9 +63,12 @@ __device__ __forceinline__ uint4 for_scale(const uint4& v, float was, float now)
 // is written, and the pages' scales need no second copy.
 //
 // What bounds it: the dependent reads (lengths, numbers, table, codes) of a short
-// window (25 drafts of 64 sequences, 8 heads: 7 us) and of each run of a long one
-// (half of 2 x 16384 tokens, 8 heads, d = 128, 54 MB: REPLACE; with every run's
-// reads behind the writes of the one before 25 us).
+// window (25 drafts of 64 sequences, 8 heads: 5.2 us; of one 4.5) and of each run
+// of a long one (half of 2 x 16384 tokens, 8 heads, d = 128, 54 MB: 20 us, 40% of
+// what a copy reaches; with every run's reads behind the writes of the one before
+// 25 us).  Loops are left rolled: the code runs once or twice a launch, and its
+// instructions come from L2 (unrolled by four the drafts took 10.7 us instead of
+// 7.4).
 struct KeepParams {
   Cache cache;
   int page_log2, slots_log2;       // 16-byte slots of a row
@@ -217,8 +220,13 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
 // the row), and blocks of 8192 pages write down which of them are free, a bit
 // each.  The second writes: a block finds its sequence's free pages by the
 // numbers of those that the sequences before it take, brings the counts up to
-// date and copies the tokens of a page that is not full (several blocks a
-// sequence).
+// date, and others copy the tokens of a page that is not full.
+//
+// What bounds it: two kernels' dependent reads (32 sequences 6.7 us, 256 that
+// share whole pages only 8.4), and then the copies: 256 samples of 4 prompts, 28 MB
+// read and as much written, 18 us; of one prompt, 67 MB written, 25 us.  (A head
+// after another, one slot a thread at a time: 11.3 and 24 us.  More blocks or
+// slots a thread: the same.)
 constexpr int kChunkWords = 256;                 // of 32 pages
 
 struct ForkInfo {

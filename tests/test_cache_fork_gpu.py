@@ -188,6 +188,34 @@ def test_on_streams_and_in_a_graph():
     s.fork([0, 1, 1, 3], [5, 60, 60, 60], stream=side)
 
 
+def test_pages_far_apart():
+    """Byte offsets past 32 bits, heads and rows inside a wider buffer."""
+    d, page, Hkv, pages, apart = 64, 16, 2, 9, 1 << 29
+    g = torch.Generator().manual_seed(8)
+    codes = [torch.randint(0, 256, (pages, Hkv, page, d), generator=g, dtype=torch.uint8) for _ in range(2)]
+    scales = [torch.rand(pages, Hkv, generator=g) + 0.5 for _ in range(2)]
+    wide = torch.zeros(apart * (pages - 1) + 4 * Hkv * page * d, dtype=torch.uint8, device=DEV)
+    views = []
+    for i in (0, 1):
+        v = torch.as_strided(wide, (pages, Hkv, page, d), (apart, 2 * page * d, 2 * d, 1), i * d)
+        v.copy_(codes[i])
+        views.append(v)
+    table = [[7, 8, -1], [-1, -1, -1], [3, -1, -1]]
+    refs, lens, parents = [0, 1, 0, 1, 2, 2, 2, 1, 1], [27, 0, 16], [0, 0, 2]
+    cache = binding.Cache(*views, *(s.to(DEV) for s in scales), ints(table))
+    d_refs = ints(refs)
+    out = binding.cache_fork(cache, d_refs, ints(parents), ints(lens))
+    binding.device_status()
+    new, now, length, copies = branch.fork(table, refs, parents, lens, None, page)
+    assert out.tolist() == length and cache.tensors[4].tolist() == new and d_refs.tolist() == now
+    assert copies == [(8, 0, 11)]
+    for src, dst, rows in copies:
+        for i in (0, 1):
+            codes[i][dst, :, :rows], scales[i][dst] = codes[i][src, :, :rows], scales[i][src]
+    for i in (0, 1):
+        assert torch.equal(views[i].cpu(), codes[i]) and torch.equal(cache.tensors[2 + i].cpu(), scales[i])
+
+
 def test_refusals_of_the_binding():
     s = Server(64, 16, 1, 20, 2, 3)
     p, n = ints([0, 1]), ints([0, 0])

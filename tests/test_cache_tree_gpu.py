@@ -198,6 +198,13 @@ def test_graphs_that_run_together_and_the_same_bits(N):
         assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("N", [3, 30, 200])
+def test_a_batch_without_tokens(d, N):
+    run("bf16", d, 64, 4, 2, N, [0, 70, 0], new=[0, 0, 0])
+    run("bf16", d, 64, 4, 2, N, [0, N, 0], new=[0, N, 0], kind="any")
+
+
 def test_refusals_of_the_binding():
     c = torch.zeros(4, 2, 16, 64, dtype=torch.uint8, device=DEV)
     s = torch.ones(4, 2, device=DEV)

@@ -457,8 +457,10 @@ cache_merge_kernel(const __grid_constant__ FwdCacheParams p) {
 }
 
 // Launches the join behind the attention kernel, as its programmatic
-// dependent.  With records, units of few rows (`rows` of them at most, not 0)
-// and many pieces have a row a warp.
+// dependent.  With records, units of one tile of rows (`rows` of them at most, not
+// 0), which lie in many pieces, have a row a warp (a tree's 100 rows, d = 256, 2
+// sequences of 60000 tokens: 121 -> 114 us; with two tiles, 256 rows, d = 128, 8 of
+// 8192, 79 -> 82, so not there).
 template <int D, int RT, int STEP, int OVER, bool RECORDS>
 cudaError_t launch_cache_merge(const FwdCacheParams& p, cudaStream_t stream, int rows = 0) {
   constexpr int kWarps = kMergeThreads / 32;

@@ -1258,7 +1258,9 @@ cudaError_t launch_seg(const Cache& cache, FwdCacheParams& p, int sms, cudaStrea
   p.ctas = sms;
   kern<<<p.ctas, kThreads, Pre<D>::kAlloc, stream>>>(tk, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_cache_merge<D, Pre<D>::kRows, 128, unit_over<D, SPLIT>(), true>(p, stream, SPLIT ? p.rows : 0);
+  constexpr bool kOneTile = SPLIT || Pre<D>::kTiles == 1;
+  return launch_cache_merge<D, Pre<D>::kRows, 128, unit_over<D, SPLIT>(), true>(
+      p, stream, kTree && kOneTile ? std::min(p.rows, 128) : 0);
 }
 
 template <int D>

@@ -780,7 +780,7 @@ def cache_keep(cache: Cache, seq_lens, window: int, keep, keep_lens=None, new_le
     the most there may be) those numbered keep[b] [:keep_lens[b]] (None: all of
     keep's row), in increasing order, move to the front of them, in place; the
     new lengths are returned (fa_cache_keep).  keep: int32 [B, K]; out_lens is
-    allocated unless given, and must not be seq_lens."""
+    allocated unless given, and must not overlap an input."""
     return _on_stream(cache.device_index, stream, _cache_keep, cache, seq_lens, window, keep, keep_lens,
                       new_lens, out_lens)
 

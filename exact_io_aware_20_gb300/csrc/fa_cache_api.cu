@@ -302,6 +302,12 @@ int norm_args(NormCall* c, RopeArgs* r, int weights_f32, float eps, float offset
   return FA_OK;
 }
 
+// Whether n values at a and m at b, which may be missing, have none in common.
+bool apart(const int* a, long long n, const int* b, long long m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return b == nullptr || x + n * sizeof(int) <= y || y + m * sizeof(int) <= x;
+}
+
 // The lengths and the cache of fa_cache_keep and fa_cache_fork.
 int rows_args(const fa_cache* cache, int B, const int* seq_lens, int* out_lens, Cache* ca) {
   const int st = cache_args(cache, ca);
@@ -436,7 +442,9 @@ extern "C" int fa_cache_keep(const fa_cache* cache, int B, int N, int K, const i
   if (N < 1 || K < 1 || K > N || 1ll * B * K > INT_MAX || !keep || !fa::aligned(keep, 4) ||
       !fa::aligned(new_lens, 4) || !fa::aligned(keep_lens, 4))
     return FA_ERR_INVALID_ARG;
-  if (out_lens == seq_lens || out_lens == new_lens || out_lens == keep || out_lens == keep_lens)
+  // (a cluster's CTAs read the lengths each on its own: they have to find the same)
+  if (!fa::apart(out_lens, B, seq_lens, B) || !fa::apart(out_lens, B, new_lens, B) ||
+      !fa::apart(out_lens, B, keep, 1ll * B * K) || !fa::apart(out_lens, B, keep_lens, B))
     return FA_ERR_INVALID_ARG;
   fa::KeepCall c = {B, N, K, seq_lens, new_lens, keep, keep_lens, out_lens};
   if ((st = fa::check_device(&c.err)) != FA_OK) return st;
@@ -459,6 +467,8 @@ extern "C" int fa_cache_fork(const fa_cache* cache, int* block_table, int* refs,
   if (!block_table || !refs || !parents || !fa::aligned(block_table, 4) || !fa::aligned(refs, 4) ||
       !fa::aligned(parents, 4) || !fa::aligned(reserve_lens, 4))
     return FA_ERR_INVALID_ARG;
+  const long long entries = 1ll * B * ca.width;
+  if (block_table != ca.table && !fa::apart(block_table, entries, ca.table, entries)) return FA_ERR_INVALID_ARG;
   if (!workspace || !fa::aligned(workspace, 256) ||
       workspace_bytes < fa::cache_fork_workspace_bytes(B, ca.pages, ca.width))
     return FA_ERR_WORKSPACE;

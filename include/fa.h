@@ -494,7 +494,7 @@ size_t fa_qk_norm_rope_bwd_workspace_size(int B, int H, int Hkv, int N, int d);
  * up to the front of them, for K and V and every head; out_lens[b] =
  * seq_lens[b] - new_lens[b] + keep_lens[b].  keep: int32 [B][K], 1 <= K <= N;
  * keep_lens: int32 [B], 0 <= keep_lens[b] <= K, NULL: all K.  out_lens must not
- * be one of the inputs (every head reads those).  The block table does not
+ * overlap any of the inputs (every head reads those).  The block table does not
  * change.
  *
  * A page that takes tokens has one scale for them: the largest of the scales
@@ -521,7 +521,7 @@ int fa_cache_keep(const fa_cache *cache, int B, int N, int K, const int *seq_len
  * begins empty; a sequence that is nobody's parent ends, and lets its pages
  * go).  The cache's block_table is the table before the call; the table after
  * it is written to block_table, which may be the same array or one of the same
- * shape elsewhere.  Here a table row holds its sequence's pages and -1 (or
+ * shape that does not overlap it.  Here a table row holds its sequence's pages and -1 (or
  * another number out of range) behind them.  refs: int32 [pages], how many hold
  * each page: table rows, and whoever else the caller counts (a page that
  * prompts share, say); 0: the page is free.  Brought up to date.

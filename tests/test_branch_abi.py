@@ -79,6 +79,20 @@ def test_fork_rejects(lib, case, expect):  # noqa: F811
     assert fork(lib, **case) == expect
 
 
+@pytest.mark.parametrize("case", [
+    dict(out=FAKE + 4), dict(out=FAKE + 64 + 28), dict(out=FAKE + 60), dict(out=FAKE - 4), dict(new=FAKE + 132),
+    dict(keep_lens=FAKE + 124),
+])
+def test_keep_refuses_outputs_that_overlap_inputs(lib, case):  # noqa: F811
+    assert keep(lib, **case) == BAD
+
+
+@pytest.mark.parametrize("at", [4, -4, 4 * (2 * 8 - 1), -4 * (2 * 8 - 1)])
+def test_fork_refuses_tables_that_overlap(lib, at):  # noqa: F811
+    c = cache(table_width=8)
+    assert fork(lib, cache=c, table=c.block_table + at) == BAD
+
+
 def norm(lib, back, **kw):
     a = dict(q=FAKE, k=FAKE, qo=FAKE, ko=FAKE, dqo=FAKE, dko=FAKE, wq=FAKE, wk=FAKE, f32=0, eps=1e-6, offset=0.0, B=2,
              H=4, Hkv=2, N=8, d=64, dtype=1, spec=spec(), pos=FAKE, pos_batch=2, strides=None, dwq=FAKE, dwk=FAKE,

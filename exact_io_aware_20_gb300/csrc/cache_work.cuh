@@ -325,14 +325,14 @@ struct Walk {
 // 130; 10 with the records, 6 with four rows a warp).  With few rows the search
 // is over before the attention kernel's end, and a record would be one more
 // read behind it.
-constexpr int kMergeThreads = 128, kMergeRows = 4;
+constexpr int kMergeThreads = 128, kMergeRows = 4, kPairRows = 2;
 template <int D, int RT, int STEP, int OVER, bool RECORDS, int ROWS>
 __global__ void __launch_bounds__(kMergeThreads)
 cache_merge_kernel(const __grid_constant__ FwdCacheParams p) {
   constexpr int kVec = D / 32, kWarps = kMergeThreads / 32;
   constexpr int kRows = ROWS;                          // of a warp at a time
   constexpr int kLanes = 32 / kRows;                   // that share out a row's pieces
-  constexpr int kPieces = ROWS > 1 ? 1 : 4;            // whose O is in flight at once
+  constexpr int kPieces = ROWS > kPairRows ? 1 : 4;    // whose O is in flight at once
   __shared__ long long red[2 * kWarps];
   __shared__ longlong2 found;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -370,6 +370,78 @@ cache_merge_kernel(const __grid_constant__ FwdCacheParams p) {
       const int rr = first + own;
       const bool on = row0 + rr < p.rows;
       float top = kNoMax, sum = 0.f;
+      if constexpr (ROWS == kPairRows) {
+        // two rows of a block of eight: a lane has every second one's columns
+        // 4 (lane / 2) + 64 t, so that two lanes read a sector
+        constexpr int kPart = D / 64;
+        const int y = lane & 1, col4 = lane >> 1;
+        float4 acc[kPart];
+        #pragma unroll
+        for (int t = 0; t < kPart; ++t) acc[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = c0 + pl; on && c <= c1; c += kLanes)
+          top = fmaxf(top, p.part_ml[(2ll * c + (c == c0)) * RT + rr].x);
+        #pragma unroll
+        for (int x = kLanes / 2; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        for (int cb = c0; cb <= c1; cb += kLanes) {
+          float2 ml = make_float2(kNoMax, 0.f);
+          const int mine = cb + pl;
+          if (on && mine <= c1) ml = p.part_ml[(2ll * mine + (mine == c0)) * RT + rr];
+          const float w = ex2_approx(ml.x - top);
+          float part = ml.y == 0.f ? 0.f : ml.y * w;
+          #pragma unroll
+          for (int x = kLanes / 2; x > 0; x >>= 1) part += __shfl_xor_sync(0xffffffffu, part, x);
+          sum += part;
+          // a piece without keys for the row has left its O unwritten
+          const uint32_t has = __ballot_sync(0xffffffffu, ml.y != 0.f);
+          const int n = min(kLanes, c1 - cb + 1);
+          for (int k0 = 0; k0 < n; k0 += kPieces) {
+            float4 x[kPieces][kPart];
+            float wk[kPieces];
+            #pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+              const int c = cb + k0 + k, from = kLanes * y + ((k0 + k) & (kLanes - 1));
+              wk[k] = __shfl_sync(0xffffffffu, w, from);
+              const bool there = k0 + k < n && (has >> from & 1);
+              const float4* src = reinterpret_cast<const float4*>(
+                  p.part_o + ((2ll * c + (c == c0)) * RT + (first & ~7)) * D) + 8 * col4 + (first & 7) + y;
+              #pragma unroll
+              for (int t = 0; t < kPart; ++t) {
+                x[k][t] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (there) x[k][t] = src[8 * 16 * t];
+              }
+            }
+            #pragma unroll
+            for (int k = 0; k < kPieces; ++k)
+              #pragma unroll
+              for (int t = 0; t < kPart; ++t) {
+                acc[t].x = fmaf(x[k][t].x, wk[k], acc[t].x);
+                acc[t].y = fmaf(x[k][t].y, wk[k], acc[t].y);
+                acc[t].z = fmaf(x[k][t].z, wk[k], acc[t].z);
+                acc[t].w = fmaf(x[k][t].w, wk[k], acc[t].w);
+              }
+          }
+        }
+        if ((row0 + rr) / p.seq.G >= join.w) sum = 0.f;
+        const float total = __shfl_sync(0xffffffffu, sum, kLanes * y), m = __shfl_sync(0xffffffffu, top, kLanes * y);
+        const int r = row0 + first + y;
+        if (r < p.rows) {
+          const int i = r / p.seq.G, head = join.y * p.seq.G + r - i * p.seq.G;
+          const float inv = total == 0.f ? 0.f : kHeadInv / total;
+          uint2* dst = reinterpret_cast<uint2*>(p.o + b * p.os.b + head * p.os.h + i * p.os.n) + col4;
+          #pragma unroll
+          for (int t = 0; t < kPart; ++t) {
+            uint2 z = make_uint2(0u, 0u);
+            if (total != 0.f)
+              z = p.bf16 ? make_uint2(pack2<true>(acc[t].x * inv, acc[t].y * inv), pack2<true>(acc[t].z * inv, acc[t].w * inv))
+                         : make_uint2(pack2<false>(acc[t].x * inv, acc[t].y * inv), pack2<false>(acc[t].z * inv, acc[t].w * inv));
+            dst[16 * t] = z;
+          }
+          if (col4 == 0)
+            p.lse[(static_cast<long long>(b) * p.H + head) * p.seq.Nq + i] =
+                total == 0.f ? -INFINITY : (m + kHead + log2f(total)) * kLogE2;
+        }
+        continue;
+      }
       float acc[kRows][kVec];
       #pragma unroll
       for (int k = 0; k < kRows; ++k)
@@ -458,9 +530,12 @@ cache_merge_kernel(const __grid_constant__ FwdCacheParams p) {
 
 // Launches the join behind the attention kernel, as its programmatic
 // dependent.  With records, units of one tile of rows (`rows` of them at most, not
-// 0), which lie in many pieces, have a row a warp (a tree's 100 rows, d = 256, 2
-// sequences of 60000 tokens: 121 -> 114 us; with two tiles, 256 rows, d = 128, 8 of
-// 8192, 79 -> 82, so not there).
+// 0), which lie in many pieces, have two rows a warp, of results that lie in
+// blocks of eight rows [columns / 4][row][4]: the attention kernel's threads, a
+// row each, so write whole lines (a tree's 100 rows, 8 sequences of 8192 tokens,
+// d = 128: rows one behind another, four a warp 51 us, one 49, in blocks 47; d =
+// 256, 128 rows of 4 x 32768 136.3 -> 134.6; with two tiles, 256 rows, d = 128, 8
+// of 8192, one row a warp instead of four 79 -> 82, so not there).
 template <int D, int RT, int STEP, int OVER, bool RECORDS>
 cudaError_t launch_cache_merge(const FwdCacheParams& p, cudaStream_t stream, int rows = 0) {
   constexpr int kWarps = kMergeThreads / 32;
@@ -469,8 +544,8 @@ cudaError_t launch_cache_merge(const FwdCacheParams& p, cudaStream_t stream, int
   auto kern = cache_merge_kernel<D, RT, STEP, OVER, RECORDS, RECORDS ? kMergeRows : 1>;
   if constexpr (RECORDS && kTree) {
     if (rows > 0) {
-      kern = cache_merge_kernel<D, RT, STEP, OVER, true, 1>;
-      cfg.gridDim.y = static_cast<unsigned>((rows + kWarps - 1) / kWarps);
+      kern = cache_merge_kernel<D, RT, STEP, OVER, true, kPairRows>;
+      cfg.gridDim.y = static_cast<unsigned>((rows + kWarps * kPairRows - 1) / (kWarps * kPairRows));
     }
   }
   cfg.blockDim = dim3(kMergeThreads);

@@ -124,7 +124,7 @@ struct Pre {
 // keys of each tile instead, each with its own maximum, sum and O, the scores a
 // tile ahead in the other buffer; where a piece ends they join.  (100 rows, 8
 // sequences of 8192 tokens, 8 key/value heads, d = 128: 75 us with one group idle,
-// 55 with whole key tiles by turns, 51 so, 49 with a row a warp in the joins; the
+// 55 with whole key tiles by turns, 51 so, 47 with the joins of one tile; the
 // values' codes by TMA through shared memory 55, not kept.  With one wait a tile
 // for the issuing warp a tile takes 0.95 us instead of 0.99: 24 rows of 4 ragged
 // sequences up to 131072 161 -> 156 us.)  The place of the
@@ -1191,11 +1191,13 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
               dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           } else if (sum != 0.f) {
+            constexpr bool kBlocks = kTree && kOneTile;      // (launch_cache_merge)
             uint4* dst = reinterpret_cast<uint4*>(
-                p.part_o + (slot * L::kRows + (SPLIT ? 0 : 128 * u) + r_tile) * D + 32 * c);
+                kBlocks ? p.part_o + (slot * L::kRows + (r_tile & ~7)) * D + 256 * c + 4 * (r_tile & 7)
+                        : p.part_o + (slot * L::kRows + (SPLIT ? 0 : 128 * u) + r_tile) * D + 32 * c);
             #pragma unroll
             for (int k = 0; k < 8; ++k)
-              dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              dst[kBlocks ? 8 * k : k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
         }
       };

@@ -735,9 +735,11 @@ namespace {
 // 107 / 76; d = 256 at 8 rows 64 / 70, at 16 rows 103 / 71.  A tree's rows, whose
 // many-row kernel shares one tile's keys out among its softmax groups: from more
 // rows than one unit holds (2 sequences of 60000 tokens, this kernel / the other:
-// d = 128 at 8 rows 63 / 66, 16 70 / 66, 32 91 / 67; d = 64 at 32 rows 63 / 58, 64
-// 106 / 59; 8 of 8192, d = 128 at 8 rows 39 / 45, 16 46 / 46; one of 1000, d = 128
-// at 8 rows 13 / 15, 28 15.5 / 15.4).
+// d = 128 at 8 rows 59 / 63 us, 16 68 / 64, 32 91 / 64; d = 64 at 32 rows 60 / 59,
+// 64 106 / 60; 8 of 8192, d = 128 at 8 rows 39 / 43, 16 46 / 43; one of 1000, d =
+// 128 at 8 rows 13.4 / 13.7, 28 15.5 / 14.1).  16 rows at d = 128 go either way, by
+// how many units there are: one sequence of 16000 34 / 23, 64 ragged ones up to
+// 4000 81 / 92, of 1000 53 / 70; they stay here, where large batches are.
 bool many_rows(long long rows, int d) { return rows > (kTree || d == 256 ? 1 : 2) * most_rows(d); }
 
 // Rows of a unit, and CTAs at most.

@@ -4,6 +4,7 @@
 #include <algorithm>
 
 #include "cache_codes.cuh"
+#include "cache_keep.cuh"
 #include "fa_internal.h"
 #include "sm103_ptx.cuh"
 
@@ -104,9 +105,9 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
   const int kept = p.keep_lens != nullptr ? p.keep_lens[b] : p.K;
   const int* keep = p.keep + static_cast<long long>(b) * p.K;
   const bool first_cta = rank == 0 && h == 0 && key && tid == 0;
-  const int base = len - n, end = base + kept;
-  const bool valid = n >= 0 && n <= p.N && len >= n && kept >= 0 && kept <= p.K &&
-                     len <= (static_cast<long long>(ca.width) << p.page_log2);
+  const KeepWindow window = keep_window(len, n, kept, p.N, p.K, static_cast<long long>(ca.width) << p.page_log2);
+  const int base = window.base, end = window.end;
+  const bool valid = window.valid;
   if (!valid || kept == 0) {         // (the whole cluster)
     if (first_cta) {
       p.out_lens[b] = valid ? base : len;

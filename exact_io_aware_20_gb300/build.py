@@ -10,6 +10,7 @@ import concurrent.futures as cf
 import glob
 import os
 import platform
+import re
 import shutil
 import subprocess
 
@@ -41,6 +42,23 @@ def _stale(out: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def dependencies(src: str) -> set:
+    """The files that an object of `src` is made from: itself, and what it includes
+    by a quoted name (a kernel that is compiled twice is included as a .cu), in turn."""
+    seen, todo = set(), [src]
+    while todo:
+        path = todo.pop()
+        if path in seen:
+            continue
+        seen.add(path)
+        with open(path) as f:
+            names = re.findall(r'^[ \t]*#[ \t]*include[ \t]*"([^"]+)"', f.read(), re.M)
+        for name in names:
+            places = (os.path.join(d, name) for d in (os.path.dirname(path), CSRC, INCLUDE))
+            todo += [p for p in places if os.path.exists(p)][:1]
+    return seen
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     nvcc = nvcc_path()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -52,12 +70,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         with open(stamp, "w") as f:
             f.write(arch)
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    headers = glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(INCLUDE, "*.h"))
     jobs = []
     for src in sources:
         obj = os.path.join(BUILD_DIR, os.path.basename(src)[:-3] + ".o")
-        if force or _stale(obj, [src, __file__] + headers):
+        if force or _stale(obj, dependencies(src) | {__file__}):
             cmd = [nvcc] + common_flags(extra_flags) + ["-c", src, "-o", obj]
             if verbose:
                 cmd += ["-Xptxas", "-v"]

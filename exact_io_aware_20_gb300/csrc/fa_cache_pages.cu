@@ -87,8 +87,10 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
   extern __shared__ __align__(16) unsigned char keep_smem[];
   uint4* codes = reinterpret_cast<uint4*>(keep_smem);
   // Of two runs by turns: [row] where it comes from (nullptr: it is there already,
-  // or there is none) and the scale that it comes with (0: there is none); [page]
-  // the bits of its scale, and its number (-1: out of range)
+  // or there is none) and the scale that it comes with (below 0: there is none; 0 is
+  // a page of zeros, whose tokens are rounded for their new page's scale like any);
+  // [page] the bits of its scale (-1: no token of it is there), and its number (-1: out
+  // of range)
   const unsigned char** from_of =
       reinterpret_cast<const unsigned char**>(keep_smem + (static_cast<size_t>(p.rows) << (p.slots_log2 + 4)));
   float* scale_of = reinterpret_cast<float*>(from_of + 2 * p.rows);
@@ -148,7 +150,8 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
       const int tok = first + i, number = tok < base ? tok - base : keep[tok - base];
       const int from = number < n ? base + number : -1;      // (below 0: out of range)
       const int page = from >= 0 ? page_at(from) : -1;
-      const float scale = page >= 0 ? scales[static_cast<long long>(page) * ca.Hkv] : 0.f;
+      // (without its sign: -0, or a NaN's)
+      const float scale = page >= 0 ? fabsf(scales[static_cast<long long>(page) * ca.Hkv]) : -1.f;
       from_of[at + i] = from == tok || page < 0 ? nullptr : data + page * st.b + (from & page_mask) * st.n;
       scale_of[at + i] = scale;
       atomicMax(top + page0 + (i >> p.page_log2), __float_as_int(scale));
@@ -159,7 +162,7 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
     const unsigned char* src = from_of[(r & 1) * p.rows + (x >> p.slots_log2)];
     if (src != nullptr) copy_async_16(smem_u32(codes + x), src + 16 * (x & (slots - 1)));
   };
-  for (int i = tid; i < 2 * pages; i += threads) top[i] = 0;
+  for (int i = tid; i < 2 * pages; i += threads) top[i] = -1;
   __syncthreads();
   records(0);
   __syncthreads();
@@ -192,7 +195,7 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
         const float was = scale_of[at + i], now = __int_as_float(top[page0 + (i >> p.page_log2)]);
         const bool moved = from_of[at + i] != nullptr;
         // (a row that is there already changes where its page's scale grows)
-        if (was != 0.f && page >= 0 && (moved || was != now)) {
+        if (!(was < 0.f) && page >= 0 && (moved || was != now)) {
           uint4* to = reinterpret_cast<uint4*>(data + page * st.b + ((first + i) & page_mask) * st.n +
                                                16 * (x & (slots - 1)));
           uint4 v = moved ? codes[x] : *to;
@@ -205,9 +208,9 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const __grid_constan
     __syncthreads();
     for (int i = tid; i < pages; i += threads) {      // (the records' places are free for run r + 2)
       const int bits = top[page0 + i];
-      if (bits != 0 && page_of[page0 + i] >= 0)
+      if (bits >= 0 && page_of[page0 + i] >= 0)
         scales[static_cast<long long>(page_of[page0 + i]) * ca.Hkv] = __int_as_float(bits);
-      top[page0 + i] = 0;
+      top[page0 + i] = -1;
     }
     __syncthreads();
   }

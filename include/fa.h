@@ -501,7 +501,8 @@ size_t fa_qk_norm_rope_bwd_workspace_size(int B, int H, int Hkv, int N, int d);
  * that its tokens come with (its own among them when a token of the sequence
  * that was in it is still there).  Codes that come with a smaller scale are
  * rounded again for it (exact but for e4m3 subnormals where scales are powers
- * of two).  Rows of a page behind the sequence's last token are left as they
+ * of two).  A scale of 0 is one like any (its tokens are zeros, and stay so);
+ * scales must not be negative.  Rows of a page behind the sequence's last token are left as they
  * are.  Pages that hold the tokens in question must not be shared between
  * sequences.
  *

@@ -41,3 +41,49 @@ def test_more_kept_tokens_than_the_window_has(d, page, N, K, given):
     for c in want:
         branch.keep(c, table[1], lens[1] - N, keep)
     same(cache, want)
+
+
+def keep_with_zeros(held, table_row, base, kept):
+    """branch.keep where scales may be 0: a page whose tokens all come with 0 takes them as they are."""
+    page = held.values.shape[2]
+    old, scales = held.values.clone(), held.scales.clone()
+    end = base + len(kept)
+    for number in range(base // page, -(-end // page)):
+        toks = range(number * page, min(end, (number + 1) * page))
+        at = [divmod(t if t < base else base + kept[t - base], page) for t in toks]
+        p = int(table_row[number])
+        for h in range(scales.shape[1]):
+            came = [(old[int(table_row[i]), h, r], float(scales[int(table_row[i]), h])) for i, r in at]
+            top = max(s for _, s in came)
+            for r, (x, s) in enumerate(came):
+                held.values[p, h, r] = x if top == 0 else ref.to_e4m3(x * (s / top))
+            held.scales[p, h] = top
+
+
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64), (256, 32)])
+@pytest.mark.parametrize("zeros", [[0], [1], [2, 3], [1, 2, 3], [0, 1, 2, 3], [3]])
+def test_pages_of_scale_zero(d, page, zeros):
+    """Tokens from pages of scale 0 (with codes of every kind under it) to places that held
+    others, among tokens with a scale and alone; places whose own page has none."""
+    g = torch.Generator().manual_seed(d + page)
+    L = 4 * page - 3
+    for base, keep in ((page // 2, range(0, L - page // 2, 2)), (3, range(2 * page, 3 * page)), (0, range(page, 2 * page)),
+                       (page, list(range(5)) + list(range(page, page + 9)))):
+        keep = list(keep)
+        codes, scales, table = ref.make_cache(6, 2, page, d, 1, 4, g)
+        for x in codes:
+            x.view(torch.uint8)[:, :, ::5, ::7] = 0x7F          # (0 * NaN is NaN)
+            x.view(torch.uint8)[:, :, ::3, ::9] = 0x80
+        for i in (0, 1):
+            for n in zeros:
+                scales[i][int(table[0, n]), i:] = 0.0 if n % 2 else -0.0
+        cache = binding.Cache(*(t.to(DEV) for t in (*codes, *scales, table)))
+        out = binding.cache_keep(cache, ints([L]), L - base, ints([keep]))
+        binding.device_status()
+        assert out.tolist() == [base + len(keep)]
+        want = [ref.Paged(codes[i], scales[i].abs()) for i in (0, 1)]
+        for c in want:
+            keep_with_zeros(c, table[0], base, keep)
+        # (a page without tokens of the sequence keeps the sign of its 0)
+        cache.tensors[2].abs_(), cache.tensors[3].abs_()
+        same(cache, want)

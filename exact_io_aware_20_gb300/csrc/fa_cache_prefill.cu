@@ -1146,10 +1146,9 @@ cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
           reg_fence(o2);
           #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            // (an O that counts for nothing may be anything)
-            const float x = of0 == 0.f ? 0.f : __uint_as_float(o[k]) * of0;
-            const float y = of1 == 0.f ? 0.f : __uint_as_float(o2[k]) * of1;
-            o[k] = __float_as_uint(x + y);
+            // (also where a group counts 0: its O, begun by a product in every piece, is
+            // finite, or NaN by a value that every row of the tile sees)
+            o[k] = __float_as_uint(fmaf(__uint_as_float(o2[k]), of1, __uint_as_float(o[k]) * of0));
           }
         } else if (some) {
           tmem_ld32(tO + 32 * c, o);

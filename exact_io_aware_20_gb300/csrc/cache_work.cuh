@@ -77,6 +77,9 @@ constexpr float kNoMax = -1e30f;    // running maximum before the first key
 // steps end at 2^-24) go to the others.  With m at the maximum itself keys of
 // less than 2^-25 of it were lost from the products, which over 2^17 keys came
 // to 2^-8 of a result.
+// Sums and O of parts (warps, softmax groups, pieces; a row's own when m moves) are
+// taken times 2^(m - the joined m), which fp32 ends at 2^-126: a part whose maximum
+// is 2^-118 of the whole one's or more is never lost, as m may stand 8 higher in it.
 constexpr float kHead = 7.f, kGrow = 8.f;   // (log2 units)
 // 2^-kHead: row sums are kept without it, their terms' factor 2^-kHead / vs as a
 // product (2^-7 over the largest scale, 2^120, is no normal number, and the

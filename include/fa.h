@@ -393,9 +393,11 @@ int fa_cache_append(const fa_cache *cache, const void *q, const void *k, const v
  * down to 2^-21 of a row's largest, and to 2^-32 of that below.
  * Weights carry the value scale in fp32: with j the key of the largest weight
  * times value scale that a row sees, a key whose page's value scale is 2^-g of
- * j's is left out of the sum when its weight is below 2^(g - 133) of j's.  A
- * sequence's value scales should lie within 2^100 of one another (a page of
- * zeros has 2^-100).
+ * j's counts in the sum when its weight is at least 2^(g - 118) of j's, and may
+ * be left out below that (keys are joined by maxima that stand 2^7 to 2^15 below
+ * their parts' own, in fp32).  A sequence's value scales should lie within 2^80
+ * of one another, so that what is left out weighs below 2^-38; against values of
+ * scale 2^-8 a page of zeros, 2^-100, may lose weights below 2^-26.
  * strides[2]: of q, o; NULL: contiguous.  workspace: device memory of at
  * least fa_fwd_cache_workspace_size(...) bytes for the current device,
  * 256-byte aligned; its contents on entry do not matter (calls whose work may

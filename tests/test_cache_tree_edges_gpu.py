@@ -1,5 +1,7 @@
 """fa_fwd_cache_tree where parts of a row's keys are joined: parts that weigh nothing
-beside the others but hold a NaN."""
+beside the others but hold a NaN, parts whose value scales lie far apart."""
+import math
+
 import pytest
 import torch
 
@@ -52,3 +54,38 @@ def test_nan_values_in_halves_that_weigh_nothing(dtype, d, N, low):
     err[..., col] = 0
     assert (err <= ref.half_step(dtype) * want.abs() * 1.001 + 2.0 ** -25 + o_slack).all()
     assert ((lse.cpu().double() - l_want).abs() <= l_slack + 2.0 ** -23 * l_want.abs()).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("N", ROWS)
+@pytest.mark.parametrize("L", [700, 9000])
+@pytest.mark.parametrize("down", [1.0, 8.0, 16.5])
+def test_value_scales_far_apart_between_parts(d, N, L, down):
+    """One page of 64 keys has value scale 1, all others 2^-100 and weights 2^-down of its keys':
+    2^-116.5 at most, which the joins have to keep (down to 2^-118).  The others are many, so that
+    together they count in the sum."""
+    page = 64
+    width = -(-(L + N) // page)
+    lens = [L + N]
+    g = torch.Generator().manual_seed(d + N)
+    codes, scales, table = ref.make_cache(width, 1, page, d, 1, width, g, lens)
+    high = int(table[0, width // 2])
+    codes[0][:] = torch.zeros(1).to(torch.float8_e4m3fn)
+    codes[0][high] = torch.ones(1, page, d).to(torch.float8_e4m3fn)
+    # one of the page's keys stands above the others alone
+    codes[0][high, 0, 1:] = torch.zeros(page - 1, d).to(torch.float8_e4m3fn)
+    ks, vs = torch.ones(width, 1), torch.full((width, 1), 2.0 ** -100)
+    vs[high] = 1.0
+    codes[1][high] = torch.full((1, page, d), 256.0).to(torch.float8_e4m3fn)
+    sees = torch.ones(N, N, dtype=torch.bool).tril()
+    q = torch.ones(1, 1, N, d, dtype=torch.float16)
+    scale = down * math.log(2.0) / d
+    o, lse = binding.forward_cache_tree(q.to(DEV), cache_of(codes, (ks, vs), table), ints(lens),
+                                        branch.pack(sees, N)[None].to(DEV), scale)
+    binding.device_status()
+    K, V = ref.Paged(codes[0], ks), ref.Paged(codes[1], vs)
+    want, l_want, o_slack, l_slack = branch.attend_tree(q, K, V, table, lens, [sees], scale)
+    assert ((lse.cpu().double() - l_want).abs() <= l_slack + 2.0 ** -23 * l_want.abs()).all()
+    # weights: half a step of f16, and the scores' and the sums' error on either side
+    err = (o.cpu().double() - want).abs()
+    assert (err <= want.abs() * (2.0 ** -11 * 1.001 + 2.0 ** -11 + 2 * l_slack[..., None])).all()

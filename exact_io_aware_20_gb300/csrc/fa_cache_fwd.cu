@@ -105,7 +105,7 @@ struct Smem {
   static constexpr int kStatBytes = kWarps * 8 * NT * 8;
   static constexpr int kQsOff = kStatOff + kStatBytes;     // [row] power of two taken off q
   static constexpr int kTreeOff = kQsOff + 8 * NT * 4;     // [row] what it sees of the drafted tokens, a bit each
-  static constexpr int kMetaOff = kTreeOff + (kTree ? 8 * NT * 8 : 0);     // (ks, log2 vs, 2^-7 / vs) [warp][stage][page]
+  static constexpr int kMetaOff = kTreeOff + (kTree ? 8 * NT * 4 : 0);     // (ks, log2 vs, 2^-7 / vs) [warp][stage][page]
   static constexpr int kMetaBytes = kWarps * kStages * T::kSub * 16;
   static constexpr int kBarOff = kMetaOff + kMetaBytes;
   static constexpr int kMiscOff = kBarOff + kWarps * kStages * 8;
@@ -135,7 +135,7 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
   uint2* q_frag = reinterpret_cast<uint2*>(smem + S::kQOff);
   float2* stat = reinterpret_cast<float2*>(smem + S::kStatOff);
   float* q_pow = reinterpret_cast<float*>(smem + S::kQsOff);
-  unsigned long long* tree = reinterpret_cast<unsigned long long*>(smem + S::kTreeOff);
+  uint32_t* tree = reinterpret_cast<uint32_t*>(smem + S::kTreeOff);
   const uint32_t meta = base + S::kMetaOff + warp * kStages * T::kSub * 16;
   const uint32_t ring = base + warp * kStages * 2 * T::kBytes;
   const uint32_t bars = base + S::kBarOff + warp * kStages * 8;
@@ -286,15 +286,9 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         }
       }
       if constexpr (kTree) {
-        // (this kernel's rows are those of 64 tokens at most: two words of each)
-        if (t == 0) {
-          unsigned long long bits = 0;
-          if (r < p.rows && r / p.seq.G < at.seq.n) {
-            const uint32_t* row = tree_row(p, b, r / p.seq.G);
-            bits = row[0] | (p.tree_words > 1 ? static_cast<unsigned long long>(row[1]) << 32 : 0ull);
-          }
-          tree[nt * 8 + g] = bits;
-        }
+        // (this kernel's rows are those of 32 tokens at most: a word of each)
+        if (t == 0)
+          tree[nt * 8 + g] = r < p.rows && r / p.seq.G < at.seq.n ? *tree_row(p, b, r / p.seq.G) : 0u;
       }
       float down = 1.f;
       if (p.bf16) {
@@ -677,7 +671,7 @@ cache_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 }
 
 // The rows that a unit of this kernel holds at most.
-int most_rows(int d) { return d == 64 ? 32 : d == 128 ? 16 : 8; }
+constexpr int most_rows(int d) { return d == 64 ? 32 : d == 128 ? 16 : 8; }
 
 // Rows of a unit's tile: the fewest 8-row fragments that hold all G * Nq rows.
 int row_fragments(int rows, int d) {
@@ -740,7 +734,10 @@ namespace {
 // 128 at 8 rows 13.4 / 13.7, 28 15.5 / 14.1).  16 rows at d = 128 go either way, by
 // how many units there are: one sequence of 16000 34 / 23, 64 ragged ones up to
 // 4000 81 / 92, of 1000 53 / 70; they stay here, where large batches are.
-bool many_rows(long long rows, int d) { return rows > (kTree || d == 256 ? 1 : 2) * most_rows(d); }
+constexpr int few_rows(int d) { return (kTree || d == 256 ? 1 : 2) * most_rows(d); }
+static_assert(!kTree || (few_rows(64) <= 32 && few_rows(128) <= 32 && few_rows(256) <= 32),
+              "this file's kernel has one word of a tree's mask for each row");
+bool many_rows(long long rows, int d) { return rows > few_rows(d); }
 
 // Rows of a unit, and CTAs at most.
 void unit_shape(long long rows, int d, int sms, size_t* unit_rows, size_t* ctas) {

@@ -231,7 +231,8 @@ __global__ void __launch_bounds__(kFwdThreads, 6) norm_kernel(const __grid_const
   };
   #pragma unroll
   for (int u = 0; u < kAhead; ++u) load(u, u);
-  // y1 = r (x1 w1 c - x2 w2 s), y2 = r (x2 w2 c + x1 w1 s)
+  // with h = r x: y1 = h1 w1 c - h2 w2 s, y2 = h2 w2 c + h1 w1 s (in this order, so that
+  // no product leaves fp32 whose result does not)
   Vals w = load_weights<BF16, PAIRS>(p, p.weight[which], at), ws;
   if (at.turn_a) {       // (where chunk b turns, a does)
     f2 c[4], s[4];
@@ -251,6 +252,7 @@ __global__ void __launch_bounds__(kFwdThreads, 6) norm_kernel(const __grid_const
       load(u, h + u + kAhead);
       float down;
       const float r = row_norm<SLOTS>(p.eps, x, &down);
+      scale_vals(x, r);
       #pragma unroll
       for (int k = 0; k < 4; ++k) {
         f2 y = fmul2(x.a[k], w.a[k]), z = fmul2(x.b[k], w.b[k]);
@@ -261,7 +263,6 @@ __global__ void __launch_bounds__(kFwdThreads, 6) norm_kernel(const __grid_const
         x.a[k] = y;
         x.b[k] = z;
       }
-      scale_vals(x, r);
       if (on && h + u < heads) {
         uint4 a, v;
         pack_vals<BF16, PAIRS>(x, a, v);

@@ -62,3 +62,18 @@ def test_gradients_of_rows_far_from_one(dtype, power, dy_power, d, interleaved):
     want_dw = branch.norm_backward(dy, x, w, eps, 0.0, still)[1]
     size = (dy.double() * branch.norm(x, None, eps, 0.0, still)).abs().sum((0, 1, 2))
     assert ((dw.cpu().double() - want_dw).abs() <= 2.0 ** -17 * size).all()
+
+
+@pytest.mark.parametrize("power,w_power,eps", [
+    (60, 70, 1e-6), (30, 110, 1e-6), (100, 120, 1e-6), (-60, -80, 2.0 ** -99), (-20, -110, 1e-6), (66, -100, 1e-6)])
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_weights_far_from_one(power, w_power, eps, d, interleaved):
+    """y = (x r) w: where x w leaves fp32, but the result does not."""
+    g = torch.Generator().manual_seed(d + power)
+    x = (torch.randn(1, 3, 9, d, generator=g) * 2.0 ** power).bfloat16()
+    w = torch.rand(d, generator=g).add(0.5) * 2.0 ** w_power
+    for table in (None, binding.Rope([0.0] * (d // 2), None, interleaved)):
+        y, _ = binding.qk_norm_rope(x.to(DEV), None, w.to(DEV), None, eps, None, table)
+        binding.device_status()
+        assert forward_is(y, x, w, eps)

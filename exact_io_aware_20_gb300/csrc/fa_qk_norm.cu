@@ -180,25 +180,27 @@ __device__ __forceinline__ float row_squares(const Vals& x) {
   return row_sum<SLOTS>(s);
 }
 
-// bf16 rows whose squares leave fp32 are taken times this (eps is nothing to
-// them).
+// Rows whose squares, or whose mean and eps together, leave fp32 are taken times
+// this, and eps times its square.
 constexpr float kDown = 8.470329472543003e-22f;   // 2^-70
 
-// r of a row; where its squares leave fp32, the row and r are of x 2^-70 (*down
-// is that factor, 1 otherwise).
+// r of a row; where its mean square and eps leave fp32, the row and r are of x 2^-70
+// (*down is that factor, 1 otherwise).
 template <int SLOTS>
 __device__ __forceinline__ float row_norm(float eps, Vals& x, float* down) {
   constexpr float kInf = 3.402823466e38f;
-  float ss = row_squares<SLOTS>(x);
+  float mean = fmaf(row_squares<SLOTS>(x), 1.f / (16 * SLOTS), eps);
   *down = 1.f;
-  if (__any_sync(0xffffffffu, !(ss <= kInf))) {   // (whole rows: no lane of one alone)
-    if (!(ss <= kInf)) {
+  if (__any_sync(0xffffffffu, !(mean <= kInf))) {   // (whole rows: no lane of one alone)
+    if (!(mean <= kInf)) {
       *down = kDown;
       scale_vals(x, kDown);
+      eps *= kDown;
+      eps *= kDown;
     }
-    ss = row_squares<SLOTS>(x);
+    mean = fmaf(row_squares<SLOTS>(x), 1.f / (16 * SLOTS), eps);
   }
-  return rsqrtf(fmaf(ss, 1.f / (16 * SLOTS), *down == 1.f ? eps : 0.f));
+  return rsqrtf(mean);
 }
 
 // A thread has one slot of one token, and up to heads_per heads of q or of k, two

@@ -77,3 +77,18 @@ def test_weights_far_from_one(power, w_power, eps, d, interleaved):
         y, _ = binding.qk_norm_rope(x.to(DEV), None, w.to(DEV), None, eps, None, table)
         binding.device_status()
         assert forward_is(y, x, w, eps)
+
+
+@pytest.mark.parametrize("power,eps", [(63.5, 2.0 ** 127), (62.0, 2.0 ** 127), (64.0, 2.0 ** 126), (60.0, 1.999 * 2.0 ** 127),
+                                       (0.0, 2.0 ** 127), (66.0, 2.0 ** 120)])
+@pytest.mark.parametrize("d", [64, 256])
+def test_eps_of_any_size(power, eps, d):
+    """Also beside rows whose squares leave fp32, and where the mean and eps together do."""
+    g = torch.Generator().manual_seed(d)
+    x = (torch.randn(1, 3, 9, d, generator=g).clamp(-1.9, 1.9) * 2.0 ** power).bfloat16()
+    dy = (torch.randn(1, 3, 9, d, generator=g) * 2.0 ** 60).bfloat16()
+    y, _ = binding.qk_norm_rope(x.to(DEV), None, None, None, eps)
+    dx, *_rest = binding.qk_norm_rope_backward(dy.to(DEV), None, x.to(DEV), None, None, None, eps)
+    binding.device_status()
+    assert forward_is(y, x, None, eps)
+    assert backward_is(dx, dy, x, None, eps)

@@ -1,5 +1,5 @@
 """fa_cache_keep at the ends of what its interface allows: more tokens to keep than
-a window has, at a table's last page."""
+a window has, at a table's last page; scales of 0; a stream of the caller's."""
 import pytest
 import torch
 
@@ -87,3 +87,26 @@ def test_pages_of_scale_zero(d, page, zeros):
         # (a page without tokens of the sequence keeps the sign of its 0)
         cache.tensors[2].abs_(), cache.tensors[3].abs_()
         same(cache, want)
+
+
+def test_on_a_stream_of_its_own():
+    g = torch.Generator().manual_seed(12)
+    lens, N = [3000, 2900], 2800
+    codes, scales, table = ref.make_cache(400, 2, 16, 128, 2, 190, g, lens)
+    keeps = [sorted(torch.randperm(N, generator=g)[:1500].tolist()) for _ in lens]
+    want = [ref.Paged(codes[i], scales[i]) for i in (0, 1)]
+    for b, k in enumerate(keeps):
+        for c in want:
+            branch.keep(c, table[b], lens[b] - N, k)
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        cache = binding.Cache(*(t.to(DEV) for t in (*codes, *scales, table)))
+        n, keep = ints(lens), ints(keeps)
+        torch.cuda.synchronize()
+        out = binding.cache_keep(cache, n, N, keep, stream=side)
+        del n, keep
+        torch.full((2, 1500), -7, dtype=torch.int32, device=DEV)      # (the current stream's allocations)
+        side.synchronize()
+        assert out.tolist() == [1700, 1600]
+        same(cache, want)
+    binding.device_status()

@@ -72,7 +72,9 @@ struct Pre {
   // 240 / 243, ragged chunks of 1500 82 / 82 / 77 / 78 / 80 / 80.  d = 128, 4 / 5 /
   // 6 / 8 / 10 / 12: 4 x 2048 121 / 124 / 117 / 117 / 115 / 119, 8 x 1000 158 / 156 /
   // 154 / 154 / 162 / 155, 8192 265 / 246 / 240 / 244 / 244 / 248; d = 64,
-  // 4 x 2048: 90 / 97 / 89 / 96 / 90 / 98.  (How shares fall on a shape moves a
+  // 4 x 2048: 90 / 97 / 89 / 96 / 90 / 98.  One tile of rows shared out (Split), d =
+  // 128, 2 / 4 / 6 / 9 / 13: 100 rows of 8 x 8192 50.9 / 50.0 / 48.9 / 49.3 / 51.1, 32
+  // rows of 64 ragged ones up to 4000 102 / 93 / 92 / 93 / 94.  (How shares fall on a shape moves a
   // time by up to 8% either way; 5 and 6 are within 2% of the best on each.)
   static constexpr int kOver = kTiles == 1 ? 5 : 6;
   static constexpr int kSoftWarps = 4 * kTiles;
@@ -137,12 +139,6 @@ struct Split {
   static constexpr int kThere = kStatOff + 2 * 128 * 8, kRead = kThere + 8;
   static_assert(L::kTiles == 1 || kRead + 8 <= L::kKOff, "the second tile's place");
 };
-
-// A unit's cost besides its steps, in steps (SPLIT, d = 128, 2 / 4 / 6 / 9 / 13: 100
-// rows of 8 x 8192 tokens 50.9 / 50.0 / 48.9 / 49.3 / 51.1 us, 32 rows of 64 ragged
-// ones up to 4000 102 / 93 / 92 / 93 / 94).
-template <int D, bool SPLIT>
-constexpr int unit_over() { return SPLIT ? 6 : Pre<D>::kOver; }
 
 template <int N>
 __device__ __forceinline__ void more_registers() {
@@ -342,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 cache_prefill_kernel(const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ FwdCacheParams p) {
   using L = Pre<D>;
-  constexpr int kOver = unit_over<D, SPLIT>();
+  constexpr int kOver = L::kOver;
   using W = Walk<L::kRows, 128, kOver>;
   static_assert(!SPLIT || L::kTiles == 2, "two softmax groups");
   // rows of q that are converted (SPLIT: those that there are; what the others'
@@ -1260,7 +1256,7 @@ cudaError_t launch_seg(const Cache& cache, FwdCacheParams& p, int sms, cudaStrea
   kern<<<p.ctas, kThreads, Pre<D>::kAlloc, stream>>>(tk, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   constexpr bool kOneTile = SPLIT || Pre<D>::kTiles == 1;
-  return launch_cache_merge<D, Pre<D>::kRows, 128, unit_over<D, SPLIT>(), true>(
+  return launch_cache_merge<D, Pre<D>::kRows, 128, Pre<D>::kOver, true>(
       p, stream, kTree && kOneTile ? std::min(p.rows, 128) : 0);
 }
 

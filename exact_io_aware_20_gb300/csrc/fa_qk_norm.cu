@@ -8,8 +8,8 @@
 // each: its sums are shuffles among them, and every element is read once.
 //
 // What bounds it: memory (2 x 8192 tokens of 32 + 8 heads, d = 128, bf16:
-// forward, 2 bytes read and 2 written an element, 57 us, 5.9 TB/s, 87% of what a
-// copy reaches; backward, 4 read and 2 written, 85 us, as much), with the
+// forward, 2 bytes read and 2 written an element, 57.3 us, 5.9 TB/s, 86% of what a
+// copy reaches; backward, 4 read and 2 written, 86 us, as much), with the
 // arithmetic close behind: two lanes of fp32 an instruction (without 62 and 107
 // us).  Short calls: five tokens of four sequences forward 3.4 us, backward 6; 4099
 // tokens of 32 heads, d = 64, three axes, backward 16.4 us, of which the start, the
@@ -295,7 +295,7 @@ __device__ __forceinline__ void copy_async_wait() {
 // norm_sum_kernel adds up in a fixed order.  A thread's next kRing - 1 units are
 // on their way to shared memory of its own (no barrier between them; the long
 // call above with kRing 2 / 3 / 4 / 6 94 / 85.5 / 92 / 95.5 us, through registers
-// one unit ahead 104; three blocks an SM spill, 141).
+// one unit ahead 104; three blocks an SM spill, 141, two 4 bytes a thread at most).
 constexpr int kRing = 3;
 template <bool BF16, int SLOTS, bool PAIRS>
 __global__ void __launch_bounds__(kNormThreads, 2) norm_bwd_kernel(const __grid_constant__ NormParams p) {

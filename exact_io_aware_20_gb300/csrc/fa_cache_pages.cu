@@ -462,7 +462,7 @@ int log2_of(int x) {
   return l;
 }
 
-int fork_chunks(int pages) { return (pages + 32 * kChunkWords - 1) / (32 * kChunkWords); }
+int fork_chunks(int pages) { return (pages - 1) / (32 * kChunkWords) + 1; }      // (pages may be INT_MAX)
 
 size_t padded(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
